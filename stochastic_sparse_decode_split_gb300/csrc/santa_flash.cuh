@@ -348,8 +348,8 @@ flash_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
   // ---- the shared pieces: every CTA arrives; the CTA holding a piece's last
   //      block (the piece is its range's first, started before it) merges
   //      the covering CTAs' partials into out
+  __syncthreads();   // s_gen is one thread's: a CTA without blocks has met no barrier since it was read
   unsigned* const arrivals = bar_count + (s_gen & 1u) * 32;
-  __syncthreads();
   if (tid == 0) red_release_add(arrivals, 1u);
   const bool owner = has_range && cA.pb_lo < lo && cA.pb_lo + cA.nblk <= hi;
   SANTA_STAMP(7);
@@ -371,7 +371,9 @@ flash_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
     auto stage_o = [&](int j0, int nc) {
       for (int i = tid; i < nc * (FL_MAXG * D / 4); i += NT) {
         const int jj = i / (FL_MAXG * D / 4), q = i - jj * (FL_MAXG * D / 4);
-        cp_async16(smem_addr(s_o + jj * PW + 4 * q), part_of(i_first + j0 + jj) + 4 * q);
+        // a CTA without blocks (fewer blocks than CTAs) between two covering ones left no partial
+        if (pt.nonempty(i_first + j0 + jj)) cp_async16(smem_addr(s_o + jj * PW + 4 * q), part_of(i_first + j0 + jj) + 4 * q);
+        else *reinterpret_cast<float4*>(s_o + jj * PW + 4 * q) = make_float4(0.f, 0.f, 0.f, 0.f);
       }
       cp_async_commit();
     };
@@ -379,8 +381,9 @@ flash_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
     for (int i = tid; i < ncov * G; i += NT) {
       const int jj = i / G, g = i - jj * G;
       const float* gp = part_of(i_first + jj) + FL_MAXG * D + 2 * g;
-      s_ml[2 * i] = __ldcg(gp);
-      s_ml[2 * i + 1] = __ldcg(gp + 1);
+      const bool some = pt.nonempty(i_first + jj);
+      s_ml[2 * i] = some ? __ldcg(gp) : -INFINITY;
+      s_ml[2 * i + 1] = some ? __ldcg(gp + 1) : 0.f;
     }
     __syncthreads();
     if (warp < G) {
