@@ -53,7 +53,8 @@ typedef enum {
   SANTA_SYSTEMATIC = 2  /* S2ANTA-sys: one offset shared by all strata (Sec. 2.1) */
 } santa_variant_t;
 
-typedef enum { SANTA_BF16 = 0, SANTA_FP16 = 1, SANTA_FP32 = 2 } santa_dtype_t;
+/* SANTA_E4M3 is a cache type only (see santa_paged_t). */
+typedef enum { SANTA_BF16 = 0, SANTA_FP16 = 1, SANTA_FP32 = 2, SANTA_E4M3 = 3 } santa_dtype_t;
 
 typedef enum {
   SANTA_OK = 0,
@@ -244,6 +245,120 @@ int32_t santa_workspace_layout(const santa_params_t* p, santa_ws_layout_t* layou
  * Returns SANTA_OK, SANTA_ERR_DEVICE (device flagged bad metadata; *code gets
  * the SANTA_DEVERR_* bits when code != NULL) or SANTA_ERR_CUDA. */
 santa_status_t santa_get_error(void* workspace, santa_stream_t stream, int32_t* code);
+
+/* ---------------------------------------------------------------------------
+ * The paged cache: new tokens written into it, exact attention over it, and
+ * its rows back in the packed layout that santa_decode reads.
+ *
+ * A cache is a pool of n_pages pages of page_size rows,
+ *   K, V              [n_pages, page_size, n_kv_heads, head_dim]  cache_dtype
+ *   k_scale, v_scale  [n_pages, n_kv_heads, page_size]            float32, SANTA_E4M3 only
+ * and key n of sequence b is row n % page_size of page
+ * page_table[b, n / page_size].  A pool whose table counts upwards is the
+ * packed layout of santa_decode.  An e4m3 row of one KV head holds
+ * code * scale: with amax = max(2^-60, max |x|), code = e4m3(x * (448 / amax))
+ * and scale = amax / 448, all in float32; a row with a NaN or an infinity
+ * comes back as NaN throughout.
+ *
+ * A batch is `batch` sequences.  Sequence b holds kv_lens[b] keys, of which
+ * the last n_b are this call's new tokens (rows q_offsets[b] .. q_offsets[b+1]
+ * of the token arrays; with q_offsets NULL every sequence has max_q of them).
+ * Token i of them stands at position kv_lens[b] - n_b + i.  Token rows past
+ * q_offsets[batch] are padding and are left as they were.
+ *
+ * Table entries past the last key's page are not read and may hold anything;
+ * so may the rows of the last page past the last key.
+ *
+ * Device-side checks set bits in the workspace's error word (santa_get_error):
+ *   SANTA_DEVERR_NK_BOUND        kv_lens[b] outside [0, nk]: nothing of b is written, its
+ *                                attention rows come out zero
+ *   SANTA_CACHE_DEVERR_CHUNK     q_offsets[b..b+1] decreasing, outside [0, total_q] or more
+ *                                than max_q apart (b is skipped, its rows left as they were);
+ *                                santa_kv_append: more new tokens than keys;
+ *                                santa_kv_read: kv_offsets[b..b+1] outside [0, rows] or
+ *                                fewer rows than keys
+ *   SANTA_CACHE_DEVERR_PAGE      a table entry outside [0, n_pages) was met: tokens are not
+ *                                written there, rows read from it come back zero, and the
+ *                                attention rows that are computed with it come out zero
+ *   SANTA_CACHE_DEVERR_POSITION  a position past the rotation table: the token is skipped
+ * The three calls share one workspace, cleared once by santa_workspace_init. */
+typedef struct {
+  int32_t batch;              /* 1 .. 65535 */
+  int32_t n_q_heads;          /* n_q_heads % n_kv_heads == 0, group <= SANTA_MAX_GROUP */
+  int32_t n_kv_heads;
+  int32_t head_dim;           /* 64 or 128 */
+  int32_t dtype;              /* santa_dtype_t of q, k, v, q_out, out, K_out, V_out (not SANTA_E4M3) */
+  int32_t cache_dtype;        /* dtype, or SANTA_E4M3 */
+  int32_t page_size;          /* 16, 32, 64, 128 or 256 */
+  int32_t n_pages;            /* pages of the pool; n_pages * page_size < 2^31 */
+  const int32_t* page_table;  /* device [batch, max_pages] */
+  int32_t max_pages;          /* max_pages * page_size >= nk */
+  const int32_t* kv_lens;     /* device [batch], the new tokens among them; NULL = nk each */
+  int64_t nk;                 /* upper bound on every kv_lens[b], 1 .. SANTA_MAX_NK */
+  const int64_t* q_offsets;   /* device [batch + 1], non-decreasing; NULL = b * max_q */
+  int32_t max_q;              /* new tokens per sequence; with q_offsets an upper bound */
+  int64_t total_q;            /* rows of the token arrays, < 2^31; batch * max_q without q_offsets */
+  int32_t causal;             /* 1: a token sees the keys up to its own position; 0: all of them */
+  int32_t window;             /* > 0 (causal only): of those, the last `window`; 0: no window */
+  float scale;                /* score scale; <= 0 selects 1/sqrt(head_dim) */
+} santa_paged_t;
+
+#define SANTA_CACHE_DEVERR_PAGE 16
+#define SANTA_CACHE_DEVERR_CHUNK 32
+#define SANTA_CACHE_DEVERR_POSITION 64
+
+/* Byte size of the workspace of the three calls (0 when p is invalid).  The
+ * pointers of p are not looked at. */
+size_t santa_paged_workspace_size(const santa_paged_t* p);
+
+/* What santa_kv_append does to the new tokens on their way. */
+typedef struct {
+  const void* q;              /* [total_q, n_q_heads, head_dim], token rows q_stride elements apart; NULL = no queries */
+  const void* k;              /* [total_q, n_kv_heads, head_dim], k_stride elements apart */
+  const void* v;              /* [total_q, n_kv_heads, head_dim], v_stride elements apart */
+  int64_t q_stride, k_stride, v_stride;   /* multiples of 16 bytes, at least one token's row */
+  void* q_out;                /* [total_q, n_q_heads, head_dim] contiguous; may be q when q is contiguous */
+  const void* q_norm;         /* [head_dim] weights of the heads' RMS norm, or NULL */
+  const void* k_norm;         /* the same for the keys */
+  float eps;                  /* of both norms, >= 0 */
+  const float* rope;          /* [rope_positions, rotated / 2, 2]: cos and sin of every position's angles, or NULL */
+  int64_t rope_positions;
+  int32_t rotated;            /* leading elements of each head that are rotated: a multiple of 16, <= head_dim */
+  int32_t interleaved;        /* pairs (2i, 2i + 1) when 1, (i, i + rotated / 2) when 0 */
+} santa_append_t;
+
+/* The new tokens of a batch: queries and keys normalised per head
+ * (x / sqrt(mean x^2 + eps) * weight), rotated by their positions
+ * ((x, y) -> (x cos - y sin, y cos + x sin)) and rounded once, the queries to
+ * q_out and the keys, with the values as they are, to their rows of the cache.
+ * All device memory, 16-byte aligned.  Two tokens must not fall on one cache
+ * row (no page twice among the pages written). */
+santa_status_t santa_kv_append(const santa_paged_t* p, const santa_append_t* a, void* K, void* V, float* k_scale,
+                               float* v_scale, void* workspace, size_t ws_bytes, santa_stream_t stream);
+
+/* out = softmax(scale q K^T + mask) V over the pages, exact: the new tokens'
+ * queries q [total_q, n_q_heads, head_dim] against the keys of their
+ * sequences, which the cache already holds.  dtype SANTA_BF16 or SANTA_FP16.
+ *   out  [total_q, n_q_heads, head_dim] in dtype
+ *   lse  optional float32 [total_q, n_q_heads]: the natural logarithm of the
+ *        sum of exp(scale q k) over the visible keys
+ * A token that sees no key (an empty sequence; more new tokens than keys) gets
+ * zeros and -infinity.  Scores, the running maximum and sum, and the sum over
+ * the values are float32; probabilities enter the second product in 16 bits.
+ * What masked keys hold, NaN and infinities included, does not matter. */
+santa_status_t santa_paged_attention(const santa_paged_t* p, const void* q, const void* K, const void* V,
+                                     const float* k_scale, const float* v_scale, void* out, float* lse,
+                                     void* workspace, size_t ws_bytes, santa_stream_t stream);
+
+/* The cache's keys and values as packed rows, K_out and V_out
+ * [rows, n_kv_heads, head_dim] in dtype: key n of sequence b in row
+ * kv_offsets[b] + n (device int64 [batch + 1]; NULL = b * nk, rows >=
+ * batch * nk), e4m3 rows multiplied out and rounded once.  Rows past a
+ * sequence's last key are left as they were.  With kv_offsets the exclusive
+ * sums of kv_lens, K_out, V_out and kv_offsets are what santa_decode takes. */
+santa_status_t santa_kv_read(const santa_paged_t* p, const void* K, const void* V, const float* k_scale,
+                             const float* v_scale, const int64_t* kv_offsets, int64_t rows, void* K_out, void* V_out,
+                             void* workspace, size_t ws_bytes, santa_stream_t stream);
 
 /* santa_decode without a caller-supplied workspace, for callers that cannot
  * allocate device memory: for example a plug-in that its host framework hands

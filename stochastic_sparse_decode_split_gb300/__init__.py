@@ -23,7 +23,9 @@ from typing import Optional
 
 import torch
 
+from . import paged as _paged
 from .build import LIB as _LIB_PATH
+from .paged import CACHE_DEVERR_CHUNK, CACHE_DEVERR_PAGE, CACHE_DEVERR_POSITION, PagedCache, PagedStep, rope_table
 
 __all__ = [
     "SantaError", "Params", "library", "santa_decode", "santa_decode_host_kv", "santa_decode_with_uniforms",
@@ -31,6 +33,7 @@ __all__ = [
     "workspace_size", "dense_workspace_size", "workspace_layout", "get_error", "Decoder", "exported_symbols",
     "VARIANTS", "DTYPES", "santa_decode_static", "static_warmup", "static_scratch_bytes", "SAMPLERS", "santa_decode_tiled",
     "tiled_workspace_size", "tiled_max_draws", "santa_decode_bernoulli", "bernoulli_workspace_size",
+    "PagedCache", "PagedStep", "rope_table",
 ]
 
 VARIANTS = {"iid": 0, "stratified": 1, "systematic": 2}
@@ -118,6 +121,7 @@ def library():
             lib.santa_status_string.argtypes = [i32]
             lib.santa_status_string.restype = ctypes.c_char_p
             lib.santa_version.restype = i32
+            _paged.declare(lib)
             for fn in ("santa_workspace_init", "santa_decode", "santa_decode_host_kv", "santa_decode_profiled",
                        "santa_score_pass",
                        "santa_decode_with_uniforms", "santa_dense_decode", "santa_decode_static",

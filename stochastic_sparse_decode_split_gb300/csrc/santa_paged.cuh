@@ -1,0 +1,153 @@
+// santa_paged.cuh -- what the paged-cache kernels share: the batch's
+// description, the mask as ranges of keys, and the division of a tile's keys
+// into splits.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "santa_common.cuh"
+
+namespace santa {
+
+constexpr int ERR_PAGE = 16;       // a page-table entry outside the pool
+constexpr int ERR_CHUNK = 32;      // bad q_offsets / kv_offsets, or more new tokens than keys
+constexpr int ERR_POSITION = 64;   // a position past the rotation table
+
+constexpr int PG_BLK = 16;         // keys per block: no block crosses a page (the smallest page is one block)
+
+// Everything the paged kernels need, validated and carved out of the workspace.
+struct PagedArgs {
+  int dtype, e4m3, D;   // 0 bf16, 1 fp16, 2 fp32 tokens; e4m3 cache or the tokens' type
+  int B, H, Hkv, G;
+  int page_shift, n_pages, max_pages;
+  const int32_t* table;
+  const int32_t* kv_lens;
+  const int64_t* q_offsets;
+  int nk, max_q;
+  long long total_q;
+  int causal, window;
+  float sl2;            // score scale in base-2 units (scale * log2 e)
+  const void* q;
+  const void* K;
+  const void* V;
+  const float* ks;
+  const float* vs;
+  void* out;
+  float* lse;
+  int* err;
+  // attention: packed rows (token * G + head of the group) are cut into tiles
+  // of `rows` of them (`tokens` whole tokens when the tiles keep tokens
+  // together, else 0); tiles per sequence, most splits of a tile and key
+  // blocks per split
+  int rows, tokens, tiles, splits, split_blk;
+  float* part_o;        // [B, tiles, Hkv, splits, rows, D] unnormalised sums
+  float* part_ml;       // [B, tiles, Hkv, splits, rows, 2] maximum (base 2) and sum
+  int num_sms;
+  cudaStream_t stream;
+};
+
+// One sequence: its new tokens' first row and number, its keys.  `ok` false:
+// its lengths were refused (the error word says why; n = 0 where its token
+// rows are not to be trusted).
+struct Seq {
+  long long q0;
+  int n, kv;
+  bool ok;
+};
+
+__device__ __forceinline__ Seq paged_seq(const PagedArgs& a, int b, bool flag) {
+  Seq s;
+  int e = 0;
+  if (a.q_offsets) {
+    const long long lo = a.q_offsets[b], hi = a.q_offsets[b + 1];
+    const bool fine = lo >= 0 && hi >= lo && hi <= a.total_q && hi - lo <= a.max_q;
+    s.q0 = fine ? lo : 0;
+    s.n = fine ? (int)(hi - lo) : 0;
+    if (!fine) e |= ERR_CHUNK;
+  } else {
+    s.q0 = (long long)b * a.max_q;
+    s.n = a.max_q;
+  }
+  const int kv = a.kv_lens ? a.kv_lens[b] : a.nk;
+  const bool fine = kv >= 0 && kv <= a.nk;
+  s.kv = fine ? kv : 0;
+  if (!fine) e |= ERR_NK_BOUND;
+  s.ok = e == 0;
+  if (e && flag) flag_error(a.err, e);
+  return s;
+}
+
+// The sequence of token row t (false: padding, or offsets that do not hold it).
+__device__ __forceinline__ bool paged_seq_of(const PagedArgs& a, long long t, int& b) {
+  if (!a.q_offsets) {
+    b = (int)(t / a.max_q);
+    return b < a.B;
+  }
+  int lo = 0, hi = a.B;   // the last b with q_offsets[b] <= t
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (a.q_offsets[mid] <= t) lo = mid;
+    else hi = mid;
+  }
+  b = lo;
+  return a.q_offsets[b] <= t && t < a.q_offsets[b + 1];
+}
+
+// Keys [lo, hi) that the token at position `pos` sees.
+__device__ __forceinline__ void visible_keys(const PagedArgs& a, int kv, int pos, int& lo, int& hi) {
+  hi = a.causal ? min(max(pos + 1, 0), kv) : kv;
+  lo = a.window ? min(max(pos - a.window + 1, 0), hi) : 0;
+}
+
+// The key blocks of a tile whose first and last token are i0 and i1 (of n):
+// blk blocks of `keys` keys from block lo on, in how many splits.
+struct TileKeys {
+  int blk_lo, blk, splits;
+};
+__device__ __forceinline__ TileKeys tile_keys(const PagedArgs& a, const Seq& s, int i0, int i1, int keys) {
+  int lo0, hi0, lo1, hi1;
+  visible_keys(a, s.kv, s.kv - s.n + i0, lo0, hi0);
+  visible_keys(a, s.kv, s.kv - s.n + i1, lo1, hi1);
+  TileKeys t;
+  t.blk_lo = lo0 / keys;
+  t.blk = hi1 > lo0 ? (hi1 + keys - 1) / keys - t.blk_lo : 0;
+  t.splits = max(1, (t.blk + a.split_blk - 1) / a.split_blk);
+  return t;
+}
+
+// First and last token of tile `tile` (the rows of a tile need not start at a
+// token's first head unless the tiles keep tokens together).
+__device__ __forceinline__ void tile_tokens(const PagedArgs& a, int n, int tile, int& i0, int& i1) {
+  if (a.tokens) {
+    i0 = tile * a.tokens;
+    i1 = min(n, i0 + a.tokens) - 1;
+  } else {
+    i0 = tile * a.rows / a.G;
+    i1 = min(n - 1, (tile * a.rows + a.rows - 1) / a.G);
+  }
+}
+
+// Keys per block in the split arithmetic of the two attention kernels.
+constexpr int PG_CHUNK_KEYS = 128;
+
+cudaError_t launch_paged_tokens(const PagedArgs& a);   // few rows per KV head (mma.sync)
+cudaError_t launch_paged_merge(const PagedArgs& a, int keys);
+void plan_paged_tokens(PagedArgs& a);
+
+struct AppendArgs {
+  const void *q, *k, *v;
+  long long q_stride, k_stride, v_stride;
+  void* q_out;
+  const void *q_norm, *k_norm;
+  float eps;
+  const float* rope;
+  long long rope_positions;
+  int rotated, interleaved;
+  void *K, *V;
+  float *ks, *vs;
+};
+cudaError_t launch_kv_append(const PagedArgs& a, const AppendArgs& p);
+cudaError_t launch_kv_read(const PagedArgs& a, const int64_t* kv_offsets, long long rows, void* K_out, void* V_out);
+
+}  // namespace santa

@@ -1,0 +1,331 @@
+"""The paged cache: new tokens written into it, exact attention over it, and
+its rows back in the packed layout that ``santa_decode`` reads.
+
+Binding of ``santa_kv_append``, ``santa_paged_attention`` and ``santa_kv_read``
+(``include/santa.h`` states the layouts, the mask and the device-side checks).
+``PagedCache`` holds the pool, ``PagedStep`` a batch's description and the
+workspace, so that each operator of a step is one C-ABI call.
+"""
+from __future__ import annotations
+
+import ctypes
+import math
+from typing import Optional
+
+import torch
+
+CACHE_DEVERR_PAGE, CACHE_DEVERR_CHUNK, CACHE_DEVERR_POSITION = 16, 32, 64   # SANTA_CACHE_DEVERR_* in santa.h
+E4M3 = 3                                                                   # SANTA_E4M3
+PAGE_SIZES = (16, 32, 64, 128, 256)
+
+
+class PagedParams(ctypes.Structure):
+    """Mirror of santa_paged_t."""
+    _fields_ = [
+        ("batch", ctypes.c_int32),
+        ("n_q_heads", ctypes.c_int32),
+        ("n_kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("cache_dtype", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("n_pages", ctypes.c_int32),
+        ("page_table", ctypes.c_void_p),
+        ("max_pages", ctypes.c_int32),
+        ("kv_lens", ctypes.c_void_p),
+        ("nk", ctypes.c_int64),
+        ("q_offsets", ctypes.c_void_p),
+        ("max_q", ctypes.c_int32),
+        ("total_q", ctypes.c_int64),
+        ("causal", ctypes.c_int32),
+        ("window", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+    ]
+
+
+class AppendParams(ctypes.Structure):
+    """Mirror of santa_append_t."""
+    _fields_ = [
+        ("q", ctypes.c_void_p),
+        ("k", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("q_stride", ctypes.c_int64),
+        ("k_stride", ctypes.c_int64),
+        ("v_stride", ctypes.c_int64),
+        ("q_out", ctypes.c_void_p),
+        ("q_norm", ctypes.c_void_p),
+        ("k_norm", ctypes.c_void_p),
+        ("eps", ctypes.c_float),
+        ("rope", ctypes.c_void_p),
+        ("rope_positions", ctypes.c_int64),
+        ("rotated", ctypes.c_int32),
+        ("interleaved", ctypes.c_int32),
+    ]
+
+
+def declare(lib) -> None:
+    """Argument types of the paged entry points."""
+    vp, sz, i64 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int64
+    P, A = ctypes.POINTER(PagedParams), ctypes.POINTER(AppendParams)
+    lib.santa_paged_workspace_size.argtypes = [P]
+    lib.santa_paged_workspace_size.restype = sz
+    lib.santa_kv_append.argtypes = [P, A, vp, vp, vp, vp, vp, sz, vp]
+    lib.santa_paged_attention.argtypes = [P, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.santa_kv_read.argtypes = [P, vp, vp, vp, vp, vp, i64, vp, vp, vp, sz, vp]
+    for fn in ("santa_kv_append", "santa_paged_attention", "santa_kv_read"):
+        getattr(lib, fn).restype = ctypes.c_int32
+
+
+def rope_table(positions: int, rotated: int, base: float = 10000.0, *, linear: float = 1.0, ntk: float = 1.0,
+               by_parts: Optional[tuple] = None, attention_factor: float = 1.0, device="cuda") -> torch.Tensor:
+    """cos and sin of every position's angles, float32 [positions, rotated / 2, 2], for ``PagedStep.append``.
+
+    The angle of pair i at position p is p * base^(-2 i / rotated), computed in float64.  For contexts longer than the
+    model was trained on: ``linear`` divides every frequency; ``ntk`` raises the base to base * ntk^(rotated / (rotated
+    - 2)), which divides the lowest frequency by ntk and leaves the highest; ``by_parts = (factor, low, high,
+    original)`` divides by factor the frequencies that turn less than ``low`` times in ``original`` positions, leaves
+    those that turn more than ``high`` times, and blends in between.  ``attention_factor`` multiplies cos and sin."""
+    if positions < 1 or rotated < 2 or rotated % 2:
+        raise ValueError("positions must be positive and rotated a positive even number")
+    if not (base > 0 and linear > 0 and ntk > 0):
+        raise ValueError("base, linear and ntk must be positive")
+    if ntk != 1.0:
+        if rotated == 2:
+            raise ValueError("ntk needs more than one pair")
+        base = base * ntk ** (rotated / (rotated - 2))
+    pair = torch.arange(rotated // 2, dtype=torch.float64, device=device)
+    freq = base ** (-2.0 * pair / rotated) / linear
+    if by_parts is not None:
+        factor, low, high, original = by_parts
+        if not (factor > 0 and 0 <= low < high and original > 0):
+            raise ValueError("by_parts is (factor > 0, low, high > low, original > 0)")
+        turns = original * freq / (2 * math.pi)
+        keep = ((turns - low) / (high - low)).clamp(0, 1)
+        freq = freq * keep + freq / factor * (1 - keep)
+    angle = torch.arange(positions, dtype=torch.float64, device=device)[:, None] * freq
+    return (torch.stack((angle.cos(), angle.sin()), -1) * attention_factor).to(torch.float32)
+
+
+class PagedCache:
+    """A pool of pages: K and V [n_pages, page_size, n_kv_heads, head_dim] and, for an e4m3 cache, the rows' scales
+    k_scale and v_scale [n_pages, n_kv_heads, page_size]."""
+
+    def __init__(self, n_pages: int, page_size: int, n_kv_heads: int, head_dim: int, dtype=torch.bfloat16,
+                 device="cuda"):
+        shape = (n_pages, page_size, n_kv_heads, head_dim)
+        K, V = (torch.zeros(shape, dtype=torch.float32 if dtype == torch.float8_e4m3fn else dtype,
+                            device=device).to(dtype) for _ in range(2))
+        ks = vs = None
+        if dtype == torch.float8_e4m3fn:
+            ks, vs = (torch.ones((n_pages, n_kv_heads, page_size), dtype=torch.float32, device=device)
+                      for _ in range(2))
+        self._take(K, V, ks, vs)
+
+    @classmethod
+    def of(cls, K, V, k_scale=None, v_scale=None) -> "PagedCache":
+        """A cache of tensors that are there already (nothing is copied)."""
+        self = cls.__new__(cls)
+        self._take(K, V, k_scale, v_scale)
+        return self
+
+    def _take(self, K, V, ks, vs):
+        from . import DTYPES
+        if K.dim() != 4 or K.shape != V.shape or K.dtype != V.dtype:
+            raise ValueError("K and V must both be [n_pages, page_size, n_kv_heads, head_dim] of one type")
+        self.quantized = K.dtype == torch.float8_e4m3fn
+        if not self.quantized and K.dtype not in DTYPES:
+            raise ValueError("the cache must be bf16, fp16, fp32 or e4m3")
+        if self.quantized != (ks is not None) or self.quantized != (vs is not None):
+            raise ValueError("k_scale and v_scale belong to an e4m3 cache, and to no other")
+        tensors = [K, V] + ([ks, vs] if self.quantized else [])
+        if any(not t.is_cuda or not t.is_contiguous() or t.device != K.device for t in tensors):
+            raise ValueError("the cache's tensors must be contiguous CUDA tensors of one device")
+        if self.quantized:
+            want = (K.shape[0], K.shape[2], K.shape[1])
+            if any(t.shape != want or t.dtype != torch.float32 for t in (ks, vs)):
+                raise ValueError("k_scale and v_scale must be float32 [n_pages, n_kv_heads, page_size]")
+        self.K, self.V, self.k_scale, self.v_scale = K, V, ks, vs
+        self.n_pages, self.page_size, self.n_kv_heads, self.head_dim = K.shape
+        if self.page_size not in PAGE_SIZES:
+            raise ValueError(f"page_size must be one of {PAGE_SIZES}")
+
+
+class PagedStep:
+    """A batch over a paged cache: its page table, lengths and workspace.
+
+    page_table int32 [B, max_pages], kv_lens int32 [B] (the new tokens among them; None: nk each), q_offsets int64
+    [B + 1] (None: max_q new tokens each).  All three are read by the GPU when a call runs and may be changed in place
+    between calls; nk and max_q bound what they may hold.  Calls of one step share its workspace: order them on one
+    stream.  ``error()`` reports what the device refused."""
+
+    def __init__(self, cache: PagedCache, page_table, kv_lens=None, *, n_q_heads: int, dtype=None,
+                 nk: Optional[int] = None, max_q: int = 1, total_q: Optional[int] = None, q_offsets=None,
+                 causal: bool = True, window: int = 0, scale: float = 0.0):
+        from . import DTYPES, alloc_workspace, library
+        dtype = dtype if dtype is not None else (torch.bfloat16 if cache.quantized else cache.K.dtype)
+        if dtype not in DTYPES:
+            raise ValueError("dtype must be bf16, fp16 or fp32")
+        if not cache.quantized and cache.K.dtype != dtype:
+            raise ValueError("a cache that is not e4m3 has the tokens' type")
+        self.device = cache.K.device
+        self._tensor(page_table, torch.int32, "page_table", 2)
+        B = page_table.shape[0]
+        if kv_lens is not None:
+            self._tensor(kv_lens, torch.int32, "kv_lens", 1, B)
+        if q_offsets is not None:
+            self._tensor(q_offsets, torch.int64, "q_offsets", 1, B + 1)
+            if total_q is None:
+                raise ValueError("give total_q (the rows of the token arrays) with q_offsets")
+        self.cache, self.page_table, self.kv_lens, self.q_offsets = cache, page_table, kv_lens, q_offsets
+        self.dtype, self.batch, self.n_q_heads = dtype, B, n_q_heads
+        self.nk = int(nk) if nk is not None else page_table.shape[1] * cache.page_size
+        self.total_q = int(total_q) if total_q is not None else B * max_q
+        p = PagedParams()
+        p.batch, p.n_q_heads, p.n_kv_heads, p.head_dim = B, n_q_heads, cache.n_kv_heads, cache.head_dim
+        p.dtype = DTYPES[dtype]
+        p.cache_dtype = E4M3 if cache.quantized else p.dtype
+        p.page_size, p.n_pages, p.max_pages = cache.page_size, cache.n_pages, page_table.shape[1]
+        p.page_table = page_table.data_ptr()
+        p.kv_lens = None if kv_lens is None else kv_lens.data_ptr()
+        p.q_offsets = None if q_offsets is None else q_offsets.data_ptr()
+        p.nk, p.max_q, p.total_q = self.nk, int(max_q), self.total_q
+        p.causal, p.window, p.scale = int(bool(causal)), int(window), float(scale)
+        self.p, self._ref = p, ctypes.byref(p)
+        with torch.cuda.device(self.device):
+            n = library().santa_paged_workspace_size(self._ref)
+            if n == 0:
+                raise ValueError("invalid paged parameters")
+            self.workspace = alloc_workspace(n, self.device)
+
+    def _tensor(self, t, dtype, name, dim, size=None):
+        if t.dtype != dtype or t.dim() != dim or (size is not None and t.shape[0] != size):
+            raise ValueError(f"{name} must be {dtype} with {dim} dimension(s)" + (f" and {size} entries" if size else ""))
+        if t.device != self.device or not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous and on the cache's device")
+
+    def _heads(self, x, heads, name):
+        """Token rows of `heads` heads: any row stride, each row dense.  Returns the stride in elements."""
+        d = self.cache.head_dim
+        if x.dtype != self.dtype or tuple(x.shape) != (self.total_q, heads, d):
+            raise ValueError(f"{name} must be {self.dtype} [{self.total_q}, {heads}, {d}]")
+        if x.device != self.device or x.stride(2) != 1 or (heads > 1 and x.stride(1) != d):
+            raise ValueError(f"{name} must be on the cache's device, its rows dense")
+        return x.stride(0) if self.total_q > 1 else heads * d
+
+    def _dense(self, x, shape, dtype, name):
+        if x.dtype != dtype or tuple(x.shape) != tuple(shape) or x.device != self.device or not x.is_contiguous():
+            raise ValueError(f"{name} must be contiguous {dtype} {list(shape)} on the cache's device")
+        return x
+
+    def _call(self, fn, stream, outs, *args):
+        """Runs one C entry on `stream` (default: the device's current one), its new outputs allocated there."""
+        from . import SANTA_OK, SantaError, library
+        if torch.cuda.current_device() != self.device.index:
+            with torch.cuda.device(self.device):
+                return self._call(fn, stream, outs, *args)
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                made = [o if isinstance(o, torch.Tensor) or o is None else torch.empty(o[0], dtype=o[1], device=self.device)
+                        for o in outs]
+        else:
+            stream = torch.cuda.current_stream()
+            made = [o if isinstance(o, torch.Tensor) or o is None else torch.empty(o[0], dtype=o[1], device=self.device)
+                    for o in outs]
+        st = getattr(library(), fn)(self._ref, *[a if not callable(a) else a(made) for a in args],
+                                    self.workspace.data_ptr(), self.workspace.numel(), stream.cuda_stream)
+        if st != SANTA_OK:
+            raise SantaError(st, fn)
+        return made
+
+    def _pool(self):
+        c = self.cache
+        return (c.K.data_ptr(), c.V.data_ptr(), c.k_scale.data_ptr() if c.quantized else None,
+                c.v_scale.data_ptr() if c.quantized else None)
+
+    def append(self, q, k, v, *, rope=None, interleaved: bool = False, q_norm=None, k_norm=None, eps: float = 1e-6,
+               q_out=None, stream=None):
+        """New tokens into the cache; returns the rotated and normalised queries [total_q, n_q_heads, head_dim] (None
+        with q None).  q, k and v may be slices of one row-major projection.  Token rows past q_offsets[-1] of a new
+        q_out hold whatever the allocation held."""
+        c = self.cache
+        a = AppendParams()
+        a.k_stride, a.v_stride = self._heads(k, c.n_kv_heads, "k"), self._heads(v, c.n_kv_heads, "v")
+        a.k, a.v = k.data_ptr(), v.data_ptr()
+        shape = (self.total_q, self.n_q_heads, c.head_dim)
+        if q is not None:
+            a.q_stride, a.q = self._heads(q, self.n_q_heads, "q"), q.data_ptr()
+            if q_out is not None:
+                self._dense(q_out, shape, self.dtype, "q_out")
+        elif q_out is not None or q_norm is not None:
+            raise ValueError("q_out and q_norm go with q")
+        if q_norm is not None:
+            a.q_norm = self._dense(q_norm, (c.head_dim,), self.dtype, "q_norm").data_ptr()
+        if k_norm is not None:
+            a.k_norm = self._dense(k_norm, (c.head_dim,), self.dtype, "k_norm").data_ptr()
+        a.eps = eps
+        if rope is not None:
+            if rope.dim() != 3:
+                raise ValueError("rope must be [positions, rotated / 2, 2]")
+            self._dense(rope, (rope.shape[0], rope.shape[1], 2), torch.float32, "rope")
+            a.rope, a.rope_positions, a.rotated = rope.data_ptr(), rope.shape[0], 2 * rope.shape[1]
+            a.interleaved = int(bool(interleaved))
+
+        def filled(made):
+            a.q_out = None if made[0] is None else made[0].data_ptr()
+            return ctypes.byref(a)
+
+        out = None if q is None else q_out if q_out is not None else (shape, self.dtype)
+        return self._call("santa_kv_append", stream, [out], filled, *self._pool())[0]
+
+    def attend(self, q, *, out=None, lse=None, return_lse: bool = False, stream=None):
+        """softmax(scale q K^T + mask) V over the pages, [total_q, n_q_heads, head_dim] in q's type; with return_lse
+        (or an lse to fill) also the float32 [total_q, n_q_heads] logarithms of the softmax sums."""
+        shape = (self.total_q, self.n_q_heads, self.cache.head_dim)
+        self._dense(q, shape, self.dtype, "q")
+        if out is not None:
+            self._dense(out, shape, self.dtype, "out")
+        if lse is not None:
+            self._dense(lse, shape[:2], torch.float32, "lse")
+        wants = return_lse or lse is not None
+        made = self._call("santa_paged_attention", stream,
+                          [out if out is not None else (shape, self.dtype),
+                           lse if lse is not None else (shape[:2], torch.float32) if wants else None],
+                          q.data_ptr(), *self._pool(), lambda m: m[0].data_ptr(),
+                          lambda m: None if m[1] is None else m[1].data_ptr())
+        return (made[0], made[1]) if wants else made[0]
+
+    def read(self, kv_offsets=None, rows: Optional[int] = None, *, K_out=None, V_out=None, stream=None):
+        """The sequences' keys and values as packed rows [rows, n_kv_heads, head_dim] in the tokens' type: key n of
+        sequence b in row kv_offsets[b] + n (int64 [B + 1]; None: b * nk).  Rows that no key falls on keep what they
+        held."""
+        if kv_offsets is not None:
+            self._tensor(kv_offsets, torch.int64, "kv_offsets", 1, self.batch + 1)
+            if rows is None:
+                raise ValueError("give rows (of the packed arrays) with kv_offsets")
+        rows = int(rows) if rows is not None else self.batch * self.nk
+        shape = (rows, self.cache.n_kv_heads, self.cache.head_dim)
+        for x, name in ((K_out, "K_out"), (V_out, "V_out")):
+            if x is not None:
+                self._dense(x, shape, self.dtype, name)
+        made = self._call("santa_kv_read", stream,
+                          [K_out if K_out is not None else (shape, self.dtype),
+                           V_out if V_out is not None else (shape, self.dtype)],
+                          *self._pool(), None if kv_offsets is None else kv_offsets.data_ptr(), rows,
+                          lambda m: m[0].data_ptr(), lambda m: m[1].data_ptr())
+        return made[0], made[1]
+
+    def sample(self, q, S: int, kv_offsets, rows: int, *, variant: str = "systematic", seed: int = 0, step: int = 0,
+               sample_idx=None, stream=None):
+        """One S2ANTA / SANTA decode step over the paged cache: its rows read back packed (kv_offsets the exclusive
+        sums of kv_lens), then santa_decode on them.  q [B, n_q_heads, head_dim]; the result is float32."""
+        from . import santa_decode
+        with torch.cuda.device(self.device), torch.cuda.stream(stream):
+            K, V = self.read(kv_offsets, rows)
+            return santa_decode(q, K, V, S, variant=variant, seed=seed, step=step, nk=self.nk, kv_offsets=kv_offsets,
+                                scale=self.p.scale, sample_idx=sample_idx)
+
+    def error(self, stream=None) -> int:
+        """Synchronises and returns (then clears) the device error bits."""
+        from . import get_error
+        with torch.cuda.device(self.device):
+            return get_error(self.workspace, stream)
