@@ -134,6 +134,8 @@ constexpr int PG_CHUNK_KEYS = 128;
 cudaError_t launch_paged_tokens(const PagedArgs& a);   // few rows per KV head (mma.sync)
 cudaError_t launch_paged_merge(const PagedArgs& a, int keys);
 void plan_paged_tokens(PagedArgs& a);
+cudaError_t launch_paged_chunk(const PagedArgs& a);    // many (tcgen05.mma)
+void plan_paged_chunk(PagedArgs& a);
 
 struct AppendArgs {
   const void *q, *k, *v;

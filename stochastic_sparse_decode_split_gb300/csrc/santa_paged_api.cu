@@ -87,9 +87,13 @@ santa::PagedArgs args(const santa_paged_t* p) {
   return a;
 }
 
+// Up to 16 query rows per sequence and KV head go to the kernel for few rows,
+// more to the one whose tiles have 128 of them.
+bool few_rows(const santa::PagedArgs& a) { return (int64_t)a.max_q * a.G <= 16; }
+
 // The attention's split plan and the bytes of its partial sums behind the header.
 size_t plan(santa::PagedArgs& a) {
-  santa::plan_paged_tokens(a);
+  few_rows(a) ? santa::plan_paged_tokens(a) : santa::plan_paged_chunk(a);
   if (a.splits == 1) return HEADER;
   const size_t n = (size_t)a.B * a.tiles * a.Hkv * a.splits * a.rows;
   return HEADER + up(n * a.D * sizeof(float)) + up(n * 2 * sizeof(float));
@@ -183,8 +187,10 @@ santa_status_t santa_paged_attention(const santa_paged_t* p, const void* q, cons
   a.part_o = reinterpret_cast<float*>(w + HEADER);
   a.part_ml = reinterpret_cast<float*>(w + HEADER + up((size_t)a.B * a.tiles * a.Hkv * a.splits * a.rows * a.D * sizeof(float)));
   a.stream = (cudaStream_t)stream;
-  if (santa::launch_paged_tokens(a) != cudaSuccess) return SANTA_ERR_CUDA;
-  if (a.splits > 1 && santa::launch_paged_merge(a, santa::PG_BLK) != cudaSuccess) return SANTA_ERR_CUDA;
+  const bool few = few_rows(a);
+  if ((few ? santa::launch_paged_tokens(a) : santa::launch_paged_chunk(a)) != cudaSuccess) return SANTA_ERR_CUDA;
+  if (a.splits > 1 && santa::launch_paged_merge(a, few ? santa::PG_BLK : santa::PG_CHUNK_KEYS) != cudaSuccess)
+    return SANTA_ERR_CUDA;
   return SANTA_OK;
 }
 
