@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "santa_common.cuh"
 
 namespace santa {
@@ -126,6 +128,18 @@ __device__ __forceinline__ void tile_tokens(const PagedArgs& a, int n, int tile,
     i0 = tile * a.rows / a.G;
     i1 = min(n - 1, (tile * a.rows + a.rows - 1) / a.G);
   }
+}
+
+// Raises a kernel's dynamic shared memory limit, once per device (`done`: one bit each).
+inline cudaError_t raise_smem(const void* kernel, int bytes, std::atomic<unsigned long long>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = 1ull << (dev & 63);
+  if (dev < 64 && (done.load(std::memory_order_relaxed) & bit)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && dev < 64) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
 }
 
 // Keys per block in the split arithmetic of the two attention kernels.

@@ -4,6 +4,8 @@
 #include <math.h>
 #include <string.h>
 
+#include <atomic>
+
 #include "../../include/santa.h"
 #include "santa_launch.h"
 #include "santa_paged.cuh"
@@ -19,13 +21,16 @@ constexpr size_t ALIGN = 256, HEADER = 256;   // as in santa_api.cu: the error w
 size_t up(size_t x) { return (x + ALIGN - 1) / ALIGN * ALIGN; }
 bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
+// Multiprocessor count of the current device (152 where there is none), kept per device.
 int sms() {
-  int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-      n <= 0) {
+  static std::atomic<int> kept[64];
+  int dev = -1, n = 0;
+  if (cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < 64 && (n = kept[dev].load(std::memory_order_relaxed)) > 0) return n;
+  if (dev < 0 || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) {
     (void)cudaGetLastError();
     return 152;
   }
+  if (dev < 64) kept[dev].store(n, std::memory_order_relaxed);
   return n;
 }
 

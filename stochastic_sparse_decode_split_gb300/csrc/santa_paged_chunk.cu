@@ -668,7 +668,8 @@ template <typename T, bool E4M3, int D>
 cudaError_t chunk_inst(const PagedArgs& a) {
   using Gm = ChunkGeom<E4M3, D>;
   auto kern = paged_chunk_kernel<T, E4M3, D>;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Gm::SMEM);
+  static std::atomic<unsigned long long> raised{0};
+  const cudaError_t e = raise_smem((const void*)kern, (int)Gm::SMEM, raised);
   if (e != cudaSuccess) return e;
   const int rows = std::min(1 << a.page_shift, BKEYS);
   const long long pool = (long long)a.n_pages << a.page_shift;

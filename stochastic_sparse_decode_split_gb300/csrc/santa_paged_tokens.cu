@@ -564,7 +564,8 @@ template <typename T, bool E4M3, int D, int R>
 cudaError_t tokens_inst(const PagedArgs& a) {
   auto kern = paged_tokens_kernel<T, E4M3, D, R>;
   constexpr int smem = (int)smem_bytes<E4M3, D, R>();
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static std::atomic<unsigned long long> raised{0};
+  const cudaError_t e = raise_smem((const void*)kern, smem, raised);
   if (e != cudaSuccess) return e;
   kern<<<(unsigned)((long long)a.B * a.tiles * a.Hkv * a.splits), NT, smem, a.stream>>>(a);
   return cudaGetLastError();

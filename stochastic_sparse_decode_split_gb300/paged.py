@@ -196,6 +196,15 @@ class PagedStep:
             if n == 0:
                 raise ValueError("invalid paged parameters")
             self.workspace = alloc_workspace(n, self.device)
+        # what every call passes again: the pool (whose tensors the cache keeps) and the workspace
+        self._shape = torch.Size((self.total_q, n_q_heads, cache.head_dim))
+        self._kv_shape = torch.Size((self.total_q, cache.n_kv_heads, cache.head_dim))
+        self._pool = tuple(ctypes.c_void_p(None if t is None else t.data_ptr())
+                           for t in (cache.K, cache.V, cache.k_scale, cache.v_scale))
+        self._kept = (cache.K, cache.V, cache.k_scale, cache.v_scale)
+        self._ws = (ctypes.c_void_p(self.workspace.data_ptr()), ctypes.c_size_t(n))
+        lib = library()
+        self._append_fn, self._attend_fn, self._read_fn = lib.santa_kv_append, lib.santa_paged_attention, lib.santa_kv_read
 
     def _tensor(self, t, dtype, name, dim, size=None):
         if t.dtype != dtype or t.dim() != dim or (size is not None and t.shape[0] != size):
@@ -203,116 +212,105 @@ class PagedStep:
         if t.device != self.device or not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous and on the cache's device")
 
-    def _heads(self, x, heads, name):
-        """Token rows of `heads` heads: any row stride, each row dense.  Returns the stride in elements."""
-        d = self.cache.head_dim
-        if x.dtype != self.dtype or tuple(x.shape) != (self.total_q, heads, d):
-            raise ValueError(f"{name} must be {self.dtype} [{self.total_q}, {heads}, {d}]")
-        if x.device != self.device or x.stride(2) != 1 or (heads > 1 and x.stride(1) != d):
-            raise ValueError(f"{name} must be on the cache's device, its rows dense")
-        return x.stride(0) if self.total_q > 1 else heads * d
+    def _heads(self, x, shape, name):
+        """Token rows of heads: any row stride, each row dense.  Returns the stride in elements."""
+        stride = x.stride()
+        if x.dtype != self.dtype or x.shape != shape or x.device != self.device:
+            raise ValueError(f"{name} must be {self.dtype} {list(shape)} on the cache's device")
+        if stride[2] != 1 or (shape[1] > 1 and stride[1] != shape[2]):
+            raise ValueError(f"the rows of {name} must be dense")
+        return stride[0] if shape[0] > 1 else shape[1] * shape[2]
 
     def _dense(self, x, shape, dtype, name):
-        if x.dtype != dtype or tuple(x.shape) != tuple(shape) or x.device != self.device or not x.is_contiguous():
+        if x.dtype != dtype or x.shape != shape or x.device != self.device or not x.is_contiguous():
             raise ValueError(f"{name} must be contiguous {dtype} {list(shape)} on the cache's device")
         return x
 
-    def _call(self, fn, stream, outs, *args):
-        """Runs one C entry on `stream` (default: the device's current one), its new outputs allocated there."""
-        from . import SANTA_OK, SantaError, library
+    def _on(self, stream):
+        """The raw stream of a call: the given one, or the device's current one."""
         if torch.cuda.current_device() != self.device.index:
-            with torch.cuda.device(self.device):
-                return self._call(fn, stream, outs, *args)
-        if stream is not None:
-            with torch.cuda.stream(stream):
-                made = [o if isinstance(o, torch.Tensor) or o is None else torch.empty(o[0], dtype=o[1], device=self.device)
-                        for o in outs]
-        else:
-            stream = torch.cuda.current_stream()
-            made = [o if isinstance(o, torch.Tensor) or o is None else torch.empty(o[0], dtype=o[1], device=self.device)
-                    for o in outs]
-        st = getattr(library(), fn)(self._ref, *[a if not callable(a) else a(made) for a in args],
-                                    self.workspace.data_ptr(), self.workspace.numel(), stream.cuda_stream)
-        if st != SANTA_OK:
-            raise SantaError(st, fn)
-        return made
+            raise ValueError("make the cache's device the current one for its calls")
+        return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(self.device.index)
 
-    def _pool(self):
-        c = self.cache
-        return (c.K.data_ptr(), c.V.data_ptr(), c.k_scale.data_ptr() if c.quantized else None,
-                c.v_scale.data_ptr() if c.quantized else None)
+    def _new(self, shape, dtype, stream):
+        """An output, allocated for the stream that the call runs on."""
+        if stream is None:
+            return torch.empty(shape, dtype=dtype, device=self.device)
+        with torch.cuda.stream(stream):
+            return torch.empty(shape, dtype=dtype, device=self.device)
+
+    @staticmethod
+    def _check(status, fn):
+        if status != 0:
+            from . import SantaError
+            raise SantaError(status, fn)
 
     def append(self, q, k, v, *, rope=None, interleaved: bool = False, q_norm=None, k_norm=None, eps: float = 1e-6,
                q_out=None, stream=None):
         """New tokens into the cache; returns the rotated and normalised queries [total_q, n_q_heads, head_dim] (None
         with q None).  q, k and v may be slices of one row-major projection.  Token rows past q_offsets[-1] of a new
         q_out hold whatever the allocation held."""
-        c = self.cache
+        raw = self._on(stream)
+        d = self.cache.head_dim
         a = AppendParams()
-        a.k_stride, a.v_stride = self._heads(k, c.n_kv_heads, "k"), self._heads(v, c.n_kv_heads, "v")
+        a.k_stride, a.v_stride = self._heads(k, self._kv_shape, "k"), self._heads(v, self._kv_shape, "v")
         a.k, a.v = k.data_ptr(), v.data_ptr()
-        shape = (self.total_q, self.n_q_heads, c.head_dim)
         if q is not None:
-            a.q_stride, a.q = self._heads(q, self.n_q_heads, "q"), q.data_ptr()
+            a.q_stride, a.q = self._heads(q, self._shape, "q"), q.data_ptr()
             if q_out is not None:
-                self._dense(q_out, shape, self.dtype, "q_out")
+                self._dense(q_out, self._shape, self.dtype, "q_out")
+            else:
+                q_out = self._new(self._shape, self.dtype, stream)
+            a.q_out = q_out.data_ptr()
         elif q_out is not None or q_norm is not None:
             raise ValueError("q_out and q_norm go with q")
         if q_norm is not None:
-            a.q_norm = self._dense(q_norm, (c.head_dim,), self.dtype, "q_norm").data_ptr()
+            a.q_norm = self._dense(q_norm, (d,), self.dtype, "q_norm").data_ptr()
         if k_norm is not None:
-            a.k_norm = self._dense(k_norm, (c.head_dim,), self.dtype, "k_norm").data_ptr()
+            a.k_norm = self._dense(k_norm, (d,), self.dtype, "k_norm").data_ptr()
         a.eps = eps
         if rope is not None:
-            if rope.dim() != 3:
+            shape = rope.shape
+            if len(shape) != 3 or shape[2] != 2:
                 raise ValueError("rope must be [positions, rotated / 2, 2]")
-            self._dense(rope, (rope.shape[0], rope.shape[1], 2), torch.float32, "rope")
-            a.rope, a.rope_positions, a.rotated = rope.data_ptr(), rope.shape[0], 2 * rope.shape[1]
-            a.interleaved = int(bool(interleaved))
-
-        def filled(made):
-            a.q_out = None if made[0] is None else made[0].data_ptr()
-            return ctypes.byref(a)
-
-        out = None if q is None else q_out if q_out is not None else (shape, self.dtype)
-        return self._call("santa_kv_append", stream, [out], filled, *self._pool())[0]
+            a.rope = self._dense(rope, shape, torch.float32, "rope").data_ptr()
+            a.rope_positions, a.rotated, a.interleaved = shape[0], 2 * shape[1], 1 if interleaved else 0
+        self._check(self._append_fn(self._ref, ctypes.byref(a), *self._pool, *self._ws, raw), "santa_kv_append")
+        return q_out
 
     def attend(self, q, *, out=None, lse=None, return_lse: bool = False, stream=None):
         """softmax(scale q K^T + mask) V over the pages, [total_q, n_q_heads, head_dim] in q's type; with return_lse
         (or an lse to fill) also the float32 [total_q, n_q_heads] logarithms of the softmax sums."""
-        shape = (self.total_q, self.n_q_heads, self.cache.head_dim)
-        self._dense(q, shape, self.dtype, "q")
+        raw = self._on(stream)
+        self._dense(q, self._shape, self.dtype, "q")
         if out is not None:
-            self._dense(out, shape, self.dtype, "out")
+            self._dense(out, self._shape, self.dtype, "out")
+        else:
+            out = self._new(self._shape, self.dtype, stream)
         if lse is not None:
-            self._dense(lse, shape[:2], torch.float32, "lse")
-        wants = return_lse or lse is not None
-        made = self._call("santa_paged_attention", stream,
-                          [out if out is not None else (shape, self.dtype),
-                           lse if lse is not None else (shape[:2], torch.float32) if wants else None],
-                          q.data_ptr(), *self._pool(), lambda m: m[0].data_ptr(),
-                          lambda m: None if m[1] is None else m[1].data_ptr())
-        return (made[0], made[1]) if wants else made[0]
+            self._dense(lse, self._shape[:2], torch.float32, "lse")
+        elif return_lse:
+            lse = self._new(self._shape[:2], torch.float32, stream)
+        self._check(self._attend_fn(self._ref, q.data_ptr(), *self._pool, out.data_ptr(),
+                                    None if lse is None else lse.data_ptr(), *self._ws, raw), "santa_paged_attention")
+        return out if lse is None else (out, lse)
 
     def read(self, kv_offsets=None, rows: Optional[int] = None, *, K_out=None, V_out=None, stream=None):
         """The sequences' keys and values as packed rows [rows, n_kv_heads, head_dim] in the tokens' type: key n of
         sequence b in row kv_offsets[b] + n (int64 [B + 1]; None: b * nk).  Rows that no key falls on keep what they
         held."""
+        raw = self._on(stream)
         if kv_offsets is not None:
             self._tensor(kv_offsets, torch.int64, "kv_offsets", 1, self.batch + 1)
             if rows is None:
                 raise ValueError("give rows (of the packed arrays) with kv_offsets")
         rows = int(rows) if rows is not None else self.batch * self.nk
         shape = (rows, self.cache.n_kv_heads, self.cache.head_dim)
-        for x, name in ((K_out, "K_out"), (V_out, "V_out")):
-            if x is not None:
-                self._dense(x, shape, self.dtype, name)
-        made = self._call("santa_kv_read", stream,
-                          [K_out if K_out is not None else (shape, self.dtype),
-                           V_out if V_out is not None else (shape, self.dtype)],
-                          *self._pool(), None if kv_offsets is None else kv_offsets.data_ptr(), rows,
-                          lambda m: m[0].data_ptr(), lambda m: m[1].data_ptr())
-        return made[0], made[1]
+        K_out = self._dense(K_out, shape, self.dtype, "K_out") if K_out is not None else self._new(shape, self.dtype, stream)
+        V_out = self._dense(V_out, shape, self.dtype, "V_out") if V_out is not None else self._new(shape, self.dtype, stream)
+        self._check(self._read_fn(self._ref, *self._pool, None if kv_offsets is None else kv_offsets.data_ptr(), rows,
+                                  K_out.data_ptr(), V_out.data_ptr(), *self._ws, raw), "santa_kv_read")
+        return K_out, V_out
 
     def sample(self, q, S: int, kv_offsets, rows: int, *, variant: str = "systematic", seed: int = 0, step: int = 0,
                sample_idx=None, stream=None):
