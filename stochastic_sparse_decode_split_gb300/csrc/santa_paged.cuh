@@ -37,16 +37,24 @@ struct PagedArgs {
   const float* vs;
   void* out;
   float* lse;
+  int wide;             // `out` is 32-byte aligned
   int* err;
   // attention: packed rows (token * G + head of the group) are cut into tiles
   // of `rows` of them (`tokens` whole tokens when the tiles keep tokens
-  // together, else 0); tiles per sequence, most splits of a tile and key
-  // blocks per split
+  // together, else 0); tiles per sequence at most.  Few rows: most splits of a
+  // tile and key blocks per split; chunks: `splits` CTAs
   int rows, tokens, tiles, splits, split_blk;
-  float* part_o;        // [B, tiles, Hkv, splits, rows, D] unnormalised sums
-  float* part_ml;       // [B, tiles, Hkv, splits, rows, 2] maximum (base 2) and sum
+  float* part_o;        // [pieces, rows, D] unnormalised sums
+  float* part_ml;       // [pieces, rows, 2] maximum (base 2) and sum; a negative sum marks a bad page
+  struct ChunkShare* share;   // [splits] chunk attention: the shared items
   int num_sms;
   cudaStream_t stream;
+};
+
+// An item of the chunk attention that several CTAs share: its pieces are
+// slot `slot` of CTA `first` and slot 0 of the following ones (count 0: none).
+struct ChunkShare {
+  int b, kvh, tile, first, slot, count;
 };
 
 // One sequence: its new tokens' first row and number, its keys.  `ok` false:
@@ -103,9 +111,9 @@ __device__ __forceinline__ void visible_keys(const PagedArgs& a, int kv, int pos
 }
 
 // The key blocks of a tile whose first and last token are i0 and i1 (of n):
-// blk blocks of `keys` keys from block lo on, in how many splits.
+// blk blocks of `keys` keys from block blk_lo on.
 struct TileKeys {
-  int blk_lo, blk, splits;
+  int blk_lo, blk;
 };
 __device__ __forceinline__ TileKeys tile_keys(const PagedArgs& a, const Seq& s, int i0, int i1, int keys) {
   int lo0, hi0, lo1, hi1;
@@ -114,7 +122,6 @@ __device__ __forceinline__ TileKeys tile_keys(const PagedArgs& a, const Seq& s, 
   TileKeys t;
   t.blk_lo = lo0 / keys;
   t.blk = hi1 > lo0 ? (hi1 + keys - 1) / keys - t.blk_lo : 0;
-  t.splits = max(1, (t.blk + a.split_blk - 1) / a.split_blk);
   return t;
 }
 
@@ -142,14 +149,14 @@ inline cudaError_t raise_smem(const void* kernel, int bytes, std::atomic<unsigne
   return e;
 }
 
-// Keys per block in the split arithmetic of the two attention kernels.
-constexpr int PG_CHUNK_KEYS = 128;
+constexpr int PG_CHUNK_KEYS = 128;   // keys per block of the chunk attention
 
-cudaError_t launch_paged_tokens(const PagedArgs& a);   // few rows per KV head (mma.sync)
-cudaError_t launch_paged_merge(const PagedArgs& a, int keys);
-void plan_paged_tokens(PagedArgs& a);
-cudaError_t launch_paged_chunk(const PagedArgs& a);    // many (tcgen05.mma)
-void plan_paged_chunk(PagedArgs& a);
+// The two attention kernels: their plan (the number of pieces whose sums go
+// through memory) and their launches, merge included.
+size_t plan_paged_tokens(PagedArgs& a);                // few rows per KV head (mma.sync)
+cudaError_t launch_paged_tokens(const PagedArgs& a);
+int plan_paged_chunk(PagedArgs& a);                    // many (tcgen05.mma)
+cudaError_t launch_paged_chunk(const PagedArgs& a);
 
 struct AppendArgs {
   const void *q, *k, *v;

@@ -96,12 +96,20 @@ santa::PagedArgs args(const santa_paged_t* p) {
 // more to the one whose tiles have 128 of them.
 bool few_rows(const santa::PagedArgs& a) { return (int64_t)a.max_q * a.G <= 16; }
 
-// The attention's split plan and the bytes of its partial sums behind the header.
-size_t plan(santa::PagedArgs& a) {
-  few_rows(a) ? santa::plan_paged_tokens(a) : santa::plan_paged_chunk(a);
-  if (a.splits == 1) return HEADER;
-  const size_t n = (size_t)a.B * a.tiles * a.Hkv * a.splits * a.rows;
-  return HEADER + up(n * a.D * sizeof(float)) + up(n * 2 * sizeof(float));
+// The attention's plan, and its workspace: header, the chunk attention's notes
+// of shared items, the pieces' sums.
+struct Plan {
+  size_t share, part_o, part_ml, total;
+};
+Plan plan(santa::PagedArgs& a) {
+  const bool few = few_rows(a);
+  const size_t rows = (few ? santa::plan_paged_tokens(a) : (size_t)santa::plan_paged_chunk(a)) * a.rows;
+  Plan p;
+  p.share = HEADER;
+  p.part_o = p.share + (few ? 0 : up((size_t)a.splits * sizeof(santa::ChunkShare)));
+  p.part_ml = p.part_o + up(rows * a.D * sizeof(float));
+  p.total = p.part_ml + up(rows * 2 * sizeof(float));
+  return p;
 }
 
 }  // namespace
@@ -111,7 +119,7 @@ extern "C" {
 size_t santa_paged_workspace_size(const santa_paged_t* p) {
   if (check(p) != SANTA_OK) return 0;
   santa::PagedArgs a = args(p);
-  return plan(a);
+  return plan(a).total;
 }
 
 santa_status_t santa_kv_append(const santa_paged_t* p, const santa_append_t* ap, void* K, void* V, float* k_scale,
@@ -176,10 +184,11 @@ santa_status_t santa_paged_attention(const santa_paged_t* p, const void* q, cons
   if (p->dtype == SANTA_FP32) return SANTA_ERR_UNSUPPORTED;
   if (!q || !out || !aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4)) return SANTA_ERR_INVALID_ARG;
   santa::PagedArgs a = args(p);
-  const size_t need = plan(a);
-  st = check_cache(p, K, V, k_scale, v_scale, workspace, ws_bytes, need);
+  const Plan l = plan(a);
+  st = check_cache(p, K, V, k_scale, v_scale, workspace, ws_bytes, l.total);
   if (st != SANTA_OK) return st;
-  if ((int64_t)a.B * a.tiles * a.Hkv > INT32_MAX / a.splits) return SANTA_ERR_UNSUPPORTED;   // one CTA per split
+  const bool few = few_rows(a);
+  if (few && (int64_t)a.B * a.tiles * a.Hkv > INT32_MAX / a.splits) return SANTA_ERR_UNSUPPORTED;   // one CTA per split
   unsigned char* w = static_cast<unsigned char*>(workspace);
   a.q = q;
   a.K = K;
@@ -188,15 +197,13 @@ santa_status_t santa_paged_attention(const santa_paged_t* p, const void* q, cons
   a.vs = v_scale;
   a.out = out;
   a.lse = lse;
+  a.wide = aligned(out, 32);
   a.err = reinterpret_cast<int*>(w);
-  a.part_o = reinterpret_cast<float*>(w + HEADER);
-  a.part_ml = reinterpret_cast<float*>(w + HEADER + up((size_t)a.B * a.tiles * a.Hkv * a.splits * a.rows * a.D * sizeof(float)));
+  a.share = reinterpret_cast<santa::ChunkShare*>(w + l.share);
+  a.part_o = reinterpret_cast<float*>(w + l.part_o);
+  a.part_ml = reinterpret_cast<float*>(w + l.part_ml);
   a.stream = (cudaStream_t)stream;
-  const bool few = few_rows(a);
-  if ((few ? santa::launch_paged_tokens(a) : santa::launch_paged_chunk(a)) != cudaSuccess) return SANTA_ERR_CUDA;
-  if (a.splits > 1 && santa::launch_paged_merge(a, few ? santa::PG_BLK : santa::PG_CHUNK_KEYS) != cudaSuccess)
-    return SANTA_ERR_CUDA;
-  return SANTA_OK;
+  return (few ? santa::launch_paged_tokens(a) : santa::launch_paged_chunk(a)) == cudaSuccess ? SANTA_OK : SANTA_ERR_CUDA;
 }
 
 santa_status_t santa_kv_read(const santa_paged_t* p, const void* K, const void* V, const float* k_scale,

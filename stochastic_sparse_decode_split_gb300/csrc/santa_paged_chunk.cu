@@ -2,11 +2,14 @@
 // cache: both products on the fifth-generation tensor cores, sums in tensor
 // memory.
 //
-// A CTA takes two tiles of 128 query rows of one sequence and KV head (the
+// An item is two tiles of 128 query rows of one sequence and KV head (the
 // group's heads of consecutive tokens: a K or V row in shared memory serves
-// all of them) and the key blocks, 128 keys each, of its split.  With 256 rows
-// per 64 KiB of K and V the products bound the kernel, then the exponentials,
-// then the L2; HBM does not.  Roles, one CTA per SM:
+// all of them) against its keys, in blocks of 128.  With 256 rows per 64 KiB
+// of K and V the products bound the kernel, then the exponentials, then the
+// L2; HBM does not.  One CTA per SM; each takes an equal share of the blocks
+// of the whole batch, counted from the lengths on the device, so a CTA's share
+// may begin or end inside an item, whose sums then go through memory (see
+// Walk).  Roles:
 //   warps 0-3, 4-7  softmax of tile 0 and 1: one thread per row.  S comes out
 //                   of tensor memory, P goes back over it in 16 bits, the sum
 //                   O is rescaled only when the maximum has grown by 2^8
@@ -20,10 +23,14 @@
 //                   taken out and given back at the end to the rows that see them
 //   warps 12-15     e4m3 caches: codes widen to fp16 in place (TMA brings them
 //                   into the stage's upper half); the scales are staged beside
-// Order of the products: S of block j + 1 is issued after O += P V of block j
-// of the same tile and overwrites the columns P was read from; products issued
-// by one thread execute in order.  That S is complete therefore says that the
-// previous O is too, which is when the softmax may rescale O.
+// An item whose second tile is empty (few tokens) gives its blocks to the two
+// softmax groups in turn, with a sum O each, joined at the end.
+//
+// A job is one tile (or, of such an item, one group) and one block.  Order of
+// the products: S of job k + 2 is issued after O += P V of job k, whose P it
+// overwrites; products issued by one thread execute in order.  That S is
+// complete therefore says that the O of the same tile is too, which is when
+// the softmax may rescale it.
 #include <algorithm>
 #include <cstring>
 #include <mutex>
@@ -39,9 +46,12 @@ namespace santa {
 
 namespace {
 
+
 constexpr int BKEYS = PG_CHUNK_KEYS;   // keys per block
 constexpr int TROWS = 128;             // rows per tile (lanes of tensor memory)
 constexpr float RESCALE = 8.f;         // growth of the maximum (base 2) that O is rescaled for
+constexpr int CHUNK_SHARE = 8;         // blocks of time that sharing an item costs
+constexpr int CHUNK_LEAST = 16;        // items of no more blocks are never shared, and no merge is launched for them
 constexpr unsigned long long WAIT_NS = 1000000000ull;
 
 template <bool E4M3, int D>
@@ -57,21 +67,38 @@ struct ChunkGeom {
 
 // Barriers.
 enum { Q_FULL, Q_READY, K_FULL, K_READY = K_FULL + 2, K_EMPTY = K_READY + 2, V_FULL = K_EMPTY + 2, V_READY = V_FULL + 2,
-       V_EMPTY = V_READY + 2, S_FULL = V_EMPTY + 2, P_FULL = S_FULL + 2, O_DONE = P_FULL + 2, N_BAR = O_DONE + 2 };
+       V_EMPTY = V_READY + 2, S_FULL = V_EMPTY + 2, P_FULL = S_FULL + 2, O_FREE = P_FULL + 2, O_DONE = O_FREE + 2, ML_FULL,
+       Q_SEEN, N_BAR };
+
+// Whether a phase is over, without waiting.
+__device__ __forceinline__ bool test_phase(uint32_t bar, unsigned parity) {
+  uint32_t ok;
+  asm volatile("{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+               : "=r"(ok)
+               : "r"(bar), "r"(parity)
+               : "memory");
+  return ok != 0;
+}
 
 // Waits for a phase, for a second at most; after one wait has run out in the
 // CTA (`dead`), no other waits.
 __device__ __forceinline__ void wait_phase(uint32_t bar, unsigned parity, int* err, volatile int* dead) {
-  if (mbar_try_wait(bar, parity)) return;
-  const unsigned long long t0 = global_ns();
-  for (;;) {
+  if (test_phase(bar, parity)) return;   // 40 cycles; the waiting form takes more also where there is nothing to wait for
+  unsigned long long t0 = 0;
+  for (unsigned i = 0;; ++i) {
     if (mbar_try_wait(bar, parity)) return;
-    if (*dead) return;
-    if (global_ns() - t0 > WAIT_NS) break;
+    if (i % 64 == 63) {
+      if (*dead) return;
+      if (t0 == 0) t0 = global_ns();
+      else if (global_ns() - t0 > WAIT_NS) break;
+    }
   }
   *dead = 1;
   flag_error(err, ERR_TIMEOUT);
 }
+// A value that is the same in every lane, in a register that the compiler
+// knows to be uniform (loops and addresses that depend on it then are, too).
+__device__ __forceinline__ unsigned uniform(unsigned x) { return __reduce_max_sync(FULL, x); }
 
 template <typename T> __device__ __forceinline__ uint32_t pack2h(float lo, float hi);
 template <> __device__ __forceinline__ uint32_t pack2h<bf16_t>(float lo, float hi) {
@@ -106,6 +133,23 @@ __device__ __forceinline__ f2x mul2(f2x a, f2x b) {
 __device__ __forceinline__ void sts128(uint32_t addr, uint4 v) {
   asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
+__device__ __forceinline__ float2 lds_f2(uint32_t addr) {
+  float2 f;
+  asm("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(f.x), "=f"(f.y) : "r"(addr));
+  return f;
+}
+// Two e4m3 codes (the low 16 bits) as fp16, exact.
+__device__ __forceinline__ uint32_t widen8(uint32_t two) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)two));
+  return r;
+}
+// 32 bytes, 32-byte aligned.
+__device__ __forceinline__ void st_global8(void* p, const uint32_t* w) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+               "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
 __device__ __forceinline__ void tma_load_hint(uint32_t dst, const CUtensorMap* tm, int x, int y, int z, uint32_t bar) {
   asm volatile(
       "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
@@ -131,6 +175,187 @@ __device__ __forceinline__ uint32_t without_odd16(uint32_t w) {
   return w;
 }
 
+// One CTA's share of the batch.  Items in the order (sequence, tile, KV head)
+// weigh their blocks (at least one); CTA c of P takes the blocks
+// [floor(T c / P), floor(T (c + 1) / P)) of the T, or (`split` false) the items
+// that begin in that range.  Every role of the CTA walks the same pieces.
+struct Share {
+  long long lo, hi, T;
+  int P, split;
+  int b, kvh, tile;   // the item that holds block lo
+  long long pos;      // its first block
+};
+__device__ __forceinline__ long long share_begin(long long T, int c, int P) {
+  if (T < (1ll << 24)) return (unsigned)T * (unsigned)c / (unsigned)P;   // c < 256
+  return T * c / P;
+}
+struct Piece {
+  int b, kvh, tile;
+  Seq s;
+  int i0, i1;         // first and last token
+  int blk0, nblk;     // blocks of this piece (0: no key is visible)
+  bool two;           // the second tile holds tokens
+  bool whole, last;   // of the item: all its blocks, its last one
+  long long pos;      // the item's first block
+};
+struct Walk {
+  int b, kvh, tile, of, i0, i1;
+  TileKeys tk;
+  long long pos;
+  Seq s;
+  __device__ __forceinline__ void start(const PagedArgs& a, const Share& sh) {
+    b = sh.b;
+    kvh = sh.kvh;
+    tile = sh.tile;
+    pos = sh.pos;
+    if (b < a.B) load(a);
+  }
+  __device__ __forceinline__ void load(const PagedArgs& a) {   // a sequence and its tile
+    s = paged_seq(a, b, false);
+    keys(a);
+  }
+  __device__ __forceinline__ void keys(const PagedArgs& a) {
+    tile_tokens(a, s.n, tile, i0, i1);
+    tk = tile_keys(a, s, i0, i1, BKEYS);
+  }
+  __device__ __forceinline__ bool next(const PagedArgs& a, const Share& sh, Piece& p) {
+    for (;;) {
+      if (b >= a.B || pos >= sh.hi) return false;
+      if (kvh == a.Hkv || tile * a.tokens >= s.n) {
+        kvh = 0;
+        if (++tile * a.tokens >= s.n) {
+          tile = 0;
+          if (++b < a.B) load(a);
+        } else {
+          keys(a);
+        }
+        continue;
+      }
+      const int w = max(tk.blk, 1);
+      long long begin = max(sh.lo, pos) - pos, end = min(sh.hi, pos + w) - pos;
+      if (!sh.split) {
+        begin = pos >= sh.lo ? 0 : w;
+        end = w;
+      }
+      p.pos = pos;
+      p.kvh = kvh;
+      ++kvh;
+      pos += w;
+      if (begin >= end) continue;
+      p.b = b;
+      p.tile = tile;
+      p.s = s;
+      p.i0 = i0;
+      p.i1 = i1;
+      p.blk0 = tk.blk_lo + (int)begin;
+      p.nblk = tk.blk ? (int)(end - begin) : 0;
+      p.two = i0 + a.tokens / 2 < s.n;
+      p.whole = end - begin == w;
+      p.last = end == w;
+      return true;
+    }
+  }
+};
+
+// Blocks of item i = (sequence, tile), 0 where the tile has no token.
+__device__ __forceinline__ int item_weight(const PagedArgs& a, long long i, bool flag) {
+  if (i >= (long long)a.B * a.tiles) return 0;
+  const int b = (int)(i / a.tiles), tile = (int)(i - (long long)b * a.tiles);
+  const Seq s = paged_seq(a, b, flag && tile == 0);
+  if (tile * a.tokens >= s.n) return 0;
+  int i0, i1;
+  tile_tokens(a, s.n, tile, i0, i1);
+  return max(tile_keys(a, s, i0, i1, BKEYS).blk, 1);
+}
+__device__ __forceinline__ int scan_add(int v, int lane) {   // inclusive, over a warp
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(FULL, v, o);
+    if (lane >= o) v += u;
+  }
+  return v;
+}
+
+// Fills `sh` but for a barrier at the end; every thread of the CTA calls it,
+// NT of them, one item each at a time.  One round of look-ups and one barrier
+// where the batch has at most NT tiles.
+template <int NT>
+__device__ __forceinline__ void take_share(const PagedArgs& a, Share& sh, long long* s_sum, int* s_items, int* s_most) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  constexpr int NWP = NT / 32;
+  const long long n = (long long)a.B * a.tiles;
+  const int mine = item_weight(a, tid, blockIdx.x == 0);
+  int incl = scan_add(mine, lane), items = __popc(__ballot_sync(FULL, mine > 0)), most = (int)__reduce_max_sync(FULL, (unsigned)mine);
+  long long sum = __shfl_sync(FULL, incl, 31);
+  for (long long i = tid + NT; i < n + lane; i += NT) {   // whole warps
+    const int w = item_weight(a, i, blockIdx.x == 0);
+    sum += (long long)__reduce_add_sync(FULL, (unsigned)w);
+    items += __popc(__ballot_sync(FULL, w > 0));
+    most = max(most, (int)__reduce_max_sync(FULL, (unsigned)w));
+  }
+  if (tid == 0) sh.b = a.B;
+  if (lane == 0) {
+    s_sum[warp] = sum;
+    s_items[warp] = items;
+    s_most[warp] = most;
+  }
+  __syncthreads();
+  long long total = 0, all = 0, before = 0;
+#pragma unroll
+  for (int w = 0; w < NWP; ++w) {
+    if (w < warp) before += s_sum[w];
+    total += s_sum[w];
+    all += s_items[w];
+    most = max(most, s_most[w]);
+  }
+  const long long T = total * a.Hkv;
+  const int P = (int)min((long long)gridDim.x, T);
+  if ((int)blockIdx.x >= P) {
+    if (tid == 0) sh.lo = sh.hi = sh.pos = 0;
+    return;
+  }
+  const long long lo = share_begin(T, blockIdx.x, P);
+  if (tid == 0) {
+    sh.T = T;
+    sh.P = P;
+    sh.lo = lo;
+    sh.hi = share_begin(T, blockIdx.x + 1, P);
+    // A shared item costs about CHUNK_SHARE blocks of time (its sums out and
+    // in again); without sharing the longest CTA has about ceil(items / P) of
+    // the largest items.
+    all *= a.Hkv;
+    const long long each = all <= P ? 1 : (all + P - 1) / P;
+    sh.split = most > CHUNK_LEAST && each * most > sh.hi - lo + CHUNK_SHARE;
+  }
+  auto place = [&](long long i, long long first, int w) {   // item i, whose blocks (of one KV head) begin at `first`
+    const long long pos = first * a.Hkv;
+    if (w == 0 || lo < pos || lo >= pos + (long long)w * a.Hkv) return;
+    sh.b = (int)(i / a.tiles);
+    sh.tile = (int)(i - (long long)sh.b * a.tiles);
+    sh.kvh = (int)(lo - pos) / w;
+    sh.pos = pos + (long long)sh.kvh * w;
+  };
+  if (n <= NT) {
+    place(tid, before + incl - mine, mine);
+    return;
+  }
+  long long base = 0;   // weight of the items before i0
+  for (long long i0 = 0; i0 < n && base * a.Hkv <= lo; i0 += NT) {
+    const int w = item_weight(a, i0 + tid, false);
+    incl = scan_add(w, lane);
+    __syncthreads();
+    if (lane == 31) s_sum[warp] = incl;
+    __syncthreads();
+    before = base;
+#pragma unroll
+    for (int k = 0; k < NWP; ++k) {
+      if (k < warp) before += s_sum[k];
+      base += s_sum[k];
+    }
+    place(i0 + tid, before + incl - w, w);
+  }
+}
+
 // T: type of q and out; the products' type is T, or fp16 over an e4m3 cache.
 template <typename T, bool E4M3, int D>
 __global__ void __launch_bounds__(ChunkGeom<E4M3, D>::THREADS, 1)
@@ -140,108 +365,158 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
   using M16 = typename std::conditional<E4M3, fp16_t, T>::type;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   __shared__ __align__(8) unsigned long long s_bar[N_BAR];
+  __shared__ Share sh;
+  __shared__ long long s_sum[Gm::THREADS / 32];
+  __shared__ int s_items[Gm::THREADS / 32], s_most[Gm::THREADS / 32];
+  __shared__ float s_ml[2][2][TROWS], s_sl[TROWS];
   __shared__ uint32_t s_tm;
-  __shared__ int s_dead, s_bad, s_odd;
+  __shared__ int s_dead, s_bad[4], s_odd[4];   // of piece np: entry np & 3 holds np + 1
+  __shared__ Walk s_walk[8];                    // the softmax warps' walks: their registers hold rows of S
+  __shared__ Piece s_piece[8];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   allow_dependents();
-
-  // ---- which pair of tiles, which split (tiles fastest: the CTAs that run
-  // together share K and V in the L2; a causal chunk's last, longest, first)
-  unsigned x = blockIdx.x;
-  const int tile = a.tiles - 1 - (int)(x % a.tiles);
-  x /= a.tiles;
-  const int split = x % a.splits;
-  x /= a.splits;
-  const int kvh = x % a.Hkv, b = x / a.Hkv;
-  const Seq s = paged_seq(a, b, tid == 0 && split == 0 && kvh == 0 && tile == 0);
-  const int per = TROWS / a.G;                       // tokens per tile of 128 rows
-  const int tok0 = tile * a.tokens;
-  if (tok0 >= s.n) return;
-  int i0, i1;
-  tile_tokens(a, s.n, tile, i0, i1);
-  const TileKeys tk = tile_keys(a, s, i0, i1, BKEYS);
-  if (split >= tk.splits) return;
-  const int blk0 = tk.blk_lo + split * a.split_blk;
-  const int nblk = min(a.split_blk, tk.blk - split * a.split_blk);
-  const int first_pos = s.kv - s.n;
-  const bool two = tok0 + per < s.n;                 // the second tile holds tokens
 
   const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
   const uint32_t bar0 = smem_addr(s_bar);
   auto bar = [&](int i) { return bar0 + 8u * (uint32_t)i; };
   if (tid == 0) {
-    s_dead = s_bad = s_odd = 0;
+    s_dead = 0;
+    for (int i = 0; i < 4; ++i) s_bad[i] = s_odd[i] = 0;
     for (int i = 0; i < N_BAR; ++i) {
-      const int count = i == Q_READY ? (two ? 8 : 4)
+      const int count = i == Q_READY ? 8
                         : i == K_READY || i == K_READY + 1 ? 4
                         : i == V_READY || i == V_READY + 1 ? (E4M3 ? 4 : 2)
-                        : i == P_FULL || i == P_FULL + 1 ? 4 : 1;
+                        : i == P_FULL || i == P_FULL + 1 || i == O_FREE || i == O_FREE + 1 || i == ML_FULL || i == Q_SEEN ? 4 : 1;
       mbar_init(bar(i), (unsigned)count);
     }
     mbar_fence_init();
+    a.share[blockIdx.x].count = 0;
   }
   if (warp == 8) tm_alloc(smem_addr(&s_tm), 512);
+  if (tid == 288) {
+    prefetch_tensormap(&tmQ);
+    prefetch_tensormap(&tmK);
+    prefetch_tensormap(&tmV);
+  }
+  take_share<Gm::THREADS>(a, sh, s_sum, s_items, s_most);
   tm_fence_before();
   __syncthreads();
   tm_fence_after();
-  const uint32_t tm = s_tm;
+  const uint32_t tm = uniform(s_tm);
   volatile int* const dead = &s_dead;
   const uint32_t tmS = tm, tmO = tm + 256;           // tile t: S (and P) at 128 t, O at 256 + 128 t
+  const int per = TROWS / a.G;                       // tokens per tile of 128 rows
 
   if (warp >= 8) {
-    // registers: 256 x 208 + 128 x 88 of the launch's 384 x 168, 256 x 176 + 256 x 80 of 512 x 128
-    if (E4M3) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    Walk walk;
+    Piece p;
+    walk.start(a, sh);
+    // registers: 256 x 208 + 128 x 88 of the launch's 384 x 168, 256 x 192 + 256 x 64 of 512 x 128
+    if (E4M3) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     else asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == 8) {
       // -------------------------------------------------------- the products
-      if (lane == 0 && nblk > 0) {
+      {
         constexpr uint32_t shS = mma_shape(std::is_same<M16, bf16_t>::value, BKEYS, false);
         constexpr uint32_t shO = mma_shape(std::is_same<M16, bf16_t>::value, D, true);
-        auto product_s = [&](int t, int st) {
-#pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const uint32_t o = (uint32_t)((k >> 2) * Gm::HALF + (k & 3) * 32);
-            mma_ss(tmS + 128 * t, smem_operand(base + t * Gm::TILE + o, 16),
-                   smem_operand(base + Gm::OFF_K + st * Gm::TILE + o, 16), shS, k != 0);
-          }
-          mma_commit(bar(S_FULL + t));
-        };
-        auto product_o = [&](int t, int st, bool add) {
-#pragma unroll
-          for (int k = 0; k < BKEYS / 16; ++k)
-            mma_ts(tmO + 128 * t, tmS + 128 * t + 8 * k, smem_operand(base + Gm::OFF_V + st * Gm::TILE + k * 2048, Gm::HALF),
-                   shO, add || k != 0);
-        };
-        wait_phase(bar(E4M3 ? Q_READY : Q_FULL), 0, a.err, dead);
-        wait_phase(bar(E4M3 ? K_READY : K_FULL), 0, a.err, dead);
-        tm_fence_after();
-        product_s(0, 0);
-        if (two) product_s(1, 0);
-        mma_commit(bar(K_EMPTY));
-        for (int j = 0; j < nblk; ++j) {
-          const int st = j & 1, nx = (j + 1) & 1;
-          wait_phase(bar(V_READY + st), (j >> 1) & 1, a.err, dead);
-          wait_phase(bar(P_FULL), j & 1, a.err, dead);
-          tm_fence_after();
-          product_o(0, st, j > 0);
-          if (j + 1 < nblk) {
-            wait_phase(bar((E4M3 ? K_READY : K_FULL) + nx), ((j + 1) >> 1) & 1, a.err, dead);
+        unsigned np = 0, kn = 0, vn = 0;               // pieces, blocks of K and V so far
+        unsigned done0 = 0, done1 = 0, used0 = 0, used1 = 0;   // jobs and pieces of each tile so far
+        while (uniform(walk.next(a, sh, p))) {
+          const int nblk = (int)uniform((unsigned)p.nblk);
+          if (nblk == 0) continue;
+          const bool two = uniform(p.two) != 0;
+          const int jobs = two ? 2 * nblk : nblk;
+          wait_phase(bar(E4M3 ? Q_READY : Q_FULL), np & 1, a.err, dead);
+          // S with block kn of all, for tile t; between the two halves of the
+          // products `ask` looks whether what comes next is ready.  Each
+          // question takes some 50 cycles, which the products still in the
+          // queue cover there and nothing covers between two jobs.
+          auto product_s = [&](auto tile, bool ready, auto ask) {
+            constexpr int t = decltype(tile)::value;
+            const int st = kn & 1;
+            const bool first = !two || t == 0, last = !two || t == 1;   // use of this block of K
+            if (first && !ready) wait_phase(bar((E4M3 ? K_READY : K_FULL) + st), (kn >> 1) & 1, a.err, dead);
             tm_fence_after();
-            product_s(0, nx);
-          }
-          if (two) {
-            wait_phase(bar(P_FULL + 1), j & 1, a.err, dead);
+            const SmemOperand q(base + (two && t ? Gm::TILE : 0), 16), kk(base + Gm::OFF_K + st * Gm::TILE, 16);
+            if (elect_one()) {
+#pragma unroll
+              for (int i = 0; i < D / 32; ++i) mma_ss(tmS + 128 * t, q.at(i * 32), kk.at(i * 32), shS, i != 0);
+            }
+            __syncwarp();
+            kn += last;
+            ask();
+            if (elect_one()) {
+#pragma unroll
+              for (int i = D / 32; i < D / 16; ++i) {
+                const uint32_t o = (uint32_t)((i >> 2) * Gm::HALF + (i & 3) * 32);
+                mma_ss(tmS + 128 * t, q.at(o), kk.at(o), shS, 1);
+              }
+              mma_commit(bar(S_FULL + t));
+              if (last) mma_commit(bar(K_EMPTY + st));
+            }
+            __syncwarp();
+          };
+          bool v_ok = false, p_ok = false, k_ok = false;   // of the next job: V, P and its next K are there
+          // O += P V of job k, of tile t = k & 1, then S of job k + 2
+          auto job = [&](auto tile, int k, unsigned& done, unsigned& used, unsigned& next_done) {
+            constexpr int t = decltype(tile)::value;
+            const int st = vn & 1;
+            const bool first = !two || t == 0, last = !two || t == 1;
+            if (first && !v_ok) wait_phase(bar(V_READY + st), (vn >> 1) & 1, a.err, dead);
+            if (k < 2) {                               // the previous piece's sums have been read
+              if (used > 0) wait_phase(bar(O_FREE + t), (used - 1) & 1, a.err, dead);
+              ++used;
+            }
+            if (!p_ok) wait_phase(bar(P_FULL + t), done & 1, a.err, dead);
+            ++done;
             tm_fence_after();
-            product_o(1, st, j > 0);
+            const SmemOperand v(base + Gm::OFF_V + st * Gm::TILE, Gm::HALF);
+            if (elect_one()) {
+#pragma unroll
+              for (int i = 0; i < BKEYS / 16; ++i)
+                mma_ts(tmO + 128 * t, tmS + 128 * t + 8 * i, v.at(i * 2048), shO, k > 1 || i != 0);
+              if (last) mma_commit(bar(V_EMPTY + st));
+              if (k + 1 == jobs) mma_commit(bar(O_DONE));
+            }
+            __syncwarp();
+            vn += last;
+            const bool ready = k_ok;
+            if (k + 2 < jobs) {
+              product_s(tile, ready, [&] {
+                if (last) {
+                  v_ok = test_phase(bar(V_READY + (vn & 1)), (vn >> 1) & 1);
+                  k_ok = test_phase(bar((E4M3 ? K_READY : K_FULL) + (kn & 1)), (kn >> 1) & 1);
+                }
+              });
+            } else {
+              v_ok = k_ok = false;
+            }
+            p_ok = test_phase(bar(P_FULL + 1 - t), next_done & 1);
+          };
+          const std::integral_constant<int, 0> t0;
+          const std::integral_constant<int, 1> t1;
+          const auto nothing = [] {};
+          product_s(t0, false, nothing);
+          if (jobs > 1) product_s(t1, false, nothing);
+          for (int k = 0; k < jobs; k += 2) {
+            job(t0, k, done0, used0, done1);
+            if (k + 1 < jobs) job(t1, k + 1, done1, used1, done0);
           }
-          mma_commit(bar(V_EMPTY + st));
-          if (j + 1 < nblk) {
-            if (two) product_s(1, nx);
-            mma_commit(bar(K_EMPTY + nx));
+          ++np;
+          if (sh.split && !p.whole && p.last && lane == 0) {        // the merge of this item finds its pieces here
+            int c = (int)(p.pos * sh.P / sh.T);        // the CTA whose share holds the item's first block
+            while (c + 1 < sh.P && share_begin(sh.T, c + 1, sh.P) <= p.pos) ++c;
+            ChunkShare r;
+            r.b = p.b;
+            r.kvh = p.kvh;
+            r.tile = p.tile;
+            r.first = c;
+            r.slot = share_begin(sh.T, c, sh.P) == p.pos ? 0 : 1;
+            r.count = (int)blockIdx.x - c + 1;
+            a.share[blockIdx.x] = r;
           }
         }
-        mma_commit(bar(O_DONE));
-        wait_phase(bar(O_DONE), 0, a.err, dead);     // nothing of it is in flight when the CTA ends
+        if (np > 0) wait_phase(bar(O_DONE), (np - 1) & 1, a.err, dead);   // nothing is in flight when the CTA ends
       }
       __syncwarp();
     } else if (warp == 9) {
@@ -249,246 +524,313 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       const int rows = min(1 << a.page_shift, BKEYS);      // rows per box
       const int boxes = BKEYS / rows;
       constexpr int ROWB = E4M3 ? D : 2 * D;
-      if (nblk > 0) {
-        if (lane == 0) {
-          prefetch_tensormap(&tmK);
-          prefetch_tensormap(&tmV);
-          // the last token's box may reach past q, where it reads zeros
-          mbar_expect_tx(bar(Q_FULL), (unsigned)((two ? 2 : 1) * per * a.G * 2 * D));
-          for (int t = 0; t < (two ? 2 : 1); ++t)
-            for (int h = 0; h < D / 64; ++h)
-              tma_load_hint(base + t * Gm::TILE + h * Gm::HALF, &tmQ, 64 * h, kvh * a.G, (int)(s.q0 + tok0 + t * per),
-                            bar(Q_FULL));
-        }
-        const int32_t* const table = a.table + (long long)b * a.max_pages;
-        int next = 0;
-        auto page_of = [&](int j) {   // lane l: page of box l of block j (-1: no key there)
-          const int key = (blk0 + j) * BKEYS + lane * rows;
-          return j < nblk && lane < boxes && key < s.kv ? table[key >> a.page_shift] : INT32_MIN;
+      unsigned np = 0, n = 0;
+      while (walk.next(a, sh, p)) {
+        if (p.nblk == 0) continue;
+        const int32_t* const table = a.table + (long long)p.b * a.max_pages;
+        auto page_of = [&](int j) {   // lane l: page of box l of block j (INT32_MIN: no key there)
+          const int key = (p.blk0 + j) * BKEYS + lane * rows;
+          return j < p.nblk && lane < boxes && key < p.s.kv ? table[key >> a.page_shift] : INT32_MIN;
         };
-        next = page_of(0);
-        for (int j = 0; j < nblk; ++j) {
-          const int pid = next, st = j & 1;
+        int next = page_of(0);
+        for (int j = 0; j < p.nblk; ++j, ++n) {
+          const int pid = next, st = n & 1;
           next = page_of(j + 1);
-          const int key0 = (blk0 + j) * BKEYS;
+          const int key0 = (p.blk0 + j) * BKEYS;
           const bool ok = pid != INT32_MIN && (unsigned)pid < (unsigned)a.n_pages;
           if (pid != INT32_MIN && !ok) {
-            s_bad = 1;
+            s_bad[np & 3] = np + 1;
             flag_error(a.err, ERR_PAGE);
           }
           const unsigned bytes = (unsigned)__popc(__ballot_sync(FULL, ok)) * (unsigned)(rows * ROWB);
           const int row = ok ? (pid << a.page_shift) + ((key0 + lane * rows) & ((1 << a.page_shift) - 1)) : 0;
-          if (j > 1) wait_phase(bar(K_EMPTY + st), ((j >> 1) - 1) & 1, a.err, dead);
+          if (n > 1) wait_phase(bar(K_EMPTY + st), ((n >> 1) - 1) & 1, a.err, dead);
           const uint32_t kd = base + Gm::OFF_K + st * Gm::TILE, vd = base + Gm::OFF_V + st * Gm::TILE;
           if (lane == 0) mbar_expect_tx(bar(K_FULL + st), bytes);
           __syncwarp();
           if (ok) {
             if (E4M3) {
-              tma_load_hint(kd + Gm::TILE / 2 + lane * rows * D, &tmK, 0, kvh, row, bar(K_FULL + st));
+              tma_load_hint(kd + Gm::TILE / 2 + lane * rows * D, &tmK, 0, p.kvh, row, bar(K_FULL + st));
             } else {
 #pragma unroll
               for (int h = 0; h < D / 64; ++h)
-                tma_load_hint(kd + h * Gm::HALF + lane * rows * 128, &tmK, 64 * h, kvh, row, bar(K_FULL + st));
+                tma_load_hint(kd + h * Gm::HALF + lane * rows * 128, &tmK, 64 * h, p.kvh, row, bar(K_FULL + st));
             }
           }
-          if (j > 1) wait_phase(bar(V_EMPTY + st), ((j >> 1) - 1) & 1, a.err, dead);
+          if (j == 0) {
+            // Q, once the previous piece's products are over; the last
+            // token's box may reach past q, where it reads zeros
+            if (np > 0) wait_phase(bar(O_DONE), (np - 1) & 1, a.err, dead);
+            if (E4M3 && np > 0) wait_phase(bar(Q_SEEN), (np - 1) & 1, a.err, dead);
+            if (lane == 0) {
+              mbar_expect_tx(bar(Q_FULL), (unsigned)((p.two ? 2 : 1) * per * a.G * 2 * D));
+              for (int t = 0; t < (p.two ? 2 : 1); ++t)
+                for (int h = 0; h < D / 64; ++h)
+                  tma_load_hint(base + t * Gm::TILE + h * Gm::HALF, &tmQ, 64 * h, p.kvh * a.G, (int)(p.s.q0 + p.i0 + t * per),
+                                bar(Q_FULL));
+            }
+            __syncwarp();
+          }
+          if (n > 1) wait_phase(bar(V_EMPTY + st), ((n >> 1) - 1) & 1, a.err, dead);
           if (lane == 0) mbar_expect_tx(bar(V_FULL + st), bytes);
           __syncwarp();
           if (ok) {
             if (E4M3) {
-              tma_load_hint(vd + Gm::TILE / 2 + lane * rows * D, &tmV, 0, kvh, row, bar(V_FULL + st));
+              tma_load_hint(vd + Gm::TILE / 2 + lane * rows * D, &tmV, 0, p.kvh, row, bar(V_FULL + st));
             } else {
 #pragma unroll
               for (int h = 0; h < D / 64; ++h)
-                tma_load_hint(vd + h * Gm::HALF + lane * rows * 128, &tmV, 64 * h, kvh, row, bar(V_FULL + st));
+                tma_load_hint(vd + h * Gm::HALF + lane * rows * 128, &tmV, 64 * h, p.kvh, row, bar(V_FULL + st));
             }
           }
         }
-        // the copies are over before the CTA ends, also where a wait ran out
-        for (int j = max(0, nblk - 2); j < nblk; ++j) {
-          wait_phase(bar(K_FULL + (j & 1)), (j >> 1) & 1, a.err, dead);
-          wait_phase(bar(V_FULL + (j & 1)), (j >> 1) & 1, a.err, dead);
-        }
-        if (*dead)
-          for (int i = 0; i < 1000; ++i) __nanosleep(1000);
+        ++np;
       }
+      // the copies are over before the CTA ends, also where a wait ran out
+      for (unsigned i = n > 2 ? n - 2 : 0; i < n; ++i) {
+        wait_phase(bar(K_FULL + (i & 1)), (i >> 1) & 1, a.err, dead);
+        wait_phase(bar(V_FULL + (i & 1)), (i >> 1) & 1, a.err, dead);
+      }
+      if (*dead)
+        for (int i = 0; i < 1000; ++i) __nanosleep(1000);
     } else if (!E4M3 && warp < 12) {
       // ------------------------------------- V: rows past the end, odd values
-      int lo0, hi0, lo1, hi1;
-      visible_keys(a, s.kv, first_pos + i0, lo0, hi0);
-      visible_keys(a, s.kv, first_pos + i1, lo1, hi1);
-      for (int j = 0; j < nblk; ++j) {
-        const int st = j & 1, key0 = (blk0 + j) * BKEYS, live = min(BKEYS, s.kv - key0);
-        wait_phase(bar(V_FULL + st), (j >> 1) & 1, a.err, dead);
-        if (key0 < lo1 || key0 + BKEYS > hi0) {
-          const uint32_t vd = base + Gm::OFF_V + st * Gm::TILE;
-          bool found = false;
-          for (int i = tid - 320; i < Gm::TILE / 16; i += 64) {
-            const int r = (i >> 3) & (TROWS - 1);   // chunk i of the tile lies in row r of its half
-            if (r >= live) {
-              sts128(vd + i * 16, make_uint4(0u, 0u, 0u, 0u));
-            } else {
-              uint4 v = lds128(vd + i * 16);
-              if (odd16<T>(v)) {
-                v = make_uint4(without_odd16<T>(v.x), without_odd16<T>(v.y), without_odd16<T>(v.z), without_odd16<T>(v.w));
-                sts128(vd + i * 16, v);
-                found = true;
+      unsigned np = 0, n = 0;
+      while (walk.next(a, sh, p)) {
+        if (p.nblk == 0) continue;
+        int lo0, hi0, lo1, hi1;
+        visible_keys(a, p.s.kv, p.s.kv - p.s.n + p.i0, lo0, hi0);
+        visible_keys(a, p.s.kv, p.s.kv - p.s.n + p.i1, lo1, hi1);
+        for (int j = 0; j < p.nblk; ++j, ++n) {
+          const int st = n & 1, key0 = (p.blk0 + j) * BKEYS, live = min(BKEYS, p.s.kv - key0);
+          wait_phase(bar(V_FULL + st), (n >> 1) & 1, a.err, dead);
+          if (key0 < lo1 || key0 + BKEYS > hi0) {
+            const uint32_t vd = base + Gm::OFF_V + st * Gm::TILE;
+            bool found = false;
+            for (int i = tid - 320; i < Gm::TILE / 16; i += 64) {
+              const int r = (i >> 3) & (TROWS - 1);   // chunk i of the tile lies in row r of its half
+              if (r >= live) {
+                sts128(vd + i * 16, make_uint4(0u, 0u, 0u, 0u));
+              } else {
+                uint4 v = lds128(vd + i * 16);
+                if (odd16<T>(v)) {
+                  v = make_uint4(without_odd16<T>(v.x), without_odd16<T>(v.y), without_odd16<T>(v.z), without_odd16<T>(v.w));
+                  sts128(vd + i * 16, v);
+                  found = true;
+                }
               }
             }
+            if (found) s_odd[np & 3] = np + 1;
+            fence_proxy_async_smem();
           }
-          if (found) s_odd = 1;
-          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(V_READY + st));
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(V_READY + st));
+        ++np;
       }
     } else if (E4M3 && warp >= 12) {
       // ------------------------------------------------- e4m3 codes to fp16
       const int ct = tid - 384;                       // 0 .. 127
       constexpr int CPR = D / 16, PASS = BKEYS * CPR / 128;   // 16-byte chunks of a row; chunks per thread
-      const int32_t* const table = a.table + (long long)b * a.max_pages;
-      for (int i = 0; i < 2 * nblk; ++i) {
-        const int j = i >> 1, st = j & 1, key0 = (blk0 + j) * BKEYS, live = min(BKEYS, s.kv - key0);
-        const bool is_v = i & 1;
-        if (!is_v) {   // this thread's key's scales, on their way while the codes arrive
-          const int key = key0 + ct;
-          float ksc = 0.f, vsc = 1.f;
-          if (ct < live) {
-            const int pid = table[key >> a.page_shift];
-            if ((unsigned)pid < (unsigned)a.n_pages) {
-              const long long at = ((((long long)pid * a.Hkv) + kvh) << a.page_shift) + (key & ((1 << a.page_shift) - 1));
-              ksc = __ldg(a.ks + at);
-              vsc = __ldg(a.vs + at);
-            }
-          }
-          if (!(vsc <= 3.402823466e38f)) {   // the values are NaN, the softmax is not: given back at the end
-            s_odd = 1;
-            vsc = 1.f;
-          }
-          float lv, rv;
-          asm("lg2.approx.f32 %0, %1;" : "=f"(lv) : "f"(vsc));
-          asm("rcp.approx.f32 %0, %1;" : "=f"(rv) : "f"(vsc));
-          const uint32_t sc = base + Gm::OFF_SC + (j & 3) * Gm::SC_STAGE + ct * 4;
-          asm volatile("st.shared.f32 [%0], %1;" ::"r"(sc), "f"(ksc) : "memory");
-          asm volatile("st.shared.f32 [%0], %1;" ::"r"(sc + BKEYS * 4), "f"(lv) : "memory");
-          asm volatile("st.shared.f32 [%0], %1;" ::"r"(sc + 2 * BKEYS * 4), "f"(rv) : "memory");
-        }
-        const uint32_t dst = base + (is_v ? Gm::OFF_V : Gm::OFF_K) + st * Gm::TILE, src = dst + Gm::TILE / 2;
-        wait_phase(bar((is_v ? V_FULL : K_FULL) + st), (j >> 1) & 1, a.err, dead);
-        uint4 w[PASS];
-#pragma unroll
-        for (int p = 0; p < PASS; ++p) w[p] = lds128(src + (ct + 128 * p) * 16);
-        group_sync(1, 128);
-#pragma unroll
-        for (int p = 0; p < PASS; ++p) {
-          const int c = (ct + 128 * p) % CPR, r = (ct + 128 * p) / CPR;
-          uint32_t word[4] = {w[p].x, w[p].y, w[p].z, w[p].w}, h[8];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            if (r >= live) word[e] = 0u;
-            if (is_v) {
-              const uint32_t nan = ((word[e] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
-              if (nan) {   // NaN codes come back at the end, too
-                s_odd = 1;
-                word[e] &= ~((nan >> 7) * 0xffu);
+      unsigned np = 0, n = 0;
+      while (walk.next(a, sh, p)) {
+        if (p.nblk == 0) continue;
+        const int32_t* const table = a.table + (long long)p.b * a.max_pages;
+        for (int i = 0; i < 2 * p.nblk; ++i) {
+          const bool is_v = i & 1;
+          const int st = n & 1, key0 = (p.blk0 + (i >> 1)) * BKEYS, live = min(BKEYS, p.s.kv - key0);
+          if (!is_v) {   // this thread's key's scales, on their way while the codes arrive
+            const int key = key0 + ct;
+            float ksc = 0.f, vsc = 1.f;
+            if (ct < live) {
+              const int pid = table[key >> a.page_shift];
+              if ((unsigned)pid < (unsigned)a.n_pages) {
+                const long long at = ((((long long)pid * a.Hkv) + p.kvh) << a.page_shift) + (key & ((1 << a.page_shift) - 1));
+                ksc = __ldg(a.ks + at);
+                vsc = __ldg(a.vs + at);
               }
             }
-            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h[2 * e]) : "h"((uint16_t)word[e]));
-            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h[2 * e + 1]) : "h"((uint16_t)(word[e] >> 16)));
+            if (!(vsc <= 3.402823466e38f)) {   // the values are NaN, the softmax is not: given back at the end
+              s_odd[np & 3] = np + 1;
+              vsc = 1.f;
+            }
+            float lv, rv;
+            asm("lg2.approx.f32 %0, %1;" : "=f"(lv) : "f"(vsc));
+            asm("rcp.approx.f32 %0, %1;" : "=f"(rv) : "f"(vsc));
+            const uint32_t sc = base + Gm::OFF_SC + (n & 3) * Gm::SC_STAGE + ct * 4;
+            asm volatile("st.shared.f32 [%0], %1;" ::"r"(sc), "f"(ksc) : "memory");
+            asm volatile("st.shared.f32 [%0], %1;" ::"r"(sc + BKEYS * 4), "f"(lv) : "memory");
+            asm volatile("st.shared.f32 [%0], %1;" ::"r"(sc + 2 * BKEYS * 4), "f"(rv) : "memory");
           }
-          // chunks 2c and 2c + 1 of the row; the upper half's lanes store them
-          // the other way round, off the lower half's banks
-          const uint32_t row = dst + (uint32_t)((c >> 2) * Gm::HALF + r * 128);
-          const int c0 = (2 * c) & 7, swap = (c >> 2) & 1;
-          const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
-          sts128(row + (((c0 + swap) ^ (r & 7)) << 4), swap ? hi : lo);
-          sts128(row + (((c0 + 1 - swap) ^ (r & 7)) << 4), swap ? lo : hi);
+          const uint32_t dst = base + (is_v ? Gm::OFF_V : Gm::OFF_K) + st * Gm::TILE, src = dst + Gm::TILE / 2;
+          wait_phase(bar((is_v ? V_FULL : K_FULL) + st), (n >> 1) & 1, a.err, dead);
+          const int c = ct % CPR, r0 = ct / CPR;      // this thread's chunk of rows r0, r0 + 128 / CPR, ...
+          // chunks 2c and 2c + 1 of a row's 16-bit elements; rows of a thread are 0 modulo 8 apart
+          const uint32_t row = dst + (uint32_t)((c >> 2) * Gm::HALF + r0 * 128);
+          const uint32_t lo = row + ((((2 * c) & 7) ^ (r0 & 7)) << 4), hi = row + ((((2 * c + 1) & 7) ^ (r0 & 7)) << 4);
+          // Four chunks at a time.  With 128 elements a row's codes lie where
+          // its own second half goes, and a row's threads are of one warp;
+          // with 64 all codes are read before any is overwritten.
+#pragma unroll 1
+          for (int q0 = 0; q0 < PASS; q0 += 4) {
+            uint4 w[4];
+            uint32_t nan = 0;   // bit 7 of a byte: some code there is a NaN
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              w[q] = lds128(src + (ct + 128 * (q0 + q)) * 16);
+              nan |= ((w[q].x & 0x7f7f7f7fu) + 0x01010101u) | ((w[q].y & 0x7f7f7f7fu) + 0x01010101u) |
+                     ((w[q].z & 0x7f7f7f7fu) + 0x01010101u) | ((w[q].w & 0x7f7f7f7fu) + 0x01010101u);
+            }
+            if (PASS == 4) group_sync(1, 128);
+            else __syncwarp();
+            if (live < BKEYS) {
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+                if (r0 + (q0 + q) * (128 / CPR) >= live) w[q] = make_uint4(0u, 0u, 0u, 0u);
+            }
+            if (is_v && (nan & 0x80808080u)) {        // NaN codes come back at the end, too
+              auto clean = [](uint32_t x) { return x & ~(((((x & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7) * 0xffu); };
+              s_odd[np & 3] = np + 1;
+#pragma unroll
+              for (int q = 0; q < 4; ++q) w[q] = make_uint4(clean(w[q].x), clean(w[q].y), clean(w[q].z), clean(w[q].w));
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const uint32_t o = (uint32_t)((q0 + q) * (128 / CPR) * 128);
+              sts128(lo + o, make_uint4(widen8(w[q].x), widen8(w[q].x >> 16), widen8(w[q].y), widen8(w[q].y >> 16)));
+              sts128(hi + o, make_uint4(widen8(w[q].z), widen8(w[q].z >> 16), widen8(w[q].w), widen8(w[q].w >> 16)));
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar((is_v ? V_READY : K_READY) + st));
+          n += is_v;
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar((is_v ? V_READY : K_READY) + st));
+        ++np;
       }
     }
   } else {
     // -------------------------------------------------------------- softmax
-    if (E4M3) asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+    if (E4M3) asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
     else asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     const int t = warp >> 2, row = tid & 127;
-    if (t == 0 || two) {
-      const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-      const uint32_t mS = tmS + 128 * t + lanes, mO = tmO + 128 * t + lanes;
-      const int ta = tok0 + t * per, tb = min(ta + per, s.n) - 1;   // the tile's tokens
-      const int tok = min(ta + row / a.G, tb);                      // rows past the last compute it again, for nothing
-      const bool live_row = row < per * a.G && ta + row / a.G <= tb;
-      int lo, hi, lo_last, hi_last, lo_first, hi_first;
-      visible_keys(a, s.kv, first_pos + tok, lo, hi);
-      visible_keys(a, s.kv, first_pos + ta, lo_first, hi_first);
-      visible_keys(a, s.kv, first_pos + tb, lo_last, hi_last);
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t mS = tmS + 128 * t + lanes, mO = tmO + 128 * t + lanes;
+    unsigned np = 0, jobs = 0, n = 0, joined = 0;      // pieces, this tile's jobs, blocks, pieces whose groups were joined
+    int slot = 0;
+    Piece& pc = s_piece[warp];
+    if (lane == 0) s_walk[warp].start(a, sh);
+    for (;;) {
+      int more = 0;
+      if (lane == 0) {
+        Walk w = s_walk[warp];
+        more = w.next(a, sh, pc);
+        s_walk[warp] = w;
+      }
+      more = __shfl_sync(FULL, more, 0);
+      __syncwarp();
+      if (!more) break;
+      const int nblk = pc.nblk, blk0 = pc.blk0;
+      const bool two = pc.two;
+      const int step = two ? 1 : 2;
+      int lo, hi, lo_last, hi_first;                   // keys that the row sees; that every row of the tile sees
+      {
+        const int first_pos = pc.s.kv - pc.s.n;
+        const int ta = pc.i0 + (two ? t * per : 0), tb = min(ta + per, pc.s.n) - 1;   // the tile's tokens
+        int none;
+        visible_keys(a, pc.s.kv, first_pos + min(ta + row / a.G, tb), lo, hi);   // rows past the last compute it again, for nothing
+        visible_keys(a, pc.s.kv, first_pos + ta, none, hi_first);
+        visible_keys(a, pc.s.kv, first_pos + tb, lo_last, none);
+      }
       float sl = a.sl2;
       if (E4M3 && nblk > 0) {
-        // the row of q in fp16 under a power of two (see santa_paged_tokens.cu)
-        wait_phase(bar(Q_FULL), 0, a.err, dead);
-        const uint32_t qr = base + t * Gm::TILE + row * 128;
-        float mx = 0.f;
-#pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
-          const uint4 v = lds128(qr + (c >> 3) * Gm::HALF + (((c & 7) ^ (row & 7)) << 4));
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 f = unpack2h<T>(w[e]);
-            mx = fmaxf(mx, fmaxf(fabsf(f.x), fabsf(f.y)));
-          }
-        }
-        float up = 1.f;
-        const int ex = (int)(__float_as_uint(mx) >> 23);
-        if (ex > 11 && ex < 255) {
-          up = __uint_as_float((uint32_t)(264 - ex) << 23);
-          sl *= __uint_as_float((uint32_t)(ex - 10) << 23);
-        }
-#pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
-          const uint32_t at = qr + (c >> 3) * Gm::HALF + (((c & 7) ^ (row & 7)) << 4);
-          const uint4 v = lds128(at);
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-          uint32_t o[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 f = unpack2h<T>(w[e]);
-            o[e] = pack2h<fp16_t>(f.x * up, f.y * up);
-          }
-          sts128(at, make_uint4(o[0], o[1], o[2], o[3]));
-        }
-        fence_proxy_async_smem();
+        // Group 1 sees every phase of Q_FULL, also of pieces that it has no
+        // part in, and the next Q waits until it has: a wait that skipped a
+        // phase, or fell two behind, would take one phase for another.
+        wait_phase(bar(Q_FULL), np & 1, a.err, dead);
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(Q_READY));
+        if (t == 1 && lane == 0) mbar_arrive(bar(Q_SEEN));
+        if (t == 0 || two) {
+          // the row of q in fp16 under a power of two (see santa_paged_tokens.cu)
+          const uint32_t qr = base + (two ? t * Gm::TILE : 0) + row * 128;
+          float mx = 0.f;
+#pragma unroll 2   // run once per piece: straight-line code that runs once waits for its instructions
+          for (int c = 0; c < D / 8; ++c) {
+            const uint4 v = lds128(qr + (c >> 3) * Gm::HALF + (((c & 7) ^ (row & 7)) << 4));
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float2 f = unpack2h<T>(w[e]);
+              mx = fmaxf(mx, fmaxf(fabsf(f.x), fabsf(f.y)));
+            }
+          }
+          float up = 1.f;
+          const int ex = (int)(__float_as_uint(mx) >> 23);
+          if (ex > 11 && ex < 255) {
+            up = __uint_as_float((uint32_t)(264 - ex) << 23);
+            sl *= __uint_as_float((uint32_t)(ex - 10) << 23);
+          }
+#pragma unroll 2
+          for (int c = 0; c < D / 8; ++c) {
+            const uint32_t at = qr + (c >> 3) * Gm::HALF + (((c & 7) ^ (row & 7)) << 4);
+            const uint4 v = lds128(at);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            uint32_t o[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float2 f = unpack2h<T>(w[e]);
+              o[e] = pack2h<fp16_t>(f.x * up, f.y * up);
+            }
+            sts128(at, make_uint4(o[0], o[1], o[2], o[3]));
+          }
+          if (!two) s_sl[row] = sl;
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(bar(Q_READY));
+            if (!two) mbar_arrive(bar(Q_READY));   // for the other group's warp
+          }
+        } else if (nblk > 1) {
+          wait_phase(bar(Q_READY), np & 1, a.err, dead);
+          sl = s_sl[row];
+        }
       }
-      float m = -INFINITY;          // the maximum that P and O are relative to
-      f2x l2 = pack2(0.f, 0.f);
-      for (int j = 0; j < nblk; ++j) {
+      float m = -INFINITY, l = 0.f;   // the row's maximum that P and O are relative to, and sum
+      const int j_first = two ? 0 : t;
+      f2x l2[E4M3 ? 2 : 4];         // chains of additions: one would take longer than the exponentials
+#pragma unroll
+      for (int e = 0; e < (E4M3 ? 2 : 4); ++e) l2[e] = pack2(0.f, 0.f);
+      for (int j = j_first; j < nblk; j += step, ++jobs) {
         const int key0 = (blk0 + j) * BKEYS;
-        wait_phase(bar(S_FULL + t), j & 1, a.err, dead);
+        wait_phase(bar(S_FULL + t), jobs & 1, a.err, dead);
         tm_fence_after();
         uint32_t sr[BKEYS];
-#pragma unroll
-        for (int c = 0; c < BKEYS; c += 32) tm_ld32(mS + c, sr + c);
-        tm_wait_ld();
         if (E4M3) {
-          const uint32_t sc = base + Gm::OFF_SC + (j & 3) * Gm::SC_STAGE;
+          // a key's three factors from shared memory: 96 loads of 16 bytes per
+          // thread, which take 3000 cycles per block (128 bytes a cycle)
+          const uint32_t sc = base + Gm::OFF_SC + ((n + j) & 3) * Gm::SC_STAGE;
           const f2x sl_2 = pack2(sl, sl);
 #pragma unroll
-          for (int c = 0; c < BKEYS; c += 4) {
-            const uint4 k4 = lds128(sc + c * 4), v4 = lds128(sc + (BKEYS + c) * 4);
-            f2x y0 = mul2(pack2(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), sl_2);
-            f2x y1 = mul2(pack2(__uint_as_float(sr[c + 2]), __uint_as_float(sr[c + 3])), sl_2);
-            y0 = ffma2(y0, pack2(__uint_as_float(k4.x), __uint_as_float(k4.y)), pack2(__uint_as_float(v4.x), __uint_as_float(v4.y)));
-            y1 = ffma2(y1, pack2(__uint_as_float(k4.z), __uint_as_float(k4.w)), pack2(__uint_as_float(v4.z), __uint_as_float(v4.w)));
-            const float2 f0 = unpack2(y0), f1 = unpack2(y1);
-            sr[c] = __float_as_uint(f0.x);
-            sr[c + 1] = __float_as_uint(f0.y);
-            sr[c + 2] = __float_as_uint(f1.x);
-            sr[c + 3] = __float_as_uint(f1.y);
+          for (int c0 = 0; c0 < BKEYS; c0 += 32) {
+            tm_ld32(mS + c0, sr + c0);
+            tm_wait_ld();
+#pragma unroll
+            for (int c = c0; c < c0 + 32; c += 4) {
+              const uint4 k4 = lds128(sc + c * 4), v4 = lds128(sc + (BKEYS + c) * 4);
+              const f2x x0 = mul2(pack2(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), sl_2);
+              const f2x x1 = mul2(pack2(__uint_as_float(sr[c + 2]), __uint_as_float(sr[c + 3])), sl_2);
+              const float2 y0 = unpack2(ffma2(x0, pack2(__uint_as_float(k4.x), __uint_as_float(k4.y)), pack2(__uint_as_float(v4.x), __uint_as_float(v4.y))));
+              const float2 y1 = unpack2(ffma2(x1, pack2(__uint_as_float(k4.z), __uint_as_float(k4.w)), pack2(__uint_as_float(v4.z), __uint_as_float(v4.w))));
+              sr[c] = __float_as_uint(y0.x);
+              sr[c + 1] = __float_as_uint(y0.y);
+              sr[c + 2] = __float_as_uint(y1.x);
+              sr[c + 3] = __float_as_uint(y1.y);
+            }
           }
+        } else {
+#pragma unroll
+          for (int c = 0; c < BKEYS; c += 32) tm_ld32(mS + c, sr + c);
+          tm_wait_ld();
         }
         if (key0 < lo_last || key0 + BKEYS > hi_first) {
           const int c0 = lo - key0, cn = hi - lo;
@@ -502,46 +844,45 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             mx[e] = fmaxf(fmaxf(mx[e], __uint_as_float(sr[c + 2 * e])), __uint_as_float(sr[c + 2 * e + 1]));
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * (E4M3 ? 1.f : sl);
-        const float mn = fmaxf(m, top);
-        if (j == 0) {
+        const float mn = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * (E4M3 ? 1.f : sl));
+        if (j == j_first) {
           m = mn;
         } else if (__any_sync(FULL, mn > m + RESCALE)) {
           const float f = fast_exp2(m - (mn > -INFINITY ? mn : 0.f));
           m = mn;
-          const float2 l = unpack2(l2);
-          l2 = pack2(l.x * f, l.y * f);
+#pragma unroll
+          for (int e = 0; e < (E4M3 ? 2 : 4); ++e) l2[e] = mul2(l2[e], pack2(f, f));
 #pragma unroll 1
-          for (int c = 0; c < D; c += 32) {
-            uint32_t o[32];
-            tm_ld32(mO + c, o);
+          for (int c = 0; c < D; c += 16) {
+            uint32_t o[16];
+            tm_ld16(mO + c, o);
             tm_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-            tm_st32(mO + c, o);
+            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+            tm_st16(mO + c, o);
           }
         }
         const float neg = m > -INFINITY ? -m : 0.f;
         const f2x neg2 = pack2(neg, neg), sl_2 = pack2(sl, sl);
-        const uint32_t sc = base + Gm::OFF_SC + (j & 3) * Gm::SC_STAGE + 2 * BKEYS * 4;
+        const uint32_t sc = base + Gm::OFF_SC + ((n + j) & 3) * Gm::SC_STAGE + 2 * BKEYS * 4;
 #pragma unroll
         for (int c = 0; c < BKEYS; c += 32) {
           uint32_t pk[16];
 #pragma unroll
           for (int e = 0; e < 32; e += 4) {
-            f2x y0 = pack2(__uint_as_float(sr[c + e]), __uint_as_float(sr[c + e + 1]));
-            f2x y1 = pack2(__uint_as_float(sr[c + e + 2]), __uint_as_float(sr[c + e + 3]));
-            y0 = E4M3 ? add2(y0, neg2) : ffma2(y0, sl_2, neg2);
-            y1 = E4M3 ? add2(y1, neg2) : ffma2(y1, sl_2, neg2);
-            const float2 f0 = unpack2(y0), f1 = unpack2(y1);
-            const float p0 = fast_exp2(f0.x), p1 = fast_exp2(f0.y), p2 = fast_exp2(f1.x), p3 = fast_exp2(f1.y);
+            f2x x0 = pack2(__uint_as_float(sr[c + e]), __uint_as_float(sr[c + e + 1]));
+            f2x x1 = pack2(__uint_as_float(sr[c + e + 2]), __uint_as_float(sr[c + e + 3]));
+            const float2 y0 = unpack2(E4M3 ? add2(x0, neg2) : ffma2(x0, sl_2, neg2));
+            const float2 y1 = unpack2(E4M3 ? add2(x1, neg2) : ffma2(x1, sl_2, neg2));
+            const float p0 = fast_exp2(y0.x), p1 = fast_exp2(y0.y), p2 = fast_exp2(y1.x), p3 = fast_exp2(y1.y);
             if (E4M3) {
               const uint4 r4 = lds128(sc + (c + e) * 4);
-              l2 = ffma2(pack2(p0, p1), pack2(__uint_as_float(r4.x), __uint_as_float(r4.y)), l2);
-              l2 = ffma2(pack2(p2, p3), pack2(__uint_as_float(r4.z), __uint_as_float(r4.w)), l2);
+              l2[0] = ffma2(pack2(p0, p1), pack2(__uint_as_float(r4.x), __uint_as_float(r4.y)), l2[0]);
+              l2[1] = ffma2(pack2(p2, p3), pack2(__uint_as_float(r4.z), __uint_as_float(r4.w)), l2[1]);
             } else {
-              l2 = add2(l2, pack2(p0, p1));
-              l2 = add2(l2, pack2(p2, p3));
+              f2x &la = l2[(e >> 1) & 3], &lb = l2[((e >> 1) + 1) & 3];
+              la = add2(la, pack2(p0, p1));
+              lb = add2(lb, pack2(p2, p3));
             }
             pk[e / 2] = pack2h<M16>(p0, p1);
             pk[e / 2 + 1] = pack2h<M16>(p2, p3);
@@ -553,82 +894,137 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(P_FULL + t));
       }
-      // ------------------------------------------------------- the result
-      if (nblk > 0) {
-        wait_phase(bar(O_DONE), 0, a.err, dead);
-        tm_fence_after();
+      {
+        f2x s2 = add2(l2[0], l2[1]);
+        if (!E4M3) s2 = add2(s2, add2(l2[E4M3 ? 0 : 2], l2[E4M3 ? 0 : 3]));
+        const float2 lp = unpack2(s2);
+        l = lp.x + lp.y;
       }
-      const float2 lp = unpack2(l2);
-      const float l = lp.x + lp.y;
-      const bool bad = s_bad != 0, odd = s_odd != 0, empty = bad || l == 0.f;
-      const long long at = (s.q0 + tok) * a.H + (long long)kvh * a.G + row % a.G;
-      const long long part = ((((long long)b * a.tiles + tile) * a.Hkv + kvh) * a.splits + split) * a.rows + t * TROWS + row;
-      const bool whole = tk.splits == 1;
-      const float inv = whole && !empty ? __fdividef(1.f, l) : 1.f;
-#pragma unroll 1
-      for (int c = 0; c < D; c += 32) {
-        uint32_t o[32];
+      // ------------------------------------------------------- the result
+      const bool join = !two && nblk > 1;          // both groups hold sums of these rows
+      const bool mine = t == 0 || two;               // this group writes
+      if (join && t == 1) {
+        s_ml[joined & 1][0][row] = m;
+        s_ml[joined & 1][1][row] = l;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(ML_FULL));
+      }
+      if (mine) {
+        float f0 = 1.f, f1 = 0.f;                      // weights of the two sums
         if (nblk > 0) {
-          tm_ld32(mO + c, o);
-          tm_wait_ld();
-        } else {
-#pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = 0u;
+          wait_phase(bar(O_DONE), np & 1, a.err, dead);
+          tm_fence_after();
         }
-        float f[32];
+        if (join) {
+          wait_phase(bar(ML_FULL), joined & 1, a.err, dead);
+          const float m1 = s_ml[joined & 1][0][row], l1 = s_ml[joined & 1][1][row], mm = fmaxf(m, m1), mu = mm > -INFINITY ? mm : 0.f;
+          f0 = fast_exp2(m - mu);
+          f1 = fast_exp2(m1 - mu);
+          l = l * f0 + l1 * f1;
+          m = mm;
+        }
+        const bool bad = nblk > 0 && s_bad[np & 3] == (int)np + 1, odd = nblk > 0 && s_odd[np & 3] == (int)np + 1;
+        const bool empty = bad || l == 0.f;
+        const int ta = pc.i0 + (two ? t * per : 0), tb = min(ta + per, pc.s.n) - 1, tok = min(ta + row / a.G, tb), kvh = pc.kvh;
+        const bool live_row = row < per * a.G && ta + row / a.G <= tb, whole = pc.whole;
+        const long long at = (pc.s.q0 + tok) * a.H + (long long)kvh * a.G + row % a.G;
+        const long long part = ((long long)blockIdx.x * 2 + slot) * a.rows + (two ? t * TROWS : 0) + row;
+        if (whole && !empty) {
+          const float inv = __fdividef(1.f, l);
+          f0 *= inv;
+          f1 *= inv;
+        }
+        // all of the row's sums at once, so that the next piece's products may
+        // overwrite them while this one is stored; 32 at a time over an e4m3
+        // cache, where registers are fewer
+        constexpr int EC = E4M3 ? 32 : D;
+#pragma unroll 1
+        for (int c0 = 0; c0 < D; c0 += EC) {
+          float f[EC];
 #pragma unroll
-        for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(o[e]) * inv;
-        if (odd && live_row) {
-          // what was taken out of V, to the rows that see its key
-          for (int key = max(lo, blk0 * BKEYS); key < min(hi, (blk0 + nblk) * BKEYS); ++key) {
-            const int pid = a.table[(long long)b * a.max_pages + (key >> a.page_shift)];
-            if ((unsigned)pid >= (unsigned)a.n_pages) continue;
-            const int slot = key & ((1 << a.page_shift) - 1);
-            const long long vr = (((long long)pid << a.page_shift) + slot) * a.Hkv + kvh;
-            if (E4M3) {
-              const float sc = a.vs[((((long long)pid * a.Hkv) + kvh) << a.page_shift) + slot];
-              const unsigned char* v = static_cast<const unsigned char*>(a.V) + vr * D + c;
+          for (int c = 0; c < EC; c += 32) {
+            uint32_t o[32];
+            if (nblk > 0) {
+              tm_ld32(mO + c0 + c, o);
+              tm_wait_ld();
+            }
 #pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (!(sc <= 3.402823466e38f) || (v[e] & 0x7f) == 0x7f) f[e] = __int_as_float(0x7fffffff);
-            } else {
-              const uint32_t* v = reinterpret_cast<const uint32_t*>(static_cast<const T*>(a.V) + vr * D + c);
+            for (int e = 0; e < 32; ++e) f[c + e] = nblk > 0 ? __uint_as_float(o[e]) * f0 : 0.f;
+            if (join) {
+              tm_ld32(mO + 128 + c0 + c, o);
+              tm_wait_ld();
 #pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                const float2 y = unpack2h<T>(v[e]);
-                if (!(fabsf(y.x) <= 3.402823466e38f)) f[2 * e] += y.x;
-                if (!(fabsf(y.y) <= 3.402823466e38f)) f[2 * e + 1] += y.y;
+              for (int e = 0; e < 32; ++e) f[c + e] = fmaf(__uint_as_float(o[e]), f1, f[c + e]);
+            }
+          }
+          if (nblk > 0 && c0 + EC == D) {
+            tm_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(bar(O_FREE + t));
+              if (join) mbar_arrive(bar(O_FREE + 1));
+            }
+          }
+          if (odd && live_row) {
+            // what was taken out of V, to the rows that see its key
+            for (int key = max(lo, blk0 * BKEYS); key < min(hi, (blk0 + nblk) * BKEYS); ++key) {
+              const int pid = a.table[(long long)pc.b * a.max_pages + (key >> a.page_shift)];
+              if ((unsigned)pid >= (unsigned)a.n_pages) continue;
+              const int in_page = key & ((1 << a.page_shift) - 1);
+              const long long vr = (((long long)pid << a.page_shift) + in_page) * a.Hkv + kvh;
+              if (E4M3) {
+                const float sc = a.vs[((((long long)pid * a.Hkv) + kvh) << a.page_shift) + in_page];
+                const unsigned char* v = static_cast<const unsigned char*>(a.V) + vr * D + c0;
+#pragma unroll
+                for (int e = 0; e < EC; ++e)
+                  if (!(sc <= 3.402823466e38f) || (v[e] & 0x7f) == 0x7f) f[e] = __int_as_float(0x7fffffff);
+              } else {
+                const uint32_t* v = reinterpret_cast<const uint32_t*>(static_cast<const T*>(a.V) + vr * D + c0);
+#pragma unroll
+                for (int e = 0; e < EC / 2; ++e) {
+                  const float2 y = unpack2h<T>(v[e]);
+                  if (!(fabsf(y.x) <= 3.402823466e38f)) f[2 * e] += y.x;
+                  if (!(fabsf(y.y) <= 3.402823466e38f)) f[2 * e + 1] += y.y;
+                }
               }
+            }
+          }
+          if (live_row) {
+            // 32 bytes per lane and store: a lane's row is its own, and half
+            // sectors would be written twice
+            if (whole) {
+              T* const dst = static_cast<T*>(a.out) + at * D + c0;
+#pragma unroll
+              for (int c = 0; c < EC; c += 16) {
+                uint32_t w[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) w[e] = empty ? 0u : pack2h<T>(f[c + 2 * e], f[c + 2 * e + 1]);
+                if (a.wide) st_global8(dst + c, w);
+                else {
+                  *reinterpret_cast<uint4*>(dst + c) = make_uint4(w[0], w[1], w[2], w[3]);
+                  *reinterpret_cast<uint4*>(dst + c + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+                }
+              }
+            } else {
+              float* const dst = a.part_o + part * D + c0;
+#pragma unroll
+              for (int c = 0; c < EC; c += 8) st_global8(dst + c, reinterpret_cast<const uint32_t*>(f + c));
             }
           }
         }
         if (live_row) {
-          if (whole) {
-            uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(a.out) + at * D + c);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              uint4 w;
-              w.x = empty ? 0u : pack2h<T>(f[8 * e], f[8 * e + 1]);
-              w.y = empty ? 0u : pack2h<T>(f[8 * e + 2], f[8 * e + 3]);
-              w.z = empty ? 0u : pack2h<T>(f[8 * e + 4], f[8 * e + 5]);
-              w.w = empty ? 0u : pack2h<T>(f[8 * e + 6], f[8 * e + 7]);
-              dst[e] = w;
-            }
-          } else {
-            float4* dst = reinterpret_cast<float4*>(a.part_o + part * D + c);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) dst[e] = make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
+          if (!whole) {
+            a.part_ml[2 * part] = m;
+            a.part_ml[2 * part + 1] = bad ? -1.f : l;
+          } else if (a.lse) {
+            a.lse[at] = empty ? -INFINITY : m * 0.6931471805599453f + __logf(l);
           }
         }
       }
-      if (live_row) {
-        if (!whole) {
-          a.part_ml[2 * part] = m;
-          a.part_ml[2 * part + 1] = bad ? -1.f : l;
-        } else if (a.lse) {
-          a.lse[at] = empty ? -INFINITY : m * 0.6931471805599453f + __logf(l);
-        }
-      }
+      if (nblk > 0) ++np;
+      n += nblk;
+      joined += join;
+      slot = 1;
     }
     tm_fence_before();
   }
@@ -636,6 +1032,83 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
   if (warp == 8) {
     tm_fence_after();
     tm_free(tm, 512);
+  }
+}
+
+// The items that CTAs shared: CTA c of the attention left a note of the one
+// whose last piece it had.  Two rows per warp, 32 per CTA; one pass over the
+// pieces under a running maximum, four of each row requested at a time.
+template <typename T, int D>
+__global__ void __launch_bounds__(512, 2) chunk_merge_kernel(PagedArgs a) {
+  const int lane = threadIdx.x & 31, row0 = blockIdx.y * 32 + (threadIdx.x >> 5) * 2;
+  const int per = TROWS / a.G, sub = row0 / TROWS;
+  wait_for_predecessor();
+  const ChunkShare r = a.share[blockIdx.x];
+  if (r.count == 0 || row0 % TROWS >= per * a.G) return;
+  const Seq s = paged_seq(a, r.b, false);
+  const int tok0 = r.tile * a.tokens + sub * per;
+  if (tok0 + row0 % TROWS / a.G >= s.n) return;
+  constexpr int E = D / 32, U = 4, R = 2;
+  float m[R], l[R], o[R][E];
+  bool bad[R];
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    m[i] = -INFINITY;
+    l[i] = 0.f;
+    bad[i] = false;
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[i][e] = 0.f;
+  }
+  for (int k0 = 0; k0 < r.count; k0 += U) {
+    float2 ml[U][R], y[U][R][E / 2];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (k0 + u >= r.count) continue;
+      const long long at = ((long long)(r.first + k0 + u) * 2 + (k0 + u == 0 ? r.slot : 0)) * a.rows + row0;
+      // a row past the tile's last one reads what its lane computed for nothing, or nobody wrote: it is not stored
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        ml[u][i] = *reinterpret_cast<const float2*>(a.part_ml + 2 * (at + i));
+#pragma unroll
+        for (int e = 0; e < E / 2; ++e) y[u][i][e] = *reinterpret_cast<const float2*>(a.part_o + (at + i) * D + lane * E + 2 * e);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      float mn = m[i];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (k0 + u < r.count) mn = fmaxf(mn, ml[u][i].x);
+      const float mu = mn > -INFINITY ? mn : 0.f, f0 = fast_exp2(m[i] - mu);
+      m[i] = mn;
+      l[i] *= f0;
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[i][e] *= f0;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (k0 + u >= r.count) continue;
+        bad[i] |= ml[u][i].y < 0.f;
+        const float f = fast_exp2(ml[u][i].x - mu);
+        l[i] = fmaf(ml[u][i].y, f, l[i]);
+#pragma unroll
+        for (int e = 0; e < E / 2; ++e) {
+          o[i][2 * e] = fmaf(y[u][i][e].x, f, o[i][2 * e]);
+          o[i][2 * e + 1] = fmaf(y[u][i][e].y, f, o[i][2 * e + 1]);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    const int in_tile = row0 % TROWS + i, tok = tok0 + in_tile / a.G;
+    if (in_tile >= per * a.G || tok >= s.n) continue;
+    const bool empty = bad[i] || l[i] == 0.f;
+    const float inv = empty ? 0.f : __fdividef(1.f, l[i]);
+    const long long at = (s.q0 + tok) * a.H + (long long)r.kvh * a.G + in_tile % a.G;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<T*>(a.out) + at * D + lane * E);
+#pragma unroll
+    for (int e = 0; e < E; e += 2) dst[e / 2] = empty ? 0u : pack2h<T>(o[i][e] * inv, o[i][e + 1] * inv);
+    if (a.lse && lane == 0) a.lse[at] = empty ? -INFINITY : m[i] * 0.6931471805599453f + __logf(l[i]);
   }
 }
 
@@ -664,6 +1137,13 @@ bool encode(CUtensorMap* tm, const void* base, int es, int d, int heads, long lo
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Most blocks of keys of one item.
+int chunk_blocks(const PagedArgs& a) {
+  const int span = a.window ? (int)std::min<long long>(a.nk, (long long)a.window + a.tokens) : a.nk;
+  return (span + BKEYS - 1) / BKEYS + (a.window ? 1 : 0);
+}
+bool chunk_may_share(const PagedArgs& a) { return chunk_blocks(a) > CHUNK_LEAST; }
+
 template <typename T, bool E4M3, int D>
 cudaError_t chunk_inst(const PagedArgs& a) {
   using Gm = ChunkGeom<E4M3, D>;
@@ -681,8 +1161,20 @@ cudaError_t chunk_inst(const PagedArgs& a) {
   if (!encode(&tq, a.q, 2, D, a.H, a.total_q, 64, a.G, TROWS / a.G) || !encode(&tk, a.K, es, D, a.Hkv, pool, bx, 1, rows) ||
       !encode(&tv, a.V, es, D, a.Hkv, pool, bx, 1, rows))
     return cudaErrorInvalidValue;
-  kern<<<(unsigned)((long long)a.B * a.Hkv * a.splits * a.tiles), Gm::THREADS, Gm::SMEM, a.stream>>>(tq, tk, tv, a);
-  return cudaGetLastError();
+  kern<<<(unsigned)a.splits, Gm::THREADS, Gm::SMEM, a.stream>>>(tq, tk, tv, a);
+  const cudaError_t launched = cudaGetLastError();
+  if (launched != cudaSuccess || !chunk_may_share(a)) return launched;
+  // the merge waits for the kernel's end (programmatic dependent launch: its own start overlaps it)
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)a.splits, a.rows / 32);
+  cfg.blockDim = dim3(512);
+  cfg.stream = a.stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, chunk_merge_kernel<T, D>, a);
 }
 template <typename T>
 cudaError_t chunk_type(const PagedArgs& a) {
@@ -692,27 +1184,14 @@ cudaError_t chunk_type(const PagedArgs& a) {
 
 }  // namespace
 
-// Splits: the fewest blocks of keys that one SM works through one after
-// another, a CTA's start and end counted as 4 blocks and those of a split,
-// whose sums go through memory, as 12 (128 KiB out and in again).
-void plan_paged_chunk(PagedArgs& a) {
-  const int per = TROWS / a.G;
+// One CTA per SM at most (`splits` of them), and two pieces' sums of each: at
+// most its first and its last item are shared.  Returns their number.
+int plan_paged_chunk(PagedArgs& a) {
   a.rows = 2 * TROWS;
-  a.tokens = 2 * per;
+  a.tokens = 2 * (TROWS / a.G);
   a.tiles = (a.max_q + a.tokens - 1) / a.tokens;
-  const long long items = (long long)a.B * a.Hkv * a.tiles;
-  const int span = a.window ? (int)std::min<long long>(a.nk, (long long)a.window + a.tokens) : a.nk;
-  const int blks = (span + BKEYS - 1) / BKEYS + (a.window ? 1 : 0);
-  long long best = -1;
-  for (int n = 1; n <= std::min(blks, 64); ++n) {
-    const int each = (blks + n - 1) / n;
-    const long long waves = (items * n + a.num_sms - 1) / a.num_sms, cost = waves * (each + (n > 1 ? 12 : 4));
-    if (best < 0 || cost < best) {
-      best = cost;
-      a.split_blk = each;
-    }
-  }
-  a.splits = (blks + a.split_blk - 1) / a.split_blk;
+  a.splits = (int)std::min<long long>(a.num_sms, (long long)a.B * a.Hkv * a.tiles * chunk_blocks(a));
+  return chunk_may_share(a) ? 2 * a.splits : 0;
 }
 
 cudaError_t launch_paged_chunk(const PagedArgs& a) {

@@ -128,7 +128,8 @@ __global__ void __launch_bounds__(NT, 2) paged_tokens_kernel(PagedArgs a) {
   int i0, i1;
   tile_tokens(a, s.n, tile, i0, i1);
   const TileKeys tk = tile_keys(a, s, i0, i1, PG_BLK);
-  if (split >= tk.splits) return;
+  const int splits = max(1, (tk.blk + a.split_blk - 1) / a.split_blk);
+  if (split >= splits) return;
   const int blk0 = tk.blk_lo + split * a.split_blk;
   const int nblk = min(a.split_blk, tk.blk - split * a.split_blk);
   const int mine = nblk > warp ? (nblk - warp + NW - 1) / NW : 0;
@@ -478,7 +479,7 @@ __global__ void __launch_bounds__(NT, 2) paged_tokens_kernel(PagedArgs a) {
       o.z = fmaf(y.z, f, o.z);
       o.w = fmaf(y.w, f, o.w);
     }
-    if (tk.splits == 1) {
+    if (splits == 1) {
       const float inv = bad || l == 0.f ? 0.f : __fdividef(1.f, l);
       const int pr = row0 + r;
       const long long at = (s.q0 + pr / a.G) * a.H + (long long)kvh * a.G + pr % a.G;
@@ -497,13 +498,14 @@ __global__ void __launch_bounds__(NT, 2) paged_tokens_kernel(PagedArgs a) {
   }
 }
 
-// One warp per output row of a split tile: its splits' sums weighted by
-// 2^(m - max).  Rows of tiles that were not split are written already.
+// One warp per output row of a split tile: its splits' sums under a running
+// maximum, eight requested at a time.  Rows of tiles that were not split are
+// written already.  What it looks up of the batch is none of the attention
+// kernel's output, and so is read while that still runs.
 template <typename T, int D>
-__global__ void __launch_bounds__(128) paged_merge_kernel(PagedArgs a, int keys) {
+__global__ void __launch_bounds__(128) paged_merge_kernel(PagedArgs a) {
   const int lane = threadIdx.x & 31;
   const long long w = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-  wait_for_predecessor();
   const long long t = w / a.H;
   const int h = (int)(w - t * a.H);
   int b;
@@ -511,44 +513,46 @@ __global__ void __launch_bounds__(128) paged_merge_kernel(PagedArgs a, int keys)
   const Seq s = paged_seq(a, b, false);
   const int i = (int)(t - s.q0), kvh = h / a.G, g = h % a.G;
   if (i >= s.n) return;
-  int tile, r;
-  if (a.tokens) {   // tiles of two halves of 128 rows, whole tokens in each
-    const int per = a.tokens / (a.rows / 128), j = i % a.tokens;
-    tile = i / a.tokens;
-    r = (j / per) * 128 + (j % per) * a.G + g;
-  } else {
-    tile = (i * a.G + g) / a.rows;
-    r = (i * a.G + g) % a.rows;
-  }
+  const int tile = (i * a.G + g) / a.rows, r = (i * a.G + g) % a.rows;
   int i0, i1;
   tile_tokens(a, s.n, tile, i0, i1);
-  const TileKeys tk = tile_keys(a, s, i0, i1, keys);
-  if (tk.splits == 1) return;
+  const int splits = max(1, (tile_keys(a, s, i0, i1, PG_BLK).blk + a.split_blk - 1) / a.split_blk);
+  if (splits == 1) return;
   const long long base = (((long long)b * a.tiles + tile) * a.Hkv + kvh) * a.splits;
-  float m = -INFINITY;
+  constexpr int E = D / 32, U = 8;
+  float m = -INFINITY, l = 0.f, o[E] = {};
   bool bad = false;
-  for (int k = lane; k < tk.splits; k += 32) {
-    const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + 2 * ((base + k) * a.rows + r));
-    bad |= ml.y < 0.f;
-    m = fmaxf(m, ml.x);
-  }
-  bad = __any_sync(FULL, bad);
-  m = warp_max(m);
-  const float mu = m > -INFINITY ? m : 0.f;
-  constexpr int E = D / 32;
-  float o[E] = {}, l = 0.f;
-#pragma unroll 4
-  for (int k = 0; k < tk.splits; ++k) {
-    const long long at = (base + k) * a.rows + r;
-    const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + 2 * at);
-    const float f = fast_exp2(ml.x - mu);
-    l = fmaf(ml.y, f, l);
-    const float* po = a.part_o + at * D + lane * E;
+  wait_for_predecessor();
+  for (int k0 = 0; k0 < splits; k0 += U) {
+    float2 ml[U], y[U][E / 2];
 #pragma unroll
-    for (int e = 0; e < E; e += 2) {
-      const float2 y = *reinterpret_cast<const float2*>(po + e);
-      o[e] = fmaf(y.x, f, o[e]);
-      o[e + 1] = fmaf(y.y, f, o[e + 1]);
+    for (int u = 0; u < U; ++u) {
+      if (k0 + u >= splits) continue;
+      const long long at = (base + k0 + u) * a.rows + r;
+      ml[u] = *reinterpret_cast<const float2*>(a.part_ml + 2 * at);
+#pragma unroll
+      for (int e = 0; e < E / 2; ++e) y[u][e] = *reinterpret_cast<const float2*>(a.part_o + at * D + lane * E + 2 * e);
+    }
+    float mn = m;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (k0 + u < splits) mn = fmaxf(mn, ml[u].x);
+    const float mu = mn > -INFINITY ? mn : 0.f, f0 = fast_exp2(m - mu);
+    m = mn;
+    l *= f0;
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] *= f0;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (k0 + u >= splits) continue;
+      bad |= ml[u].y < 0.f;
+      const float f = fast_exp2(ml[u].x - mu);
+      l = fmaf(ml[u].y, f, l);
+#pragma unroll
+      for (int e = 0; e < E / 2; ++e) {
+        o[2 * e] = fmaf(y[u][e].x, f, o[2 * e]);
+        o[2 * e + 1] = fmaf(y[u][e].y, f, o[2 * e + 1]);
+      }
     }
   }
   const bool empty = bad || l == 0.f;
@@ -585,7 +589,7 @@ cudaError_t tokens_type(const PagedArgs& a) {
 // Splits: enough CTAs for two on every SM.  Sequences differ in length, and a
 // CTA's share is the longest's, so long tiles are cut finer, into up to four
 // CTAs for every place, while a split keeps 1024 keys.
-void plan_paged_tokens(PagedArgs& a) {
+size_t plan_paged_tokens(PagedArgs& a) {
   a.rows = a.max_q * a.G <= 8 ? 8 : 16;
   a.tokens = 0;
   a.tiles = (int)(((long long)a.max_q * a.G + a.rows - 1) / a.rows);
@@ -597,15 +601,13 @@ void plan_paged_tokens(PagedArgs& a) {
   want = std::max(want, std::min<long long>(4 * places / pieces, blks / 64));
   a.split_blk = (int)std::max<long long>(NW, (blks + want - 1) / want);
   a.splits = (blks + a.split_blk - 1) / a.split_blk;
+  return a.splits == 1 ? 0 : (size_t)pieces * a.splits;
 }
 
 cudaError_t launch_paged_tokens(const PagedArgs& a) {
-  return a.dtype == 0 ? tokens_type<bf16_t>(a) : tokens_type<fp16_t>(a);
-}
-
-// After either attention kernel on the same stream, whose end it waits for
-// (programmatic dependent launch: its own start overlaps the kernel's end).
-cudaError_t launch_paged_merge(const PagedArgs& a, int keys) {
+  const cudaError_t e = a.dtype == 0 ? tokens_type<bf16_t>(a) : tokens_type<fp16_t>(a);
+  if (e != cudaSuccess || a.splits == 1) return e;
+  // the merge waits for the kernel's end (programmatic dependent launch: its own start overlaps it)
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((a.total_q * a.H * 32 + 127) / 128));
   cfg.blockDim = dim3(128);
@@ -616,10 +618,10 @@ cudaError_t launch_paged_merge(const PagedArgs& a, int keys) {
   cfg.attrs = at;
   cfg.numAttrs = 1;
   if (a.dtype == 0)
-    return a.D == 128 ? cudaLaunchKernelEx(&cfg, paged_merge_kernel<bf16_t, 128>, a, keys)
-                      : cudaLaunchKernelEx(&cfg, paged_merge_kernel<bf16_t, 64>, a, keys);
-  return a.D == 128 ? cudaLaunchKernelEx(&cfg, paged_merge_kernel<fp16_t, 128>, a, keys)
-                    : cudaLaunchKernelEx(&cfg, paged_merge_kernel<fp16_t, 64>, a, keys);
+    return a.D == 128 ? cudaLaunchKernelEx(&cfg, paged_merge_kernel<bf16_t, 128>, a)
+                      : cudaLaunchKernelEx(&cfg, paged_merge_kernel<bf16_t, 64>, a);
+  return a.D == 128 ? cudaLaunchKernelEx(&cfg, paged_merge_kernel<fp16_t, 128>, a)
+                    : cudaLaunchKernelEx(&cfg, paged_merge_kernel<fp16_t, 64>, a);
 }
 
 }  // namespace santa

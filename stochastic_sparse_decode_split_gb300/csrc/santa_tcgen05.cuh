@@ -34,6 +34,14 @@ __device__ __forceinline__ void tm_ld32(uint32_t addr, uint32_t* r) {
       : "r"(addr)
       : "memory");
 }
+__device__ __forceinline__ void tm_ld16(uint32_t addr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(addr)
+      : "memory");
+}
 __device__ __forceinline__ void tm_st32(uint32_t addr, const uint32_t* r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
@@ -53,19 +61,64 @@ __device__ __forceinline__ void tm_st16(uint32_t addr, const uint32_t* r) {
       : "memory");
 }
 
+// 16 lanes from the address's lane on, 32 columns: register 4 g + i holds, of
+// group g of eight columns, column 2 (l % 4) + (i & 1) of lane l / 4 + 8 (i / 2)
+// (l the thread's number in the warp: four threads share a row's columns).
+__device__ __forceinline__ void tm_ld16x32(uint32_t addr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tm_st16x32(uint32_t addr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+// The same 16 lanes, 16 columns: register 2 g + i goes, of group g of four
+// columns, to column l % 4 of lane l / 4 + 8 i: a pair of the load's columns as one.
+__device__ __forceinline__ void tm_st16x16(uint32_t addr, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(addr), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
 // Operand in shared memory, 128-byte swizzle (the layout TMA writes: rows of
 // 128 bytes, 16-byte chunk c of row r at chunk c ^ (r & 7); groups of eight
 // rows 1024 bytes apart).  Contracted along the row ("K-major"): `lead` is not
 // used.  Contracted across the rows ("MN-major"): `lead` is the distance in
 // bytes between blocks of 64 elements along the row.
-__device__ __forceinline__ uint64_t smem_operand(uint32_t addr, uint32_t lead) {
-  return (uint64_t)((addr & 0x3ffffu) >> 4) | (uint64_t)(lead >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
-         (uint64_t)1 << 46 | (uint64_t)2 << 61;
-}
+// Offsets are added to the low word of a descriptor made once: recomputed per
+// product they cost 18 of its 58 cycles of issue.
+struct SmemOperand {
+  uint32_t lo, hi;
+  __device__ __forceinline__ SmemOperand(uint32_t addr, uint32_t lead)
+      : lo((addr & 0x3ffffu) >> 4 | (lead >> 4) << 16), hi((1024u >> 4) | 1u << 14 | 2u << 29) {}
+  __device__ __forceinline__ uint64_t at(uint32_t bytes) const {   // of the operand `bytes` (a multiple of 16) further on
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo + (bytes >> 4)), "r"(hi));
+    return d;
+  }
+};
 // Products of 128 x 16 by 16 x n: 32-bit sums, 16-bit operands of one type
 // (bf16 or fp16), the second one MN-major where b_mn.
 __host__ __device__ constexpr uint32_t mma_shape(bool bf16, int n, bool b_mn) {
   return 1u << 4 | (bf16 ? 1u << 7 | 1u << 10 : 0u) | (b_mn ? 1u << 16 : 0u) | (uint32_t)(n >> 3) << 17 | (128u >> 4) << 24;
+}
+// True in one lane of the (whole, converged) warp, the same one every time.
+// The issuing warp runs its loop as a whole and branches on this around each
+// run of products: their operands then stay in uniform registers.  Under
+// `lane == 0`, or predicated one by one, eight products took 490 and 650
+// cycles to issue instead of 420, and the issue, not the 64 cycles that a
+// product of 128 x 128 x 16 runs, set the pace.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred P;\n elect.sync _|P, 0xffffffff;\n selp.u32 %0, 1, 0, P;\n}" : "=r"(p));
+  return p != 0;
 }
 // One thread issues; d (+)= a b^T, `add` 0 overwrites.
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t shape, uint32_t add) {
@@ -82,7 +135,7 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
       "r"(a), "l"(b), "r"(shape), "r"(add)
       : "memory");
 }
-// Arrives on `bar` once everything this thread has issued to the tensor core is done.
+// Arrives on `bar` once everything this thread has given to the tensor core is done.
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
