@@ -530,7 +530,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         const int32_t* const table = a.table + (long long)p.b * a.max_pages;
         auto page_of = [&](int j) {   // lane l: page of box l of block j (INT32_MIN: no key there)
           const int key = (p.blk0 + j) * BKEYS + lane * rows;
-          return j < p.nblk && lane < boxes && key < p.s.kv ? table[key >> a.page_shift] : INT32_MIN;
+          return j < p.nblk && lane < boxes && key < p.s.kv ? max(table[key >> a.page_shift], -1) : INT32_MIN;
         };
         int next = page_of(0);
         for (int j = 0; j < p.nblk; ++j, ++n) {
