@@ -92,9 +92,17 @@ santa::PagedArgs args(const santa_paged_t* p) {
   return a;
 }
 
-// Up to 16 query rows per sequence and KV head go to the kernel for few rows,
-// more to the one whose tiles have 128 of them.
-bool few_rows(const santa::PagedArgs& a) { return (int64_t)a.max_q * a.G <= 16; }
+// Which kernel: up to 16 query rows per sequence and KV head the one for few
+// rows; more than that it takes 16 by 16, reading the cache again for each, and
+// starts in 7 us where the kernel for chunks (tiles of 128 rows) takes 13 to
+// 26.  So it also has the calls whose 16-row tiles read at most 2^25 elements
+// of the cache in all.  Measured at that border (8 sequences of 4096 keys, 2 KV
+// heads of 64, 64 rows): 18.3 against 19.2 us, e4m3 21.1 against 23.8; at twice
+// as much (128 rows): 32.6 against 21.6; at half (32 rows): 13.5 against 18.6.
+bool few_rows(const santa::PagedArgs& a) {
+  const int64_t rows = (int64_t)a.max_q * a.G, span = a.window && a.window + a.max_q < a.nk ? a.window + a.max_q : a.nk;
+  return rows <= 16 || (rows + 15) / 16 <= (int64_t(1) << 25) / (2 * span * a.D) / ((int64_t)a.B * a.Hkv);
+}
 
 // The attention's plan, and its workspace: header, the chunk attention's notes
 // of shared items, the pieces' sums.

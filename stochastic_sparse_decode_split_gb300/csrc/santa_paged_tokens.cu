@@ -84,7 +84,9 @@ struct Geom {
   static constexpr int CH = ROWB / 16;                 // its 16-byte chunks
   static constexpr int KB = PG_BLK * ROWB;             // a block of K (or V)
   static constexpr int STAGE = 2 * KB + (E4M3 ? 2 * PG_BLK * 4 : 0);
-  static constexpr int NS = KB >= 4096 ? 3 : KB >= 2048 ? 6 : 10;   // stages per warp: about 96 KiB of ring per CTA
+  // Stages per warp.  16-bit caches: 96 KiB of ring per CTA and two CTAs per
+  // SM; e4m3, where more is computed per byte: 66 KiB and three.
+  static constexpr int NS = KB >= 4096 ? 3 : !E4M3 ? 6 : KB >= 2048 ? 4 : 7;
   static constexpr int RING = NW * NS * STAGE;
   // offset of chunk c of row r in a block: eight rows at one chunk fall on
   // eight bank groups (128-byte lines, chunk index xor line number)
@@ -104,7 +106,7 @@ constexpr size_t smem_bytes() {
 
 // R: query rows per tile (8 or 16).
 template <typename T, bool E4M3, int D, int R>
-__global__ void __launch_bounds__(NT, 2) paged_tokens_kernel(PagedArgs a) {
+__global__ void __launch_bounds__(NT, E4M3 ? 3 : 2) paged_tokens_kernel(PagedArgs a) {
   using Gm = Geom<E4M3, D>;
   using M16 = typename std::conditional<E4M3, fp16_t, T>::type;   // the products' type
   constexpr int NS = Gm::NS, NB = R / 8;
@@ -302,40 +304,55 @@ __global__ void __launch_bounds__(NT, 2) paged_tokens_kernel(PagedArgs a) {
     const bool whole = key0 >= lo_all && key0 + PG_BLK <= hi_all;   // the same in every lane
     float p[NB][2][2];   // [nb][key g8 + 8 j][row hh]
     float alpha[NB][2];
+    auto softmax = [&](auto all) {
+      constexpr bool ALL = decltype(all)::value;   // every row sees every key of the block
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb)
+      for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-      for (int hh = 0; hh < 2; ++hh) {
-        bool vis[2] = {true, true};
-        float sc[2];
+        for (int hh = 0; hh < 2; ++hh) {
+          bool vis[2] = {true, true};
+          float sc[2];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int key = key0 + g8 + 8 * j;
-          vis[j] = whole || (key >= lo_[nb][hh] && key < hi_[nb][hh]);
-          const float v = (acc[nb][0][2 * j + hh] + acc[nb][1][2 * j + hh]) * sl[nb][hh];
-          sc[j] = vis[j] ? (E4M3 ? fmaf(v, ksc[j], lv[j]) : v) : -INFINITY;
+          for (int j = 0; j < 2; ++j) {
+            const int key = key0 + g8 + 8 * j;
+            if (!ALL) vis[j] = key >= lo_[nb][hh] && key < hi_[nb][hh];
+            const float v = (acc[nb][0][2 * j + hh] + acc[nb][1][2 * j + hh]) * sl[nb][hh];
+            sc[j] = E4M3 ? fmaf(v, ksc[j], lv[j]) : v;
+            if (!ALL && !vis[j]) sc[j] = -INFINITY;
+          }
+          float m = fmaxf(sc[0], sc[1]);
+          m = fmaxf(m, __shfl_xor_sync(FULL, m, 4));
+          m = fmaxf(m, __shfl_xor_sync(FULL, m, 8));
+          m = fmaxf(m, __shfl_xor_sync(FULL, m, 16));
+          const float mn = fmaxf(rm[nb][hh], m), mu = mn > -INFINITY ? mn : 0.f;
+          alpha[nb][hh] = fast_exp2(rm[nb][hh] - mu);
+          rm[nb][hh] = mn;
+          float sum = 0.f;
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            p[nb][j][hh] = ALL || vis[j] ? fast_exp2(sc[j] - mu) : 0.f;
+            sum += E4M3 ? (ALL || vis[j] ? p[nb][j][hh] * rv[j] : 0.f) : p[nb][j][hh];
+            if (E4M3 && (ALL || vis[j])) p[nb][j][hh] += vnan[j];
+          }
+          rl[nb][hh] = fmaf(rl[nb][hh], alpha[nb][hh], sum);
         }
-        float m = fmaxf(sc[0], sc[1]);
-        m = fmaxf(m, __shfl_xor_sync(FULL, m, 4));
-        m = fmaxf(m, __shfl_xor_sync(FULL, m, 8));
-        m = fmaxf(m, __shfl_xor_sync(FULL, m, 16));
-        const float mn = fmaxf(rm[nb][hh], m), mu = mn > -INFINITY ? mn : 0.f;
-        alpha[nb][hh] = fast_exp2(rm[nb][hh] - mu);
-        rm[nb][hh] = mn;
-        float sum = 0.f;
+    };
+    if (whole) softmax(std::true_type());
+    else softmax(std::false_type());
+    bool moved = false;   // most blocks leave the maxima where they are
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          p[nb][j][hh] = vis[j] ? fast_exp2(sc[j] - mu) : 0.f;
-          sum += E4M3 ? (vis[j] ? p[nb][j][hh] * rv[j] : 0.f) : p[nb][j][hh];
-          if (E4M3 && vis[j]) p[nb][j][hh] += vnan[j];
-        }
-        rl[nb][hh] = fmaf(rl[nb][hh], alpha[nb][hh], sum);
+    for (int nb = 0; nb < NB; ++nb) moved |= alpha[nb][0] != 1.f || alpha[nb][1] != 1.f;
+    if (__any_sync(FULL, moved)) {
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          oacc[nb][i][hh] *= alpha[nb][hh];
-          oacc[nb][i][2 + hh] *= alpha[nb][hh];
-        }
-      }
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) {
+            oacc[nb][i][hh] *= alpha[nb][hh];
+            oacc[nb][i][2 + hh] *= alpha[nb][hh];
+          }
+    }
     // A masked key's value is multiplied by zero below, which a NaN or an
     // infinity would survive: blocks that not every row sees in full are
     // looked over, and such a block is added up without the tensor cores.
@@ -498,14 +515,16 @@ __global__ void __launch_bounds__(NT, 2) paged_tokens_kernel(PagedArgs a) {
   }
 }
 
-// One warp per output row of a split tile: its splits' sums under a running
-// maximum, eight requested at a time.  Rows of tiles that were not split are
+// One warp per output row of a split tile, or WPR = 4 where there are more than
+// eight splits: their sums under a running maximum, eight requested at a time
+// (76 splits a row: 17 us with one warp).  Rows of tiles that were not split are
 // written already.  What it looks up of the batch is none of the attention
 // kernel's output, and so is read while that still runs.
-template <typename T, int D>
+template <typename T, int D, int WPR>
 __global__ void __launch_bounds__(128) paged_merge_kernel(PagedArgs a) {
-  const int lane = threadIdx.x & 31;
-  const long long w = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+  __shared__ float s_o[WPR][D], s_ml[WPR][2];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = WPR == 1 ? 0 : warp;
+  const long long w = (long long)blockIdx.x * (4 / WPR) + warp / WPR;   // the row
   const long long t = w / a.H;
   const int h = (int)(w - t * a.H);
   int b;
@@ -523,7 +542,7 @@ __global__ void __launch_bounds__(128) paged_merge_kernel(PagedArgs a) {
   float m = -INFINITY, l = 0.f, o[E] = {};
   bool bad = false;
   wait_for_predecessor();
-  for (int k0 = 0; k0 < splits; k0 += U) {
+  for (int k0 = part * U; k0 < splits; k0 += WPR * U) {
     float2 ml[U], y[U][E / 2];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -555,6 +574,33 @@ __global__ void __launch_bounds__(128) paged_merge_kernel(PagedArgs a) {
       }
     }
   }
+  if (WPR > 1) {   // a row's warps: the whole CTA came here
+    if (bad) l = -1.f;
+    if (lane == 0) {
+      s_ml[part][0] = m;
+      s_ml[part][1] = l;
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) s_o[part][lane * E + e] = o[e];
+    __syncthreads();
+    if (part) return;
+    float mn = m;
+#pragma unroll
+    for (int u = 1; u < WPR; ++u) mn = fmaxf(mn, s_ml[u][0]);
+    const float mu = mn > -INFINITY ? mn : 0.f, f0 = fast_exp2(m - mu);
+    m = mn;
+    l = bad ? 0.f : l * f0;
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] *= f0;
+#pragma unroll
+    for (int u = 1; u < WPR; ++u) {
+      const float f = fast_exp2(s_ml[u][0] - mu);
+      bad |= s_ml[u][1] < 0.f;
+      l = fmaf(s_ml[u][1], f, l);
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] = fmaf(s_o[u][lane * E + e], f, o[e]);
+    }
+  }
   const bool empty = bad || l == 0.f;
   const float inv = empty ? 0.f : __fdividef(1.f, l);
   const long long at = t * a.H + h;
@@ -584,6 +630,13 @@ cudaError_t tokens_type(const PagedArgs& a) {
   return a.e4m3 ? tokens_shape<T, true>(a) : tokens_shape<T, false>(a);
 }
 
+template <typename T>
+cudaError_t merge_type(const PagedArgs& a, const cudaLaunchConfig_t& cfg) {
+  if (a.D == 128)
+    return a.splits > 8 ? cudaLaunchKernelEx(&cfg, paged_merge_kernel<T, 128, 4>, a) : cudaLaunchKernelEx(&cfg, paged_merge_kernel<T, 128, 1>, a);
+  return a.splits > 8 ? cudaLaunchKernelEx(&cfg, paged_merge_kernel<T, 64, 4>, a) : cudaLaunchKernelEx(&cfg, paged_merge_kernel<T, 64, 1>, a);
+}
+
 }  // namespace
 
 // Splits: enough CTAs for two on every SM.  Sequences differ in length, and a
@@ -609,7 +662,8 @@ cudaError_t launch_paged_tokens(const PagedArgs& a) {
   if (e != cudaSuccess || a.splits == 1) return e;
   // the merge waits for the kernel's end (programmatic dependent launch: its own start overlaps it)
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((a.total_q * a.H * 32 + 127) / 128));
+  const int per = a.splits > 8 ? 1 : 4;   // rows per CTA
+  cfg.gridDim = dim3((unsigned)((a.total_q * a.H + per - 1) / per));
   cfg.blockDim = dim3(128);
   cfg.stream = a.stream;
   cudaLaunchAttribute at[1];
@@ -617,11 +671,7 @@ cudaError_t launch_paged_tokens(const PagedArgs& a) {
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  if (a.dtype == 0)
-    return a.D == 128 ? cudaLaunchKernelEx(&cfg, paged_merge_kernel<bf16_t, 128>, a)
-                      : cudaLaunchKernelEx(&cfg, paged_merge_kernel<bf16_t, 64>, a);
-  return a.D == 128 ? cudaLaunchKernelEx(&cfg, paged_merge_kernel<fp16_t, 128>, a)
-                    : cudaLaunchKernelEx(&cfg, paged_merge_kernel<fp16_t, 64>, a);
+  return a.dtype == 0 ? merge_type<bf16_t>(a, cfg) : merge_type<fp16_t>(a, cfg);
 }
 
 }  // namespace santa
