@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import struct
 from typing import Optional
 
 import torch
@@ -44,7 +45,7 @@ class PagedParams(ctypes.Structure):
 
 
 class AppendParams(ctypes.Structure):
-    """Mirror of santa_append_t."""
+    """Mirror of santa_append_t (calls pack it with _APPEND, in a quarter of the time)."""
     _fields_ = [
         ("q", ctypes.c_void_p),
         ("k", ctypes.c_void_p),
@@ -63,10 +64,14 @@ class AppendParams(ctypes.Structure):
     ]
 
 
+_APPEND = struct.Struct("@PPPqqqPPPfPqii")   # AppendParams' fields in their order, natively aligned
+_current_device = torch.cuda.current_device
+
+
 def declare(lib) -> None:
     """Argument types of the paged entry points."""
     vp, sz, i64 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int64
-    P, A = ctypes.POINTER(PagedParams), ctypes.POINTER(AppendParams)
+    P, A = ctypes.POINTER(PagedParams), vp   # a packed santa_append_t
     lib.santa_paged_workspace_size.argtypes = [P]
     lib.santa_paged_workspace_size.restype = sz
     lib.santa_kv_append.argtypes = [P, A, vp, vp, vp, vp, vp, sz, vp]
@@ -156,7 +161,9 @@ class PagedStep:
     page_table int32 [B, max_pages], kv_lens int32 [B] (the new tokens among them; None: nk each), q_offsets int64
     [B + 1] (None: max_q new tokens each).  All three are read by the GPU when a call runs and may be changed in place
     between calls; nk and max_q bound what they may hold.  Calls of one step share its workspace: order them on one
-    stream.  ``error()`` reports what the device refused."""
+    stream.  Outputs that a call is not given are the step's own, as ``Decoder``'s: its next such call on that stream
+    overwrites them.  Keep the step while graphs that captured its calls are used.  ``error()`` reports what the device
+    refused."""
 
     def __init__(self, cache: PagedCache, page_table, kv_lens=None, *, n_q_heads: int, dtype=None,
                  nk: Optional[int] = None, max_q: int = 1, total_q: Optional[int] = None, q_offsets=None,
@@ -196,12 +203,14 @@ class PagedStep:
             if n == 0:
                 raise ValueError("invalid paged parameters")
             self.workspace = alloc_workspace(n, self.device)
-        # what every call passes again: the pool (whose tensors the cache keeps) and the workspace
+        # what every call checks and passes again: shapes, the pool (whose tensors the cache keeps), the workspace
+        self._index = self.device.index
+        self._outputs = {}
         self._shape = torch.Size((self.total_q, n_q_heads, cache.head_dim))
         self._kv_shape = torch.Size((self.total_q, cache.n_kv_heads, cache.head_dim))
-        self._pool = tuple(ctypes.c_void_p(None if t is None else t.data_ptr())
-                           for t in (cache.K, cache.V, cache.k_scale, cache.v_scale))
+        self._lse_shape, self._weight_shape = self._shape[:2], self._shape[2:]
         self._kept = (cache.K, cache.V, cache.k_scale, cache.v_scale)
+        self._pool = tuple(ctypes.c_void_p(None if t is None else t.data_ptr()) for t in self._kept)
         self._ws = (ctypes.c_void_p(self.workspace.data_ptr()), ctypes.c_size_t(n))
         lib = library()
         self._append_fn, self._attend_fn, self._read_fn = lib.santa_kv_append, lib.santa_paged_attention, lib.santa_kv_read
@@ -214,85 +223,87 @@ class PagedStep:
 
     def _heads(self, x, shape, name):
         """Token rows of heads: any row stride, each row dense.  Returns the stride in elements."""
-        stride = x.stride()
-        if x.dtype != self.dtype or x.shape != shape or x.device != self.device:
+        row, head, one = x.stride() if x.dim() == 3 else (0, 0, 0)
+        if x.dtype is not self.dtype or x.shape != shape or x.device != self.device:
             raise ValueError(f"{name} must be {self.dtype} {list(shape)} on the cache's device")
-        if stride[2] != 1 or (shape[1] > 1 and stride[1] != shape[2]):
+        if one != 1 or (head != shape[2] and shape[1] > 1):
             raise ValueError(f"the rows of {name} must be dense")
-        return stride[0] if shape[0] > 1 else shape[1] * shape[2]
+        return row if shape[0] > 1 else shape[1] * shape[2]
 
     def _dense(self, x, shape, dtype, name):
-        if x.dtype != dtype or x.shape != shape or x.device != self.device or not x.is_contiguous():
+        if x.dtype is not dtype or x.shape != shape or x.device != self.device or not x.is_contiguous():
             raise ValueError(f"{name} must be contiguous {dtype} {list(shape)} on the cache's device")
-        return x
+        return x.data_ptr()
 
     def _on(self, stream):
         """The raw stream of a call: the given one, or the device's current one."""
-        if torch.cuda.current_device() != self.device.index:
+        if _current_device() != self._index:
             raise ValueError("make the cache's device the current one for its calls")
-        return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(self.device.index)
+        return torch._C._cuda_getCurrentRawStream(self._index) if stream is None else stream.cuda_stream
 
-    def _new(self, shape, dtype, stream):
-        """An output, allocated for the stream that the call runs on."""
-        if stream is None:
-            return torch.empty(shape, dtype=dtype, device=self.device)
-        with torch.cuda.stream(stream):
-            return torch.empty(shape, dtype=dtype, device=self.device)
+    def _own(self, name, raw, shape, dtype, stream):
+        """The step's own output of that name for calls on that stream (making one anew costs as much as a call)."""
+        x = self._outputs.get((name, raw))
+        if x is None or x.shape != shape:
+            with torch.cuda.stream(stream):
+                x = self._outputs[name, raw] = torch.empty(shape, dtype=dtype, device=self.device)
+        return x
 
     @staticmethod
     def _check(status, fn):
-        if status != 0:
+        if status:
             from . import SantaError
             raise SantaError(status, fn)
 
     def append(self, q, k, v, *, rope=None, interleaved: bool = False, q_norm=None, k_norm=None, eps: float = 1e-6,
                q_out=None, stream=None):
         """New tokens into the cache; returns the rotated and normalised queries [total_q, n_q_heads, head_dim] (None
-        with q None).  q, k and v may be slices of one row-major projection.  Token rows past q_offsets[-1] of a new
-        q_out hold whatever the allocation held."""
+        with q None).  q, k and v may be slices of one row-major projection.  Token rows past q_offsets[-1] of q_out
+        are left as they were."""
         raw = self._on(stream)
-        d = self.cache.head_dim
-        a = AppendParams()
-        a.k_stride, a.v_stride = self._heads(k, self._kv_shape, "k"), self._heads(v, self._kv_shape, "v")
-        a.k, a.v = k.data_ptr(), v.data_ptr()
+        k_stride, v_stride = self._heads(k, self._kv_shape, "k"), self._heads(v, self._kv_shape, "v")
+        q_ptr = q_stride = q_out_ptr = qw = kw = rope_ptr = positions = rotated = 0
         if q is not None:
-            a.q_stride, a.q = self._heads(q, self._shape, "q"), q.data_ptr()
-            if q_out is not None:
-                self._dense(q_out, self._shape, self.dtype, "q_out")
+            q_stride, q_ptr = self._heads(q, self._shape, "q"), q.data_ptr()
+            if q_out is None:
+                q_out = self._own("q", raw, self._shape, self.dtype, stream)
+                q_out_ptr = q_out.data_ptr()
             else:
-                q_out = self._new(self._shape, self.dtype, stream)
-            a.q_out = q_out.data_ptr()
+                q_out_ptr = self._dense(q_out, self._shape, self.dtype, "q_out")
         elif q_out is not None or q_norm is not None:
             raise ValueError("q_out and q_norm go with q")
         if q_norm is not None:
-            a.q_norm = self._dense(q_norm, (d,), self.dtype, "q_norm").data_ptr()
+            qw = self._dense(q_norm, self._weight_shape, self.dtype, "q_norm")
         if k_norm is not None:
-            a.k_norm = self._dense(k_norm, (d,), self.dtype, "k_norm").data_ptr()
-        a.eps = eps
+            kw = self._dense(k_norm, self._weight_shape, self.dtype, "k_norm")
         if rope is not None:
             shape = rope.shape
             if len(shape) != 3 or shape[2] != 2:
                 raise ValueError("rope must be [positions, rotated / 2, 2]")
-            a.rope = self._dense(rope, shape, torch.float32, "rope").data_ptr()
-            a.rope_positions, a.rotated, a.interleaved = shape[0], 2 * shape[1], 1 if interleaved else 0
-        self._check(self._append_fn(self._ref, ctypes.byref(a), *self._pool, *self._ws, raw), "santa_kv_append")
+            rope_ptr = self._dense(rope, shape, torch.float32, "rope")
+            positions, rotated = shape[0], 2 * shape[1]
+        a = _APPEND.pack(q_ptr, k.data_ptr(), v.data_ptr(), q_stride, k_stride, v_stride, q_out_ptr, qw, kw, eps, rope_ptr,
+                         positions, rotated, 1 if interleaved and rotated else 0)
+        self._check(self._append_fn(self._ref, a, *self._pool, *self._ws, raw), "santa_kv_append")
         return q_out
 
     def attend(self, q, *, out=None, lse=None, return_lse: bool = False, stream=None):
         """softmax(scale q K^T + mask) V over the pages, [total_q, n_q_heads, head_dim] in q's type; with return_lse
         (or an lse to fill) also the float32 [total_q, n_q_heads] logarithms of the softmax sums."""
         raw = self._on(stream)
-        self._dense(q, self._shape, self.dtype, "q")
+        q_ptr = self._dense(q, self._shape, self.dtype, "q")
         if out is not None:
-            self._dense(out, self._shape, self.dtype, "out")
+            out_ptr = self._dense(out, self._shape, self.dtype, "out")
         else:
-            out = self._new(self._shape, self.dtype, stream)
+            out = self._own("out", raw, self._shape, self.dtype, stream)
+            out_ptr = out.data_ptr()
+        lse_ptr = None
         if lse is not None:
-            self._dense(lse, self._shape[:2], torch.float32, "lse")
+            lse_ptr = self._dense(lse, self._lse_shape, torch.float32, "lse")
         elif return_lse:
-            lse = self._new(self._shape[:2], torch.float32, stream)
-        self._check(self._attend_fn(self._ref, q.data_ptr(), *self._pool, out.data_ptr(),
-                                    None if lse is None else lse.data_ptr(), *self._ws, raw), "santa_paged_attention")
+            lse = self._own("lse", raw, self._lse_shape, torch.float32, stream)
+            lse_ptr = lse.data_ptr()
+        self._check(self._attend_fn(self._ref, q_ptr, *self._pool, out_ptr, lse_ptr, *self._ws, raw), "santa_paged_attention")
         return out if lse is None else (out, lse)
 
     def read(self, kv_offsets=None, rows: Optional[int] = None, *, K_out=None, V_out=None, stream=None):
@@ -300,16 +311,20 @@ class PagedStep:
         sequence b in row kv_offsets[b] + n (int64 [B + 1]; None: b * nk).  Rows that no key falls on keep what they
         held."""
         raw = self._on(stream)
+        off_ptr = None
         if kv_offsets is not None:
-            self._tensor(kv_offsets, torch.int64, "kv_offsets", 1, self.batch + 1)
             if rows is None:
                 raise ValueError("give rows (of the packed arrays) with kv_offsets")
-        rows = int(rows) if rows is not None else self.batch * self.nk
-        shape = (rows, self.cache.n_kv_heads, self.cache.head_dim)
-        K_out = self._dense(K_out, shape, self.dtype, "K_out") if K_out is not None else self._new(shape, self.dtype, stream)
-        V_out = self._dense(V_out, shape, self.dtype, "V_out") if V_out is not None else self._new(shape, self.dtype, stream)
-        self._check(self._read_fn(self._ref, *self._pool, None if kv_offsets is None else kv_offsets.data_ptr(), rows,
-                                  K_out.data_ptr(), V_out.data_ptr(), *self._ws, raw), "santa_kv_read")
+            off_ptr = self._dense(kv_offsets, (self.batch + 1,), torch.int64, "kv_offsets")
+        elif rows is None:
+            rows = self.batch * self.nk
+        shape = (rows, self._kv_shape[1], self._kv_shape[2])
+        if K_out is None:
+            K_out = self._own("K", raw, shape, self.dtype, stream)
+        if V_out is None:
+            V_out = self._own("V", raw, shape, self.dtype, stream)
+        self._check(self._read_fn(self._ref, *self._pool, off_ptr, rows, self._dense(K_out, shape, self.dtype, "K_out"),
+                                  self._dense(V_out, shape, self.dtype, "V_out"), *self._ws, raw), "santa_kv_read")
         return K_out, V_out
 
     def sample(self, q, S: int, kv_offsets, rows: int, *, variant: str = "systematic", seed: int = 0, step: int = 0,

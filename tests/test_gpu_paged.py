@@ -476,3 +476,18 @@ def test_a_cache_past_two_gigabytes_of_elements():
     step.append(None, x, x)
     R, _ = step.read(torch.tensor([0, 400], device="cuda"), 400)
     assert step.error() == 0 and torch.equal(R[300:], x)
+
+
+def test_a_steps_own_outputs_are_per_stream_and_kept():
+    batch = Batch([300, 20], [1, 1], 8, 2, 64, BF16, False, 16, seed=2)
+    step = batch.step()
+    first, lse = step.attend(batch.q, return_lse=True)
+    want, want_lse = first.clone(), lse.clone()
+    assert step.attend(batch.q) is first
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    other = step.attend(batch.q, stream=side)
+    side.synchronize()
+    assert other is not first and torch.equal(other, want)
+    mine = torch.empty_like(want)
+    assert step.attend(batch.q, out=mine) is mine and torch.equal(mine, want) and torch.equal(lse, want_lse)

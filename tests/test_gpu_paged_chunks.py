@@ -24,7 +24,7 @@ def attend(batch, window=0, nk=None, **kw):
     tiles = -(-max(batch.n) * (batch.H // batch.Hkv) // 16)
     assert max(batch.n) * (batch.H // batch.Hkv) > 16 and tiles * batch.B * batch.Hkv * span * 2 * batch.D > 1.2 * 2 ** 25
     step = batch.step(window=window, nk=nk, **kw)
-    out, lse = step.attend(batch.q, return_lse=True)
+    out, lse = (x.clone() for x in step.attend(batch.q, return_lse=True))   # the step's own outputs change with its next call
     return step, out, lse
 
 

@@ -145,3 +145,16 @@ def test_rope_table():
     for bad in ((0, 64), (10, 0), (10, 7)):
         with pytest.raises(ValueError):
             santa.rope_table(*bad, device="cpu")
+
+
+def test_the_packed_append_parameters_are_the_structure():
+    a = paged.AppendParams()
+    values = dict(q=1 << 40, k=2 << 40, v=3 << 40, q_stride=4, k_stride=-5, v_stride=6, q_out=7 << 33, q_norm=8, k_norm=9,
+                  eps=0.125, rope=10, rope_positions=1 << 35, rotated=12, interleaved=1)
+    for k, v in values.items():
+        setattr(a, k, v)
+    packed = paged._APPEND.pack(*values.values())
+    size = ctypes.sizeof(a)
+    assert paged._APPEND.size <= size <= paged._APPEND.size + 7      # the structure's end is padded
+    back = paged.AppendParams.from_buffer_copy(packed + bytes(8))
+    assert all(getattr(back, k) == v for k, v in values.items())
