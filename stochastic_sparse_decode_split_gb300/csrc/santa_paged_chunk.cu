@@ -133,11 +133,6 @@ __device__ __forceinline__ f2x mul2(f2x a, f2x b) {
 __device__ __forceinline__ void sts128(uint32_t addr, uint4 v) {
   asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
-__device__ __forceinline__ float2 lds_f2(uint32_t addr) {
-  float2 f;
-  asm("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(f.x), "=f"(f.y) : "r"(addr));
-  return f;
-}
 // Two e4m3 codes (the low 16 bits) as fp16, exact.
 __device__ __forceinline__ uint32_t widen8(uint32_t two) {
   uint32_t r;
@@ -150,12 +145,17 @@ __device__ __forceinline__ void st_global8(void* p, const uint32_t* w) {
                "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
                : "memory");
 }
-__device__ __forceinline__ void tma_load_hint(uint32_t dst, const CUtensorMap* tm, int x, int y, int z, uint32_t bar) {
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* tm, int x, int y, int z, uint32_t bar) {
   asm volatile(
       "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
           dst),
       "l"((uint64_t)tm), "r"(x), "r"(y), "r"(z), "r"(bar)
       : "memory");
+}
+// The same box into the L2 only.
+__device__ __forceinline__ void tma_prefetch(const CUtensorMap* tm, int x, int y, int z) {
+  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"((uint64_t)tm), "r"(x), "r"(y), "r"(z)
+               : "memory");
 }
 // NaN or infinity among the eight 16-bit elements of a chunk.
 template <typename T>
@@ -427,42 +427,38 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
           const bool two = uniform(p.two) != 0;
           const int jobs = two ? 2 * nblk : nblk;
           wait_phase(bar(E4M3 ? Q_READY : Q_FULL), np & 1, a.err, dead);
-          // S with block kn of all, for tile t; between the two halves of the
-          // products `ask` looks whether what comes next is ready.  Each
-          // question takes some 50 cycles, which the products still in the
-          // queue cover there and nothing covers between two jobs.
-          auto product_s = [&](auto tile, bool ready, auto ask) {
+          // S with block kn of all, for tile t (one lane)
+          auto product_s = [&](auto tile) {
             constexpr int t = decltype(tile)::value;
-            const int st = kn & 1;
-            const bool first = !two || t == 0, last = !two || t == 1;   // use of this block of K
-            if (first && !ready) wait_phase(bar((E4M3 ? K_READY : K_FULL) + st), (kn >> 1) & 1, a.err, dead);
+            const SmemOperand q(base + (two && t ? Gm::TILE : 0), 16), kk(base + Gm::OFF_K + (kn & 1) * Gm::TILE, 16);
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+              const uint32_t o = (uint32_t)((i >> 2) * Gm::HALF + (i & 3) * 32);
+              mma_ss(tmS + 128 * t, q.at(o), kk.at(o), shS, i != 0);
+            }
+            mma_commit(bar(S_FULL + t));
+            if (!two || t == 1) mma_commit(bar(K_EMPTY + (kn & 1)));
+          };
+          auto first_s = [&](auto tile) {
+            constexpr int t = decltype(tile)::value;
+            if (!two || t == 0) wait_phase(bar((E4M3 ? K_READY : K_FULL) + (kn & 1)), (kn >> 1) & 1, a.err, dead);
             tm_fence_after();
-            const SmemOperand q(base + (two && t ? Gm::TILE : 0), 16), kk(base + Gm::OFF_K + st * Gm::TILE, 16);
-            if (elect_one()) {
-#pragma unroll
-              for (int i = 0; i < D / 32; ++i) mma_ss(tmS + 128 * t, q.at(i * 32), kk.at(i * 32), shS, i != 0);
-            }
+            if (elect_one()) product_s(tile);
             __syncwarp();
-            kn += last;
-            ask();
-            if (elect_one()) {
-#pragma unroll
-              for (int i = D / 32; i < D / 16; ++i) {
-                const uint32_t o = (uint32_t)((i >> 2) * Gm::HALF + (i & 3) * 32);
-                mma_ss(tmS + 128 * t, q.at(o), kk.at(o), shS, 1);
-              }
-              mma_commit(bar(S_FULL + t));
-              if (last) mma_commit(bar(K_EMPTY + st));
-            }
-            __syncwarp();
+            kn += !two || t == 1;
           };
           bool v_ok = false, p_ok = false, k_ok = false;   // of the next job: V, P and its next K are there
-          // O += P V of job k, of tile t = k & 1, then S of job k + 2
+          // O += P V of job k, of tile t = k & 1, then S of job k + 2, in one
+          // run of the electing lane; then a look at what the next job waits
+          // for, under the products that are still in the queue.
           auto job = [&](auto tile, int k, unsigned& done, unsigned& used, unsigned& next_done) {
             constexpr int t = decltype(tile)::value;
             const int st = vn & 1;
-            const bool first = !two || t == 0, last = !two || t == 1;
-            if (first && !v_ok) wait_phase(bar(V_READY + st), (vn >> 1) & 1, a.err, dead);
+            const bool first = !two || t == 0, last = !two || t == 1, more = k + 2 < jobs;
+            if (first) {
+              if (!v_ok) wait_phase(bar(V_READY + st), (vn >> 1) & 1, a.err, dead);
+              if (!k_ok && more) wait_phase(bar((E4M3 ? K_READY : K_FULL) + (kn & 1)), (kn >> 1) & 1, a.err, dead);
+            }
             if (k < 2) {                               // the previous piece's sums have been read
               if (used > 0) wait_phase(bar(O_FREE + t), (used - 1) & 1, a.err, dead);
               ++used;
@@ -476,28 +472,22 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
               for (int i = 0; i < BKEYS / 16; ++i)
                 mma_ts(tmO + 128 * t, tmS + 128 * t + 8 * i, v.at(i * 2048), shO, k > 1 || i != 0);
               if (last) mma_commit(bar(V_EMPTY + st));
+              if (more) product_s(tile);
               if (k + 1 == jobs) mma_commit(bar(O_DONE));
             }
             __syncwarp();
             vn += last;
-            const bool ready = k_ok;
-            if (k + 2 < jobs) {
-              product_s(tile, ready, [&] {
-                if (last) {
-                  v_ok = test_phase(bar(V_READY + (vn & 1)), (vn >> 1) & 1);
-                  k_ok = test_phase(bar((E4M3 ? K_READY : K_FULL) + (kn & 1)), (kn >> 1) & 1);
-                }
-              });
-            } else {
-              v_ok = k_ok = false;
-            }
+            kn += last && more;
             p_ok = test_phase(bar(P_FULL + 1 - t), next_done & 1);
+            if (last) {
+              v_ok = test_phase(bar(V_READY + (vn & 1)), (vn >> 1) & 1);
+              k_ok = test_phase(bar((E4M3 ? K_READY : K_FULL) + (kn & 1)), (kn >> 1) & 1);
+            }
           };
           const std::integral_constant<int, 0> t0;
           const std::integral_constant<int, 1> t1;
-          const auto nothing = [] {};
-          product_s(t0, false, nothing);
-          if (jobs > 1) product_s(t1, false, nothing);
+          first_s(t0);
+          if (jobs > 1) first_s(t1);
           for (int k = 0; k < jobs; k += 2) {
             job(t0, k, done0, used0, done1);
             if (k + 1 < jobs) job(t1, k + 1, done1, used1, done0);
@@ -532,29 +522,30 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
           const int key = (p.blk0 + j) * BKEYS + lane * rows;
           return j < p.nblk && lane < boxes && key < p.s.kv ? max(table[key >> a.page_shift], -1) : INT32_MIN;
         };
-        int next = page_of(0);
+        auto row_of = [&](int pid, int j) {   // first row of a lane's box
+          return (pid << a.page_shift) + (((p.blk0 + j) * BKEYS + lane * rows) & ((1 << a.page_shift) - 1));
+        };
+        int pid = page_of(0), pid1 = page_of(1), pid2 = page_of(2);
         for (int j = 0; j < p.nblk; ++j, ++n) {
-          const int pid = next, st = n & 1;
-          next = page_of(j + 1);
-          const int key0 = (p.blk0 + j) * BKEYS;
+          const int st = n & 1;
           const bool ok = pid != INT32_MIN && (unsigned)pid < (unsigned)a.n_pages;
           if (pid != INT32_MIN && !ok) {
             s_bad[np & 3] = np + 1;
             flag_error(a.err, ERR_PAGE);
           }
           const unsigned bytes = (unsigned)__popc(__ballot_sync(FULL, ok)) * (unsigned)(rows * ROWB);
-          const int row = ok ? (pid << a.page_shift) + ((key0 + lane * rows) & ((1 << a.page_shift) - 1)) : 0;
+          const int row = ok ? row_of(pid, j) : 0;
           if (n > 1) wait_phase(bar(K_EMPTY + st), ((n >> 1) - 1) & 1, a.err, dead);
           const uint32_t kd = base + Gm::OFF_K + st * Gm::TILE, vd = base + Gm::OFF_V + st * Gm::TILE;
           if (lane == 0) mbar_expect_tx(bar(K_FULL + st), bytes);
           __syncwarp();
           if (ok) {
             if (E4M3) {
-              tma_load_hint(kd + Gm::TILE / 2 + lane * rows * D, &tmK, 0, p.kvh, row, bar(K_FULL + st));
+              tma_load(kd + Gm::TILE / 2 + lane * rows * D, &tmK, 0, p.kvh, row, bar(K_FULL + st));
             } else {
 #pragma unroll
               for (int h = 0; h < D / 64; ++h)
-                tma_load_hint(kd + h * Gm::HALF + lane * rows * 128, &tmK, 64 * h, p.kvh, row, bar(K_FULL + st));
+                tma_load(kd + h * Gm::HALF + lane * rows * 128, &tmK, 64 * h, p.kvh, row, bar(K_FULL + st));
             }
           }
           if (j == 0) {
@@ -566,7 +557,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
               mbar_expect_tx(bar(Q_FULL), (unsigned)((p.two ? 2 : 1) * per * a.G * 2 * D));
               for (int t = 0; t < (p.two ? 2 : 1); ++t)
                 for (int h = 0; h < D / 64; ++h)
-                  tma_load_hint(base + t * Gm::TILE + h * Gm::HALF, &tmQ, 64 * h, p.kvh * a.G, (int)(p.s.q0 + p.i0 + t * per),
+                  tma_load(base + t * Gm::TILE + h * Gm::HALF, &tmQ, 64 * h, p.kvh * a.G, (int)(p.s.q0 + p.i0 + t * per),
                                 bar(Q_FULL));
             }
             __syncwarp();
@@ -576,13 +567,26 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
           __syncwarp();
           if (ok) {
             if (E4M3) {
-              tma_load_hint(vd + Gm::TILE / 2 + lane * rows * D, &tmV, 0, p.kvh, row, bar(V_FULL + st));
+              tma_load(vd + Gm::TILE / 2 + lane * rows * D, &tmV, 0, p.kvh, row, bar(V_FULL + st));
             } else {
 #pragma unroll
               for (int h = 0; h < D / 64; ++h)
-                tma_load_hint(vd + h * Gm::HALF + lane * rows * 128, &tmV, 64 * h, p.kvh, row, bar(V_FULL + st));
+                tma_load(vd + h * Gm::HALF + lane * rows * 128, &tmV, 64 * h, p.kvh, row, bar(V_FULL + st));
             }
           }
+          // Two stages are less than HBM's latency: what comes two blocks on
+          // is brought into the L2 now.
+          if (pid2 != INT32_MIN && (unsigned)pid2 < (unsigned)a.n_pages) {
+            const int row2 = row_of(pid2, j + 2);
+#pragma unroll
+            for (int h = 0; h < (E4M3 ? 1 : D / 64); ++h) {
+              tma_prefetch(&tmK, 64 * h, p.kvh, row2);
+              tma_prefetch(&tmV, 64 * h, p.kvh, row2);
+            }
+          }
+          pid = pid1;
+          pid1 = pid2;
+          pid2 = page_of(j + 3);
         }
         ++np;
       }

@@ -61,32 +61,6 @@ __device__ __forceinline__ void tm_st16(uint32_t addr, const uint32_t* r) {
       : "memory");
 }
 
-// 16 lanes from the address's lane on, 32 columns: register 4 g + i holds, of
-// group g of eight columns, column 2 (l % 4) + (i & 1) of lane l / 4 + 8 (i / 2)
-// (l the thread's number in the warp: four threads share a row's columns).
-__device__ __forceinline__ void tm_ld16x32(uint32_t addr, uint32_t* r) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(addr)
-      : "memory");
-}
-__device__ __forceinline__ void tm_st16x32(uint32_t addr, const uint32_t* r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
-}
-// The same 16 lanes, 16 columns: register 2 g + i goes, of group g of four
-// columns, to column l % 4 of lane l / 4 + 8 i: a pair of the load's columns as one.
-__device__ __forceinline__ void tm_st16x16(uint32_t addr, const uint32_t* r) {
-  asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(addr), "r"(r[0]), "r"(r[1]),
-               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-               : "memory");
-}
-
 // Operand in shared memory, 128-byte swizzle (the layout TMA writes: rows of
 // 128 bytes, 16-byte chunk c of row r at chunk c ^ (r & 7); groups of eight
 // rows 1024 bytes apart).  Contracted along the row ("K-major"): `lead` is not
