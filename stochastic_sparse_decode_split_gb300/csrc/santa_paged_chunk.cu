@@ -678,20 +678,20 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
 #pragma unroll 1
           for (int q0 = 0; q0 < PASS; q0 += 4) {
             uint4 w[4];
-            uint32_t nan = 0;   // bit 7 of a byte: some code there is a NaN
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              w[q] = lds128(src + (ct + 128 * (q0 + q)) * 16);
-              nan |= ((w[q].x & 0x7f7f7f7fu) + 0x01010101u) | ((w[q].y & 0x7f7f7f7fu) + 0x01010101u) |
-                     ((w[q].z & 0x7f7f7f7fu) + 0x01010101u) | ((w[q].w & 0x7f7f7f7fu) + 0x01010101u);
-            }
+            for (int q = 0; q < 4; ++q) w[q] = lds128(src + (ct + 128 * (q0 + q)) * 16);
             if (PASS == 4) group_sync(1, 128);
             else __syncwarp();
-            if (live < BKEYS) {
+            if (live < BKEYS) {   // past the last key: whatever was there before
 #pragma unroll
               for (int q = 0; q < 4; ++q)
                 if (r0 + (q0 + q) * (128 / CPR) >= live) w[q] = make_uint4(0u, 0u, 0u, 0u);
             }
+            uint32_t nan = 0;     // bit 7 of a byte: some code there is a NaN
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              nan |= ((w[q].x & 0x7f7f7f7fu) + 0x01010101u) | ((w[q].y & 0x7f7f7f7fu) + 0x01010101u) |
+                     ((w[q].z & 0x7f7f7f7fu) + 0x01010101u) | ((w[q].w & 0x7f7f7f7fu) + 0x01010101u);
             if (is_v && (nan & 0x80808080u)) {        // NaN codes come back at the end, too
               auto clean = [](uint32_t x) { return x & ~(((((x & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7) * 0xffu); };
               s_odd[np & 3] = np + 1;
