@@ -281,6 +281,7 @@ santa_status_t santa_get_error(void* workspace, santa_stream_t stream, int32_t* 
  *                                written there, rows read from it come back zero, and the
  *                                attention rows that are computed with it come out zero
  *   SANTA_CACHE_DEVERR_POSITION  a position past the rotation table: the token is skipped
+ *   SANTA_DEVERR_TIMEOUT         a bounded wait inside santa_paged_attention ran out: out is not to be used
  * The three calls share one workspace, cleared once by santa_workspace_init. */
 typedef struct {
   int32_t batch;              /* 1 .. 65535 */
@@ -296,8 +297,8 @@ typedef struct {
   const int32_t* kv_lens;     /* device [batch], the new tokens among them; NULL = nk each */
   int64_t nk;                 /* upper bound on every kv_lens[b], 1 .. SANTA_MAX_NK */
   const int64_t* q_offsets;   /* device [batch + 1], non-decreasing; NULL = b * max_q */
-  int32_t max_q;              /* new tokens per sequence; with q_offsets an upper bound */
-  int64_t total_q;            /* rows of the token arrays, < 2^31; batch * max_q without q_offsets */
+  int32_t max_q;              /* new tokens per sequence; with q_offsets an upper bound (the closer, the fewer idle blocks) */
+  int64_t total_q;            /* rows of the token arrays, total_q * n_q_heads < 2^31; batch * max_q without q_offsets */
   int32_t causal;             /* 1: a token sees the keys up to its own position; 0: all of them */
   int32_t window;             /* > 0 (causal only): of those, the last `window`; 0: no window */
   float scale;                /* score scale; <= 0 selects 1/sqrt(head_dim) */
@@ -307,8 +308,8 @@ typedef struct {
 #define SANTA_CACHE_DEVERR_CHUNK 32
 #define SANTA_CACHE_DEVERR_POSITION 64
 
-/* Byte size of the workspace of the three calls (0 when p is invalid).  The
- * pointers of p are not looked at. */
+/* Byte size of the workspace of the three calls (0 when p is invalid).  Of
+ * p's pointers it only matters whether q_offsets is NULL. */
 size_t santa_paged_workspace_size(const santa_paged_t* p);
 
 /* What santa_kv_append does to the new tokens on their way. */
@@ -339,13 +340,17 @@ santa_status_t santa_kv_append(const santa_paged_t* p, const santa_append_t* a, 
 /* out = softmax(scale q K^T + mask) V over the pages, exact: the new tokens'
  * queries q [total_q, n_q_heads, head_dim] against the keys of their
  * sequences, which the cache already holds.  dtype SANTA_BF16 or SANTA_FP16.
- *   out  [total_q, n_q_heads, head_dim] in dtype
+ *   out  [total_q, n_q_heads, head_dim] in dtype; may be q itself
  *   lse  optional float32 [total_q, n_q_heads]: the natural logarithm of the
  *        sum of exp(scale q k) over the visible keys
  * A token that sees no key (an empty sequence; more new tokens than keys) gets
  * zeros and -infinity.  Scores, the running maximum and sum, and the sum over
  * the values are float32; probabilities enter the second product in 16 bits.
- * What masked keys hold, NaN and infinities included, does not matter. */
+ * What masked keys hold, NaN and infinities included, does not matter.
+ * A v_scale below 2^-60 / 448, the smallest that santa_kv_append writes, is
+ * taken as that; a negative, infinite or NaN one makes its row's values NaN
+ * (and leaves lse alone).  The weight of a key may be lost whose v_scale is
+ * more than 2^100 times smaller than another visible key's. */
 santa_status_t santa_paged_attention(const santa_paged_t* p, const void* q, const void* K, const void* V,
                                      const float* k_scale, const float* v_scale, void* out, float* lse,
                                      void* workspace, size_t ws_bytes, santa_stream_t stream);

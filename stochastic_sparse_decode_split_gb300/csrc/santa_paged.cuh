@@ -16,6 +16,12 @@ constexpr int ERR_PAGE = 16;       // a page-table entry outside the pool
 constexpr int ERR_CHUNK = 32;      // bad q_offsets / kv_offsets, or more new tokens than keys
 constexpr int ERR_POSITION = 64;   // a position past the rotation table
 
+// A v_scale is divided by: one below the smallest that santa_kv_append writes
+// (its floor of the magnitudes, 2^-60, by 448) counts as that; a negative one,
+// a NaN or an infinity makes its row of values NaN.
+constexpr float V_SCALE_LEAST = 8.673617379884035e-19f / 448.f;
+__device__ __forceinline__ bool odd_scale(float v) { return !(v >= 0.f && v <= 3.402823466e38f); }
+
 constexpr int PG_BLK = 16;         // keys per block: no block crosses a page (the smallest page is one block)
 
 // Everything the paged kernels need, validated and carved out of the workspace.

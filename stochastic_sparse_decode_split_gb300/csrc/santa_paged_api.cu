@@ -4,6 +4,7 @@
 #include <math.h>
 #include <string.h>
 
+#include <algorithm>
 #include <atomic>
 
 #include "../../include/santa.h"
@@ -50,8 +51,7 @@ santa_status_t check(const santa_paged_t* p) {
   if (p->n_q_heads / p->n_kv_heads > SANTA_MAX_GROUP) return SANTA_ERR_UNSUPPORTED;
   if ((p->causal != 0 && p->causal != 1) || p->window < 0 || (p->window && !p->causal)) return SANTA_ERR_INVALID_ARG;
   if (!(p->scale == p->scale) || isinf(p->scale)) return SANTA_ERR_INVALID_ARG;
-  // one warp per row group of a token at most, eight of them a CTA; a CTA per block of keys
-  if (p->total_q * (int64_t)(p->n_q_heads + 2 * p->n_kv_heads) > (int64_t)INT32_MAX * 4) return SANTA_ERR_UNSUPPORTED;
+  if (p->total_q * p->n_q_heads > INT32_MAX) return SANTA_ERR_UNSUPPORTED;   // a CTA per output row at most
   return SANTA_OK;
 }
 
@@ -86,7 +86,7 @@ santa::PagedArgs args(const santa_paged_t* p) {
   a.max_q = p->max_q;
   a.total_q = p->total_q;
   a.causal = p->causal;
-  a.window = p->window;
+  a.window = p->window < p->nk ? p->window : 0;   // one that no key is outside of is none
   a.sl2 = (float)((p->scale > 0.f ? (double)p->scale : 1.0 / sqrt((double)p->head_dim)) * 1.4426950408889634);
   a.num_sms = sms();
   return a;
@@ -100,7 +100,7 @@ santa::PagedArgs args(const santa_paged_t* p) {
 // heads of 64, 64 rows): 18.3 against 19.2 us, e4m3 21.1 against 23.8; at twice
 // as much (128 rows): 32.6 against 21.6; at half (32 rows): 13.5 against 18.6.
 bool few_rows(const santa::PagedArgs& a) {
-  const int64_t rows = (int64_t)a.max_q * a.G, span = a.window && a.window + a.max_q < a.nk ? a.window + a.max_q : a.nk;
+  const int64_t rows = (int64_t)a.max_q * a.G, span = a.window ? std::min<int64_t>(a.nk, (int64_t)a.window + a.max_q) : a.nk;
   return rows <= 16 || (rows + 15) / 16 <= (int64_t(1) << 25) / (2 * span * a.D) / ((int64_t)a.B * a.Hkv);
 }
 

@@ -33,7 +33,6 @@
 // the softmax may rescale it.
 #include <algorithm>
 #include <cstring>
-#include <mutex>
 #include <type_traits>
 
 #include <cudaTypedefs.h>
@@ -45,7 +44,6 @@
 namespace santa {
 
 namespace {
-
 
 constexpr int BKEYS = PG_CHUNK_KEYS;   // keys per block
 constexpr int TROWS = 128;             // rows per tile (lanes of tensor memory)
@@ -80,17 +78,23 @@ __device__ __forceinline__ bool test_phase(uint32_t bar, unsigned parity) {
   return ok != 0;
 }
 
-// Waits for a phase, for a second at most; after one wait has run out in the
-// CTA (`dead`), no other waits.
+// Waits for a phase, for a second at most in which the CTA's count of slow work
+// (dead[1]) does not move; after one wait has run out (dead[0]), no other waits.
 __device__ __forceinline__ void wait_phase(uint32_t bar, unsigned parity, int* err, volatile int* dead) {
   if (test_phase(bar, parity)) return;   // 40 cycles; the waiting form takes more also where there is nothing to wait for
   unsigned long long t0 = 0;
+  int seen = 0;
   for (unsigned i = 0;; ++i) {
     if (mbar_try_wait(bar, parity)) return;
     if (i % 64 == 63) {
       if (*dead) return;
-      if (t0 == 0) t0 = global_ns();
-      else if (global_ns() - t0 > WAIT_NS) break;
+      const unsigned long long now = global_ns();
+      if (t0 == 0 || dead[1] != seen) {
+        seen = dead[1];
+        t0 = now;
+      } else if (now - t0 > WAIT_NS) {
+        break;
+      }
     }
   }
   *dead = 1;
@@ -370,7 +374,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
   __shared__ int s_items[Gm::THREADS / 32], s_most[Gm::THREADS / 32];
   __shared__ float s_ml[2][2][TROWS], s_sl[TROWS];
   __shared__ uint32_t s_tm;
-  __shared__ int s_dead, s_bad[4], s_odd[4];   // of piece np: entry np & 3 holds np + 1
+  __shared__ int s_dead[2], s_bad[4], s_odd[4];   // of piece np: entry np & 3 holds np + 1
   __shared__ Walk s_walk[8];                    // the softmax warps' walks: their registers hold rows of S
   __shared__ Piece s_piece[8];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -380,7 +384,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
   const uint32_t bar0 = smem_addr(s_bar);
   auto bar = [&](int i) { return bar0 + 8u * (uint32_t)i; };
   if (tid == 0) {
-    s_dead = 0;
+    s_dead[0] = s_dead[1] = 0;
     for (int i = 0; i < 4; ++i) s_bad[i] = s_odd[i] = 0;
     for (int i = 0; i < N_BAR; ++i) {
       const int count = i == Q_READY ? 8
@@ -403,7 +407,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
   __syncthreads();
   tm_fence_after();
   const uint32_t tm = uniform(s_tm);
-  volatile int* const dead = &s_dead;
+  volatile int* const dead = s_dead;
   const uint32_t tmS = tm, tmO = tm + 256;           // tile t: S (and P) at 128 t, O at 256 + 128 t
   const int per = TROWS / a.G;                       // tokens per tile of 128 rows
 
@@ -654,10 +658,11 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                 vsc = __ldg(a.vs + at);
               }
             }
-            if (!(vsc <= 3.402823466e38f)) {   // the values are NaN, the softmax is not: given back at the end
+            if (odd_scale(vsc)) {   // the values are NaN, the softmax is not: given back at the end
               s_odd[np & 3] = np + 1;
               vsc = 1.f;
             }
+            vsc = fmaxf(vsc, V_SCALE_LEAST);
             float lv, rv;
             asm("lg2.approx.f32 %0, %1;" : "=f"(lv) : "f"(vsc));
             asm("rcp.approx.f32 %0, %1;" : "=f"(rv) : "f"(vsc));
@@ -969,28 +974,51 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
               if (join) mbar_arrive(bar(O_FREE + 1));
             }
           }
-          if (odd && live_row) {
-            // what was taken out of V, to the rows that see its key
-            for (int key = max(lo, blk0 * BKEYS); key < min(hi, (blk0 + nblk) * BKEYS); ++key) {
-              const int pid = a.table[(long long)pc.b * a.max_pages + (key >> a.page_shift)];
-              if ((unsigned)pid >= (unsigned)a.n_pages) continue;
+          if (odd) {
+            // what was taken out of V, to the rows that see its key: a lane
+            // looks for it in a key of its own, then all take the keys found
+            const int end = min(pc.s.kv, (blk0 + nblk) * BKEYS);
+#pragma unroll 1
+            for (int key0 = blk0 * BKEYS; key0 < end; key0 += 32) {
+              const int key = key0 + lane;
+              const int pid = key < end ? a.table[(long long)pc.b * a.max_pages + (key >> a.page_shift)] : -1;
               const int in_page = key & ((1 << a.page_shift) - 1);
-              const long long vr = (((long long)pid << a.page_shift) + in_page) * a.Hkv + kvh;
-              if (E4M3) {
-                const float sc = a.vs[((((long long)pid * a.Hkv) + kvh) << a.page_shift) + in_page];
-                const unsigned char* v = static_cast<const unsigned char*>(a.V) + vr * D + c0;
+              long long vr = 0;
+              bool is_odd = false, sc_odd = false;
+              if ((unsigned)pid < (unsigned)a.n_pages) {
+                vr = (((long long)pid << a.page_shift) + in_page) * a.Hkv + kvh;
+                const uint4* v = reinterpret_cast<const uint4*>(static_cast<const unsigned char*>(a.V) + (vr * D + c0) * (E4M3 ? 1 : 2));
+                if (E4M3) sc_odd = odd_scale(a.vs[((((long long)pid * a.Hkv) + kvh) << a.page_shift) + in_page]);
 #pragma unroll
-                for (int e = 0; e < EC; ++e)
-                  if (!(sc <= 3.402823466e38f) || (v[e] & 0x7f) == 0x7f) f[e] = __int_as_float(0x7fffffff);
-              } else {
-                const uint32_t* v = reinterpret_cast<const uint32_t*>(static_cast<const T*>(a.V) + vr * D + c0);
-#pragma unroll
-                for (int e = 0; e < EC / 2; ++e) {
-                  const float2 y = unpack2h<T>(v[e]);
-                  if (!(fabsf(y.x) <= 3.402823466e38f)) f[2 * e] += y.x;
-                  if (!(fabsf(y.y) <= 3.402823466e38f)) f[2 * e + 1] += y.y;
+                for (int q = 0; q < EC * (E4M3 ? 1 : 2) / 16; ++q) {
+                  const uint4 w = v[q];
+                  if (E4M3)
+                    is_odd |= ((((w.x & 0x7f7f7f7fu) + 0x01010101u) | ((w.y & 0x7f7f7f7fu) + 0x01010101u) |
+                                ((w.z & 0x7f7f7f7fu) + 0x01010101u) | ((w.w & 0x7f7f7f7fu) + 0x01010101u)) & 0x80808080u) != 0;
+                  else is_odd |= odd16<T>(w);
                 }
               }
+              const unsigned scales = __ballot_sync(FULL, sc_odd);
+              for (unsigned found = __ballot_sync(FULL, is_odd || sc_odd); found; found &= found - 1) {
+                const int u = __ffs(found) - 1;
+                const long long at_u = __shfl_sync(FULL, vr, u) * D + c0;
+                if (key0 + u < lo || key0 + u >= hi) continue;
+                if (E4M3) {
+                  const unsigned char* v = static_cast<const unsigned char*>(a.V) + at_u;
+#pragma unroll
+                  for (int e = 0; e < EC; ++e)
+                    if ((scales >> u & 1) || (v[e] & 0x7f) == 0x7f) f[e] = __int_as_float(0x7fffffff);
+                } else {
+                  const uint32_t* v = reinterpret_cast<const uint32_t*>(static_cast<const T*>(a.V) + at_u);
+#pragma unroll
+                  for (int e = 0; e < EC / 2; ++e) {
+                    const float2 y = unpack2h<T>(v[e]);
+                    if (!(fabsf(y.x) <= 3.402823466e38f)) f[2 * e] += y.x;
+                    if (!(fabsf(y.y) <= 3.402823466e38f)) f[2 * e + 1] += y.y;
+                  }
+                }
+              }
+              if (lane == 0) atomicAdd(&s_dead[1], 1);   // slow, but not stuck: the others keep waiting
             }
           }
           if (live_row) {
@@ -1117,15 +1145,16 @@ __global__ void __launch_bounds__(512, 2) chunk_merge_kernel(PagedArgs a) {
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 map_encoder() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-  });
+  static std::atomic<PFN_cuTensorMapEncodeTiled_v12000> kept{nullptr};
+  PFN_cuTensorMapEncodeTiled_v12000 fn = kept.load(std::memory_order_relaxed);
+  if (fn) return fn;
+  void* p = nullptr;
+  cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
+  if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+      q != cudaDriverEntryPointSuccess)
+    return nullptr;
+  fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  kept.store(fn, std::memory_order_relaxed);
   return fn;
 }
 

@@ -285,7 +285,7 @@ __global__ void __launch_bounds__(NT, E4M3 ? 3 : 2) paged_tokens_kernel(PagedArg
         for (int nb = 0; nb < NB; ++nb) Mma<M16>::run(acc[nb][ks & 1], f, bq[nb][ks][0], bq[nb][ks][1]);
       }
     }
-    // a v_scale that is not finite makes the values NaN, not the softmax: vnan is added to its probabilities
+    // a v_scale that is none makes the values NaN, not the softmax: vnan is added to its probabilities
     float ksc[2] = {1.f, 1.f}, lv[2] = {0.f, 0.f}, rv[2] = {1.f, 1.f}, vnan[2] = {0.f, 0.f};
     if (E4M3) {
 #pragma unroll
@@ -293,10 +293,11 @@ __global__ void __launch_bounds__(NT, E4M3 ? 3 : 2) paged_tokens_kernel(PagedArg
         float v;
         asm volatile("ld.shared.f32 %0, [%1];" : "=f"(ksc[j]) : "r"(vb + Gm::KB + (g8 + 8 * j) * 4));
         asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(vb + Gm::KB + 64 + (g8 + 8 * j) * 4));
-        if (!(v <= 3.402823466e38f)) {
+        if (odd_scale(v)) {
           vnan[j] = __int_as_float(0x7fffffff);
           v = 1.f;
         }
+        v = fmaxf(v, V_SCALE_LEAST);
         asm("lg2.approx.f32 %0, %1;" : "=f"(lv[j]) : "f"(v));
         asm("rcp.approx.f32 %0, %1;" : "=f"(rv[j]) : "f"(v));
       }
@@ -519,7 +520,9 @@ __global__ void __launch_bounds__(NT, E4M3 ? 3 : 2) paged_tokens_kernel(PagedArg
 // eight splits: their sums under a running maximum, eight requested at a time
 // (76 splits a row: 17 us with one warp).  Rows of tiles that were not split are
 // written already.  What it looks up of the batch is none of the attention
-// kernel's output, and so is read while that still runs.
+// kernel's output, and so is read while that still runs; but no thread ends
+// before it has waited, or the merge could be over, and the stream's next
+// kernel begin, while the attention still writes.
 template <typename T, int D, int WPR>
 __global__ void __launch_bounds__(128) paged_merge_kernel(PagedArgs a) {
   __shared__ float s_o[WPR][D], s_ml[WPR][2];
@@ -527,21 +530,25 @@ __global__ void __launch_bounds__(128) paged_merge_kernel(PagedArgs a) {
   const long long w = (long long)blockIdx.x * (4 / WPR) + warp / WPR;   // the row
   const long long t = w / a.H;
   const int h = (int)(w - t * a.H);
-  int b;
-  if (t >= a.total_q || !paged_seq_of(a, t, b)) return;
-  const Seq s = paged_seq(a, b, false);
-  const int i = (int)(t - s.q0), kvh = h / a.G, g = h % a.G;
-  if (i >= s.n) return;
-  const int tile = (i * a.G + g) / a.rows, r = (i * a.G + g) % a.rows;
-  int i0, i1;
-  tile_tokens(a, s.n, tile, i0, i1);
-  const int splits = max(1, (tile_keys(a, s, i0, i1, PG_BLK).blk + a.split_blk - 1) / a.split_blk);
+  int b, splits = 1, r = 0;
+  long long base = 0;
+  if (t < a.total_q && paged_seq_of(a, t, b)) {
+    const Seq s = paged_seq(a, b, false);
+    const int i = (int)(t - s.q0), kvh = h / a.G, pr = i * a.G + h % a.G;
+    if (i < s.n) {
+      const int tile = pr / a.rows;
+      r = pr % a.rows;
+      int i0, i1;
+      tile_tokens(a, s.n, tile, i0, i1);
+      splits = max(1, (tile_keys(a, s, i0, i1, PG_BLK).blk + a.split_blk - 1) / a.split_blk);
+      base = (((long long)b * a.tiles + tile) * a.Hkv + kvh) * a.splits;
+    }
+  }
+  wait_for_predecessor();
   if (splits == 1) return;
-  const long long base = (((long long)b * a.tiles + tile) * a.Hkv + kvh) * a.splits;
   constexpr int E = D / 32, U = 8;
   float m = -INFINITY, l = 0.f, o[E] = {};
   bool bad = false;
-  wait_for_predecessor();
   for (int k0 = part * U; k0 < splits; k0 += WPR * U) {
     float2 ml[U], y[U][E / 2];
 #pragma unroll

@@ -118,8 +118,8 @@ class PagedCache:
     def __init__(self, n_pages: int, page_size: int, n_kv_heads: int, head_dim: int, dtype=torch.bfloat16,
                  device="cuda"):
         shape = (n_pages, page_size, n_kv_heads, head_dim)
-        K, V = (torch.zeros(shape, dtype=torch.float32 if dtype == torch.float8_e4m3fn else dtype,
-                            device=device).to(dtype) for _ in range(2))
+        stored = torch.uint8 if dtype == torch.float8_e4m3fn else dtype   # code 0 is the value 0
+        K, V = (torch.zeros(shape, dtype=stored, device=device).view(dtype) for _ in range(2))
         ks = vs = None
         if dtype == torch.float8_e4m3fn:
             ks, vs = (torch.ones((n_pages, n_kv_heads, page_size), dtype=torch.float32, device=device)
@@ -187,6 +187,9 @@ class PagedStep:
         self.dtype, self.batch, self.n_q_heads = dtype, B, n_q_heads
         self.nk = int(nk) if nk is not None else page_table.shape[1] * cache.page_size
         self.total_q = int(total_q) if total_q is not None else B * max_q
+        for name, x in (("n_q_heads", n_q_heads), ("max_q", max_q), ("window", window), ("nk", self.nk), ("total_q", self.total_q)):
+            if not 0 <= x < 1 << 31:   # ctypes would cut it off
+                raise ValueError(f"{name} = {x} is out of range")
         p = PagedParams()
         p.batch, p.n_q_heads, p.n_kv_heads, p.head_dim = B, n_q_heads, cache.n_kv_heads, cache.head_dim
         p.dtype = DTYPES[dtype]
@@ -288,8 +291,8 @@ class PagedStep:
         return q_out
 
     def attend(self, q, *, out=None, lse=None, return_lse: bool = False, stream=None):
-        """softmax(scale q K^T + mask) V over the pages, [total_q, n_q_heads, head_dim] in q's type; with return_lse
-        (or an lse to fill) also the float32 [total_q, n_q_heads] logarithms of the softmax sums."""
+        """softmax(scale q K^T + mask) V over the pages, [total_q, n_q_heads, head_dim] in q's type (out may be q); with
+        return_lse (or an lse to fill) also the float32 [total_q, n_q_heads] logarithms of the softmax sums."""
         raw = self._on(stream)
         q_ptr = self._dense(q, self._shape, self.dtype, "q")
         if out is not None:

@@ -1,0 +1,118 @@
+"""Calls at the corners of what the paged cache's documentation allows, on both attention kernels: scales of zero, the
+output over the queries, a window that reaches past every key, odd values far apart in a long chunk, work that follows a
+call whose merge has nothing to do, sizes that do not fit the C structure."""
+import pytest
+import torch
+
+import stochastic_sparse_decode_split_gb300 as santa
+from paged_reference import Batch, check_attention
+
+pytestmark = pytest.mark.gpu
+BF16, FP16, F8 = torch.bfloat16, torch.float16, torch.float8_e4m3fn
+FEW, CHUNK = ([3000, 40], [2, 1], 8, 2, 128), ([3000, 900], [500, 400], 8, 4, 128)   # which kernel takes them
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA GPU")
+    santa.library()
+
+
+@pytest.mark.parametrize("shape", [FEW, CHUNK])
+def test_values_under_a_scale_of_zero_count_in_the_softmax(shape):
+    """Rows of zeros with a scale of zero, every third and then all: weights of a softmax whose values are zero."""
+    for part in (3, 1):
+        batch = Batch(*shape, BF16, True, 32, seed=4)
+        batch.V.view(torch.uint8)[:, ::part] = 0
+        batch.vs[:, :, ::part] = 0.0
+        step = batch.step()
+        out, lse = step.attend(batch.q, return_lse=True)
+        assert step.error() == 0
+        check_attention(batch, out, lse)
+        assert part == 3 or not bool(out.any())
+
+
+@pytest.mark.parametrize("odd", [-1.0, float("inf"), float("-inf"), float("nan")])
+@pytest.mark.parametrize("shape", [FEW, CHUNK])
+def test_a_v_scale_that_is_none_leaves_the_softmax_alone(shape, odd):
+    batch = Batch(*shape, BF16, True, 32, seed=4)
+    good, good_lse = (x.clone() for x in batch.step().attend(batch.q, return_lse=True))
+    batch.vs[int(batch.table[0, 7 // 32]), 0, 7 % 32] = odd      # key 7 of sequence 0, KV head 0: all its tokens see it
+    step = batch.step()
+    out, lse = step.attend(batch.q, return_lse=True)
+    n, G = shape[1][0], shape[2] // shape[3]
+    assert bool(out[:n, :G].isnan().all())
+    assert torch.equal(out[:n, G:], good[:n, G:]) and torch.equal(out[n:batch.tokens], good[n:batch.tokens])
+    # the key's own weight enters the sum divided by another scale: rounding apart, the same
+    assert float((lse[:batch.tokens] - good_lse[:batch.tokens]).abs().max()) <= 2.0 ** -16
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("shape", [FEW, CHUNK])
+def test_the_output_may_be_the_queries(shape, e4m3):
+    batch = Batch(*shape, BF16, e4m3, 16, seed=6)
+    step = batch.step()
+    good = step.attend(batch.q).clone()
+    q = batch.q.clone()
+    assert step.attend(q, out=q) is q and torch.equal(q, good) and step.error() == 0
+
+
+@pytest.mark.parametrize("shape", [FEW, CHUNK])
+def test_a_window_past_every_key_is_none(shape):
+    batch = Batch(*shape, FP16, False, 16, seed=7)
+    good = batch.step().attend(batch.q)
+    for window in (3000, 3001, (1 << 31) - 1):
+        assert torch.equal(batch.step(window=window).attend(batch.q), good)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_odd_values_all_over_a_long_chunk(e4m3):
+    """A NaN and an infinity in many blocks, the first and the last key among them; rows see those up to their own."""
+    batch = Batch([9000], [700], 4, 2, 64, BF16, e4m3, 64, seed=8)
+    for i, key in enumerate([0, 31, 32, 4095, 8300, 8301, 8600, 8999]):
+        at, slot = int(batch.table[0, key // 64]), key % 64
+        if e4m3:
+            batch.V.view(torch.uint8)[at, slot, 1, 5 + 7 * i] = 0x7F
+        else:
+            batch.V[at, slot, 1, 5 + 7 * i] = float("nan") if i % 2 else float("inf")
+    step = batch.step()
+    out, lse = step.attend(batch.q, return_lse=True)
+    assert step.error() == 0
+    check_attention(batch, out, lse)
+
+
+def test_what_follows_a_call_without_anything_to_merge_sees_its_output():
+    """Bounds that allow many splits, sequences too short for any: the merge ends at once, and nothing overtakes the call."""
+    batch = Batch([90] * 256, [4] * 256, 8, 2, 128, BF16, False, 16, seed=9)
+    table = torch.nn.functional.pad(batch.table, (0, 2048), value=-1).contiguous()
+    step = santa.PagedStep(batch.cache(), table, batch.kv_t, n_q_heads=8, nk=32768, max_q=4, total_q=batch.total_q,
+                           q_offsets=batch.offsets)
+    good = step.attend(batch.q).clone()
+    check = batch.step()
+    torch.cuda.synchronize()
+    assert torch.equal(check.attend(batch.q), good)
+    out = torch.empty_like(good)
+    for _ in range(50):
+        out.zero_()
+        step.attend(batch.q, out=out)
+        assert torch.equal(out, good)
+
+
+def test_an_e4m3_pool_is_made_in_place_and_reads_as_zeros():
+    torch.cuda.synchronize()
+    torch.cuda.reset_peak_memory_stats()
+    before = torch.cuda.memory_allocated()
+    cache = santa.PagedCache(4096, 64, 8, 128, F8)
+    held = 2 * 4096 * 64 * 8 * (128 + 4)
+    assert torch.cuda.max_memory_allocated() - before <= held + (1 << 20)
+    assert cache.K.dtype == F8 and not bool(cache.K.view(torch.uint8).any()) and not bool(cache.V.view(torch.uint8).any())
+
+
+def test_numbers_that_the_structure_cannot_hold_are_refused():
+    cache = santa.PagedCache(8, 16, 2, 64)
+    table = torch.zeros(1, 8, dtype=torch.int32, device="cuda")
+    for kw in (dict(window=(1 << 32) + 5), dict(max_q=(1 << 32) + 1, total_q=1), dict(nk=(1 << 40) + 64), dict(n_q_heads=(1 << 32) + 4),
+               dict(total_q=-1), dict(window=-1)):
+        with pytest.raises(ValueError):
+            santa.PagedStep(cache, table, **{"n_q_heads": 4, **kw})

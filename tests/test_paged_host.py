@@ -158,3 +158,14 @@ def test_the_packed_append_parameters_are_the_structure():
     assert paged._APPEND.size <= size <= paged._APPEND.size + 7      # the structure's end is padded
     back = paged.AppendParams.from_buffer_copy(packed + bytes(8))
     assert all(getattr(back, k) == v for k, v in values.items())
+
+
+def test_more_output_rows_than_a_launch_has_blocks_are_refused(lib):
+    p = params(total_q=1 << 28, q_offsets=A)
+    assert attention(lib, p) == read(lib, p) == append(lib, p) == UNSUPPORTED
+    assert lib.santa_paged_workspace_size(ctypes.byref(p)) == 0
+
+
+def test_a_window_past_every_key_needs_the_workspace_of_none(lib):
+    sizes = {lib.santa_paged_workspace_size(ctypes.byref(params(window=w))) for w in (0, 1000, (1 << 31) - 1)}
+    assert len(sizes) == 1 and sizes.pop() > 0
