@@ -78,23 +78,17 @@ __device__ __forceinline__ bool test_phase(uint32_t bar, unsigned parity) {
   return ok != 0;
 }
 
-// Waits for a phase, for a second at most in which the CTA's count of slow work
-// (dead[1]) does not move; after one wait has run out (dead[0]), no other waits.
+// Waits for a phase, for a second at most; after one wait has run out in the
+// CTA (`dead`), no other waits.
 __device__ __forceinline__ void wait_phase(uint32_t bar, unsigned parity, int* err, volatile int* dead) {
   if (test_phase(bar, parity)) return;   // 40 cycles; the waiting form takes more also where there is nothing to wait for
   unsigned long long t0 = 0;
-  int seen = 0;
   for (unsigned i = 0;; ++i) {
     if (mbar_try_wait(bar, parity)) return;
     if (i % 64 == 63) {
       if (*dead) return;
-      const unsigned long long now = global_ns();
-      if (t0 == 0 || dead[1] != seen) {
-        seen = dead[1];
-        t0 = now;
-      } else if (now - t0 > WAIT_NS) {
-        break;
-      }
+      if (t0 == 0) t0 = global_ns();
+      else if (global_ns() - t0 > WAIT_NS) break;
     }
   }
   *dead = 1;
@@ -374,7 +368,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
   __shared__ int s_items[Gm::THREADS / 32], s_most[Gm::THREADS / 32];
   __shared__ float s_ml[2][2][TROWS], s_sl[TROWS];
   __shared__ uint32_t s_tm;
-  __shared__ int s_dead[2], s_bad[4], s_odd[4];   // of piece np: entry np & 3 holds np + 1
+  __shared__ int s_dead, s_bad[4], s_odd[4];   // of piece np: entry np & 3 holds np + 1
   __shared__ Walk s_walk[8];                    // the softmax warps' walks: their registers hold rows of S
   __shared__ Piece s_piece[8];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -384,7 +378,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
   const uint32_t bar0 = smem_addr(s_bar);
   auto bar = [&](int i) { return bar0 + 8u * (uint32_t)i; };
   if (tid == 0) {
-    s_dead[0] = s_dead[1] = 0;
+    s_dead = 0;
     for (int i = 0; i < 4; ++i) s_bad[i] = s_odd[i] = 0;
     for (int i = 0; i < N_BAR; ++i) {
       const int count = i == Q_READY ? 8
@@ -407,7 +401,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
   __syncthreads();
   tm_fence_after();
   const uint32_t tm = uniform(s_tm);
-  volatile int* const dead = s_dead;
+  volatile int* const dead = &s_dead;
   const uint32_t tmS = tm, tmO = tm + 256;           // tile t: S (and P) at 128 t, O at 256 + 128 t
   const int per = TROWS / a.G;                       // tokens per tile of 128 rows
 
@@ -974,53 +968,6 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
               if (join) mbar_arrive(bar(O_FREE + 1));
             }
           }
-          if (odd) {
-            // what was taken out of V, to the rows that see its key: a lane
-            // looks for it in a key of its own, then all take the keys found
-            const int end = min(pc.s.kv, (blk0 + nblk) * BKEYS);
-#pragma unroll 1
-            for (int key0 = blk0 * BKEYS; key0 < end; key0 += 32) {
-              const int key = key0 + lane;
-              const int pid = key < end ? a.table[(long long)pc.b * a.max_pages + (key >> a.page_shift)] : -1;
-              const int in_page = key & ((1 << a.page_shift) - 1);
-              long long vr = 0;
-              bool is_odd = false, sc_odd = false;
-              if ((unsigned)pid < (unsigned)a.n_pages) {
-                vr = (((long long)pid << a.page_shift) + in_page) * a.Hkv + kvh;
-                const uint4* v = reinterpret_cast<const uint4*>(static_cast<const unsigned char*>(a.V) + (vr * D + c0) * (E4M3 ? 1 : 2));
-                if (E4M3) sc_odd = odd_scale(a.vs[((((long long)pid * a.Hkv) + kvh) << a.page_shift) + in_page]);
-#pragma unroll
-                for (int q = 0; q < EC * (E4M3 ? 1 : 2) / 16; ++q) {
-                  const uint4 w = v[q];
-                  if (E4M3)
-                    is_odd |= ((((w.x & 0x7f7f7f7fu) + 0x01010101u) | ((w.y & 0x7f7f7f7fu) + 0x01010101u) |
-                                ((w.z & 0x7f7f7f7fu) + 0x01010101u) | ((w.w & 0x7f7f7f7fu) + 0x01010101u)) & 0x80808080u) != 0;
-                  else is_odd |= odd16<T>(w);
-                }
-              }
-              const unsigned scales = __ballot_sync(FULL, sc_odd);
-              for (unsigned found = __ballot_sync(FULL, is_odd || sc_odd); found; found &= found - 1) {
-                const int u = __ffs(found) - 1;
-                const long long at_u = __shfl_sync(FULL, vr, u) * D + c0;
-                if (key0 + u < lo || key0 + u >= hi) continue;
-                if (E4M3) {
-                  const unsigned char* v = static_cast<const unsigned char*>(a.V) + at_u;
-#pragma unroll
-                  for (int e = 0; e < EC; ++e)
-                    if ((scales >> u & 1) || (v[e] & 0x7f) == 0x7f) f[e] = __int_as_float(0x7fffffff);
-                } else {
-                  const uint32_t* v = reinterpret_cast<const uint32_t*>(static_cast<const T*>(a.V) + at_u);
-#pragma unroll
-                  for (int e = 0; e < EC / 2; ++e) {
-                    const float2 y = unpack2h<T>(v[e]);
-                    if (!(fabsf(y.x) <= 3.402823466e38f)) f[2 * e] += y.x;
-                    if (!(fabsf(y.y) <= 3.402823466e38f)) f[2 * e + 1] += y.y;
-                  }
-                }
-              }
-              if (lane == 0) atomicAdd(&s_dead[1], 1);   // slow, but not stuck: the others keep waiting
-            }
-          }
           if (live_row) {
             // 32 bytes per lane and store: a lane's row is its own, and half
             // sectors would be written twice
@@ -1050,6 +997,84 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
             a.part_ml[2 * part + 1] = bad ? -1.f : l;
           } else if (a.lse) {
             a.lse[at] = empty ? -INFINITY : m * 0.6931471805599453f + __logf(l);
+          }
+        }
+        if (odd) {
+          // What was taken out of V, to the rows that see its key, in what they
+          // have just stored: a lane looks into a key of its own, 32 of them at
+          // a time.  Over an e4m3 cache it is NaNs, a bit for each column; keys
+          // that every row of the tile sees give theirs to all at once, so that
+          // 2^21 keys take well under the second that the other warps wait.  In
+          // 16 bits it is what the cleaned blocks held, few at the mask's edges.
+          // After the stores, so that the usual way is not longer for it
+          // (between the sums and the stores it took 3 %).
+          int clean_lo, clean_hi, none;
+          visible_keys(a, pc.s.kv, pc.s.kv - pc.s.n + pc.i0, none, clean_hi);
+          visible_keys(a, pc.s.kv, pc.s.kv - pc.s.n + pc.i1, clean_lo, none);
+          const int end = min(pc.s.kv, (blk0 + nblk) * BKEYS);
+          const bool mark = live_row && !(whole && empty);
+          auto give = [&](int c, float y) {   // y is odd: the sum with it is the result's, whatever the scale
+            if (whole) {
+              uint16_t* const o = static_cast<uint16_t*>(a.out) + at * D + c;
+              *o = (uint16_t)pack2h<T>(unpack2h<T>(*o).x + y, 0.f);
+            } else {
+              a.part_o[part * D + c] += y;
+            }
+          };
+          constexpr int EC_ODD = E4M3 ? 32 : D;
+#pragma unroll 1
+          for (int c0 = 0; c0 < D; c0 += EC_ODD) {
+            uint32_t nan_columns = 0;
+#pragma unroll 1
+            for (int key0 = blk0 * BKEYS; key0 < end; key0 += 32) {
+              const int block = key0 & -BKEYS, key = key0 + lane;
+              if (!E4M3 && block >= clean_lo && block + BKEYS <= clean_hi) continue;
+              const int pid = key < end ? a.table[(long long)pc.b * a.max_pages + (key >> a.page_shift)] : -1;
+              const int in_page = key & ((1 << a.page_shift) - 1);
+              long long at_v = 0;
+              uint32_t found = 0;   // e4m3: the odd columns; else whether there are any
+              if ((unsigned)pid < (unsigned)a.n_pages) {
+                at_v = ((((long long)pid << a.page_shift) + in_page) * a.Hkv + kvh) * D + c0;
+                const uint4* const v = reinterpret_cast<const uint4*>(static_cast<const unsigned char*>(a.V) + at_v * (E4M3 ? 1 : 2));
+                if (E4M3) {
+#pragma unroll
+                  for (int q = 0; q < EC_ODD / 16; ++q) {
+                    const uint4 w = v[q];
+                    const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)   // the bytes' marks side by side: bits 24 to 27 of the product
+                      found |= (((((ww[e] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7) * 0x01020408u >> 24 & 15u) << ((16 * q + 4 * e) & 31);
+                  }
+                  if (odd_scale(a.vs[((((long long)pid * a.Hkv) + kvh) << a.page_shift) + in_page])) found = ~0u;
+                } else {
+#pragma unroll 4
+                  for (int q = 0; q < D / 8; ++q) found |= odd16<T>(v[q]);
+                }
+              }
+              if (E4M3 && key0 >= lo_last && key0 + 32 <= hi_first) {
+                nan_columns |= __reduce_or_sync(FULL, found);
+                continue;
+              }
+              for (unsigned keys = __ballot_sync(FULL, found != 0); keys; keys &= keys - 1) {
+                const int u = __ffs(keys) - 1;
+                const uint32_t columns = __shfl_sync(FULL, found, u);
+                const long long at_u = __shfl_sync(FULL, at_v, u);
+                if (!mark || key0 + u < lo || key0 + u >= hi) continue;
+                if (E4M3) {
+                  nan_columns |= columns;
+                } else {
+                  const uint32_t* const v = reinterpret_cast<const uint32_t*>(static_cast<const T*>(a.V) + at_u);
+#pragma unroll 1
+                  for (int e = 0; e < D / 2; ++e) {
+                    const float2 y = unpack2h<T>(v[e]);
+                    if (!(fabsf(y.x) <= 3.402823466e38f)) give(2 * e, y.x);
+                    if (!(fabsf(y.y) <= 3.402823466e38f)) give(2 * e + 1, y.y);
+                  }
+                }
+              }
+            }
+            if (E4M3 && mark)
+              for (; nan_columns; nan_columns &= nan_columns - 1) give(c0 + __ffs(nan_columns) - 1, __int_as_float(0x7fffffff));
           }
         }
       }

@@ -530,25 +530,21 @@ __global__ void __launch_bounds__(128) paged_merge_kernel(PagedArgs a) {
   const long long w = (long long)blockIdx.x * (4 / WPR) + warp / WPR;   // the row
   const long long t = w / a.H;
   const int h = (int)(w - t * a.H);
-  int b, splits = 1, r = 0;
-  long long base = 0;
-  if (t < a.total_q && paged_seq_of(a, t, b)) {
-    const Seq s = paged_seq(a, b, false);
-    const int i = (int)(t - s.q0), kvh = h / a.G, pr = i * a.G + h % a.G;
-    if (i < s.n) {
-      const int tile = pr / a.rows;
-      r = pr % a.rows;
-      int i0, i1;
-      tile_tokens(a, s.n, tile, i0, i1);
-      splits = max(1, (tile_keys(a, s, i0, i1, PG_BLK).blk + a.split_blk - 1) / a.split_blk);
-      base = (((long long)b * a.tiles + tile) * a.Hkv + kvh) * a.splits;
-    }
-  }
-  wait_for_predecessor();
-  if (splits == 1) return;
+  int b;
+  if (t >= a.total_q || !paged_seq_of(a, t, b)) return wait_for_predecessor();
+  const Seq s = paged_seq(a, b, false);
+  const int i = (int)(t - s.q0), kvh = h / a.G, g = h % a.G;
+  if (i >= s.n) return wait_for_predecessor();
+  const int tile = (i * a.G + g) / a.rows, r = (i * a.G + g) % a.rows;
+  int i0, i1;
+  tile_tokens(a, s.n, tile, i0, i1);
+  const int splits = max(1, (tile_keys(a, s, i0, i1, PG_BLK).blk + a.split_blk - 1) / a.split_blk);
+  if (splits == 1) return wait_for_predecessor();
+  const long long base = (((long long)b * a.tiles + tile) * a.Hkv + kvh) * a.splits;
   constexpr int E = D / 32, U = 8;
   float m = -INFINITY, l = 0.f, o[E] = {};
   bool bad = false;
+  wait_for_predecessor();
   for (int k0 = part * U; k0 < splits; k0 += WPR * U) {
     float2 ml[U], y[U][E / 2];
 #pragma unroll

@@ -116,3 +116,18 @@ def test_numbers_that_the_structure_cannot_hold_are_refused():
                dict(total_q=-1), dict(window=-1)):
         with pytest.raises(ValueError):
             santa.PagedStep(cache, table, **{"n_q_heads": 4, **kw})
+
+
+def test_nothing_but_odd_values_in_a_long_chunk():
+    """65536 keys of NaN codes per item and fewer CTAs than items: giving them back stays far below the bound of the
+    kernel's waits, and the softmax's sums are those of the keys."""
+    B, kv = 320, 65536
+    batch = Batch([kv], [129], 1, 1, 64, BF16, True, 256, seed=10)
+    batch.V.view(torch.uint8).fill_(0x7F)
+    step = santa.PagedStep(batch.cache(), batch.table.expand(B, -1).contiguous(), batch.kv_t.expand(B).contiguous(), n_q_heads=1,
+                           dtype=BF16, nk=kv, max_q=129)
+    one, one_lse = (x.clone() for x in batch.step().attend(batch.q, return_lse=True))
+    out, lse = step.attend(batch.q.repeat(B, 1, 1), return_lse=True)
+    assert step.error() == 0 and bool(out.isnan().all()) and bool(one.isnan().all())
+    # shared items and whole ones sum in another order
+    assert float((lse.view(B, 129, 1) - one_lse).abs().max()) <= 2.0 ** -14
