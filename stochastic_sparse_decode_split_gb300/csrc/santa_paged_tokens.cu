@@ -7,9 +7,15 @@
 // matters is bytes in flight and an even share for every SM.  A tile (16 or 8
 // query rows of one sequence and KV head) is cut into splits of whole
 // 16-key blocks; a CTA's four warps take its blocks in turn, each with its own
-// ring of cp.async stages (no barrier inside the loop).  Scores come from the
-// tensor cores as S^T = K q^T (16 keys x 8 rows), the running softmax is kept
-// in base 2, and O^T = V^T P^T accumulates in registers.
+// ring of cp.async stages (no barrier inside the loop; a stage is refilled as
+// soon as it is left).  Scores come from the tensor cores as S^T = K q^T (16
+// keys x 8 rows), the running softmax is kept in base 2, and O^T = V^T P^T
+// accumulates in registers.
+//
+// Measured: 16 sequences of 1024 to 32768 keys, 28 and 4 heads of 128, fp16:
+// 103 us, 6.3 TB/s (0.93 of a copy's rate); two of 131072 over e4m3, 32 and 8
+// heads: 103 us, 5.4 TB/s (0.79: more instructions per byte); one token over
+// 1000 keys 5.8 us, the two launches and their chain of look-ups.
 //
 // e4m3 caches: codes widen to fp16 exactly, on the way from shared memory to
 // the tensor cores.  Queries become fp16 under a power of two per row that
@@ -96,6 +102,12 @@ struct Geom {
     const int line = r >> 1;
     return (uint32_t)(line * 128 + ((((r & 1) * 4 + c) ^ (line & 7)) << 4));
   }
+  // at(r + j JROWS, c) from at(r, c), for r < JROWS, the rows that a warp's
+  // copy covers: the line moves on, and the swizzle only in its higher bits.
+  static constexpr int JROWS = 32 / CH;
+  static __device__ __forceinline__ uint32_t at_next(uint32_t at0, int j) {
+    return ROWB == 256 ? (at0 ^ (uint32_t)((2 * j & 7) << 4)) + 256u * j : (at0 ^ (uint32_t)((4 * j & 7) << 4)) + 512u * j;
+  }
 };
 
 template <bool E4M3, int D, int R>
@@ -142,6 +154,10 @@ __global__ void __launch_bounds__(NT, E4M3 ? 3 : 2) paged_tokens_kernel(PagedArg
   // ---- the warp's ring
   const uint32_t ring = ((smem_addr(smem_raw) + 127u) & ~127u) + (uint32_t)(warp * NS * Gm::STAGE);
   const unsigned long long pol = evict_first_policy();
+  const long long step = (long long)a.Hkv * Gm::ROWB;   // from row to row of a page
+  const long long lane_off = lane / Gm::CH * step + lane % Gm::CH * 16;
+  const uint32_t lane_at = Gm::at(lane / Gm::CH, lane % Gm::CH);
+  uint32_t put = 0, get = 0;   // offsets of the next block's stage
   int pids = 0;        // lane l: page of the warp's block (k & ~31) + l
   auto issue = [&](int k) {
     if ((k & 31) == 0) {
@@ -160,16 +176,29 @@ __global__ void __launch_bounds__(NT, E4M3 ? 3 : 2) paged_tokens_kernel(PagedArg
       const int slot = key0 & ((1 << a.page_shift) - 1);
       const int live = ok ? min(PG_BLK, s.kv - key0) : 0;
       const long long row = ok ? ((long long)pid << a.page_shift) + slot : 0;
-      const uint32_t dst = ring + (uint32_t)((k % NS) * Gm::STAGE);
-      const long long off = (row * a.Hkv + kvh) * Gm::ROWB, step = (long long)a.Hkv * Gm::ROWB;
+      const uint32_t dst = ring + put;
+      const long long off = (row * a.Hkv + kvh) * Gm::ROWB;
       const unsigned char* kp = static_cast<const unsigned char*>(a.K) + off;
       const unsigned char* vp = static_cast<const unsigned char*>(a.V) + off;
+      if (live == PG_BLK) {   // addresses by additions: 103.5 -> 102.9 us where HBM bounds, 39.9 -> 39.2 with 16 rows
+        kp += lane_off;
+        vp += lane_off;
 #pragma unroll
-      for (int j = 0; j < Gm::KB / 512; ++j) {
-        const int q = lane + 32 * j, r = q / Gm::CH, c = q % Gm::CH;
-        const long long o = r < live ? r * step + c * 16 : 0;
-        cp16z(dst + Gm::at(r, c), kp + o, r < live ? 16 : 0, pol);
-        cp16z(dst + Gm::KB + Gm::at(r, c), vp + o, r < live ? 16 : 0, pol);
+        for (int j = 0; j < Gm::KB / 512; ++j) {
+          const uint32_t to = dst + Gm::at_next(lane_at, j);
+          cp_async16_hint(to, kp, pol);
+          cp_async16_hint(to + Gm::KB, vp, pol);
+          kp += Gm::JROWS * step;
+          vp += Gm::JROWS * step;
+        }
+      } else {
+#pragma unroll 1
+        for (int j = 0; j < Gm::KB / 512; ++j) {
+          const int q = lane + 32 * j, r = q / Gm::CH, c = q % Gm::CH;
+          const long long o = r < live ? r * step + c * 16 : 0;
+          cp16z(dst + Gm::at(r, c), kp + o, r < live ? 16 : 0, pol);
+          cp16z(dst + Gm::KB + Gm::at(r, c), vp + o, r < live ? 16 : 0, pol);
+        }
       }
       if (E4M3 && lane < 8) {
         const int i = (lane & 3) * 4;   // four scales; a row past the last key may hold anything
@@ -178,9 +207,10 @@ __global__ void __launch_bounds__(NT, E4M3 ? 3 : 2) paged_tokens_kernel(PagedArg
       }
     }
     cp_async_commit();
+    put = put + Gm::STAGE == NS * Gm::STAGE ? 0 : put + Gm::STAGE;
   };
 #pragma unroll
-  for (int k = 0; k < NS - 1; ++k) issue(k);
+  for (int k = 0; k < NS; ++k) issue(k);
 
   // ---- query fragments (the B operand: k = d, n = row); rows past the last read as zero
   const T* const qp = static_cast<const T*>(a.q);
@@ -252,76 +282,91 @@ __global__ void __launch_bounds__(NT, E4M3 ? 3 : 2) paged_tokens_kernel(PagedArg
   }
   const int lrow = (lane & 7) + ((lane >> 3) & 1) * 8, lhalf = lane >> 4;        // K: matrices (rows 0-7, 8-15) x (chunk, next)
   const int vrow = (lane & 7) + ((lane >> 4) & 1) * 8, vhalf = (lane >> 3) & 1;  // 16-bit V^T
-#pragma unroll 1
-  for (int k = 0; k < mine; ++k) {
-    cp_async_wait<NS - 2>();
+  // U blocks at a time: one maximum, one rescaling for all of their keys
+  auto take = [&](auto blocks, int k) {
+    constexpr int U = decltype(blocks)::value;
+    cp_async_wait<NS - U>();
     __syncwarp();
-    const uint32_t kb = ring + (uint32_t)((k % NS) * Gm::STAGE), vb = kb + Gm::KB;
-    const int key0 = (blk0 + warp + NW * k) * PG_BLK;
-    issue(k + NS - 1);   // into the stage that the previous block left (all lanes are past it)
-    float acc[NB][2][4];
+    uint32_t kb[U];
+    int key0[U];
+    bool whole = true;   // every row sees every key; the same in every lane
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb)
+    for (int u = 0; u < U; ++u) {
+      kb[u] = ring + get;
+      get = get + Gm::STAGE == NS * Gm::STAGE ? 0 : get + Gm::STAGE;
+      key0[u] = (blk0 + warp + NW * (k + u)) * PG_BLK;
+      whole &= key0[u] >= lo_all && key0[u] + PG_BLK <= hi_all;
+    }
+    float acc[U][NB][2][4];
 #pragma unroll
-      for (int e = 0; e < 2; ++e) acc[nb][e][0] = acc[nb][e][1] = acc[nb][e][2] = acc[nb][e][3] = 0.f;
-    if (E4M3) {
+    for (int u = 0; u < U; ++u) {
 #pragma unroll
-      for (int c = 0; c < D / 16; c += 2) {
-        uint32_t f[4];
-        ldmatrix_x4(kb + Gm::at(lrow, c + lhalf), f);
+      for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const uint32_t fa[4] = {widen8(f[2 * e]), widen8(f[2 * e + 1]), widen8(f[2 * e] >> 16), widen8(f[2 * e + 1] >> 16)};
+        for (int e = 0; e < 2; ++e) acc[u][nb][e][0] = acc[u][nb][e][1] = acc[u][nb][e][2] = acc[u][nb][e][3] = 0.f;
+      if (E4M3) {
 #pragma unroll
-          for (int nb = 0; nb < NB; ++nb) Mma<M16>::run(acc[nb][e], fa, bq[nb][c + e][0], bq[nb][c + e][1]);
+        for (int c = 0; c < D / 16; c += 2) {
+          uint32_t f[4];
+          ldmatrix_x4(kb[u] + Gm::at(lrow, c + lhalf), f);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const uint32_t fa[4] = {widen8(f[2 * e]), widen8(f[2 * e + 1]), widen8(f[2 * e] >> 16), widen8(f[2 * e + 1] >> 16)};
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) Mma<M16>::run(acc[u][nb][e], fa, bq[nb][c + e][0], bq[nb][c + e][1]);
+          }
         }
-      }
-    } else {
+      } else {
 #pragma unroll
-      for (int ks = 0; ks < D / 16; ++ks) {
-        uint32_t f[4];
-        ldmatrix_x4(kb + Gm::at(lrow, ks * 2 + lhalf), f);
+        for (int ks = 0; ks < D / 16; ++ks) {
+          uint32_t f[4];
+          ldmatrix_x4(kb[u] + Gm::at(lrow, ks * 2 + lhalf), f);
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) Mma<M16>::run(acc[nb][ks & 1], f, bq[nb][ks][0], bq[nb][ks][1]);
+          for (int nb = 0; nb < NB; ++nb) Mma<M16>::run(acc[u][nb][ks & 1], f, bq[nb][ks][0], bq[nb][ks][1]);
+        }
       }
     }
     // a v_scale that is none makes the values NaN, not the softmax: vnan is added to its probabilities
-    float ksc[2] = {1.f, 1.f}, lv[2] = {0.f, 0.f}, rv[2] = {1.f, 1.f}, vnan[2] = {0.f, 0.f};
+    float ksc[U][2], lv[U][2], rv[U][2], vnan[U][2];
     if (E4M3) {
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        float v;
-        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(ksc[j]) : "r"(vb + Gm::KB + (g8 + 8 * j) * 4));
-        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(vb + Gm::KB + 64 + (g8 + 8 * j) * 4));
-        if (odd_scale(v)) {
-          vnan[j] = __int_as_float(0x7fffffff);
-          v = 1.f;
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          float v;
+          asm volatile("ld.shared.f32 %0, [%1];" : "=f"(ksc[u][j]) : "r"(kb[u] + 2 * Gm::KB + (g8 + 8 * j) * 4));
+          asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(kb[u] + 2 * Gm::KB + 64 + (g8 + 8 * j) * 4));
+          vnan[u][j] = 0.f;
+          if (odd_scale(v)) {
+            vnan[u][j] = __int_as_float(0x7fffffff);
+            v = 1.f;
+          }
+          v = fmaxf(v, V_SCALE_LEAST);
+          asm("lg2.approx.f32 %0, %1;" : "=f"(lv[u][j]) : "f"(v));
+          asm("rcp.approx.f32 %0, %1;" : "=f"(rv[u][j]) : "f"(v));
         }
-        v = fmaxf(v, V_SCALE_LEAST);
-        asm("lg2.approx.f32 %0, %1;" : "=f"(lv[j]) : "f"(v));
-        asm("rcp.approx.f32 %0, %1;" : "=f"(rv[j]) : "f"(v));
-      }
     }
-    const bool whole = key0 >= lo_all && key0 + PG_BLK <= hi_all;   // the same in every lane
-    float p[NB][2][2];   // [nb][key g8 + 8 j][row hh]
+    float p[U][NB][2][2];   // [nb][key g8 + 8 j][row hh]
     float alpha[NB][2];
     auto softmax = [&](auto all) {
-      constexpr bool ALL = decltype(all)::value;   // every row sees every key of the block
+      constexpr bool ALL = decltype(all)::value;   // every row sees every key of the blocks
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {
-          bool vis[2] = {true, true};
-          float sc[2];
+          bool vis[U][2];
+          float sc[U][2], m = -INFINITY;
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const int key = key0 + g8 + 8 * j;
-            if (!ALL) vis[j] = key >= lo_[nb][hh] && key < hi_[nb][hh];
-            const float v = (acc[nb][0][2 * j + hh] + acc[nb][1][2 * j + hh]) * sl[nb][hh];
-            sc[j] = E4M3 ? fmaf(v, ksc[j], lv[j]) : v;
-            if (!ALL && !vis[j]) sc[j] = -INFINITY;
-          }
-          float m = fmaxf(sc[0], sc[1]);
+          for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const int key = key0[u] + g8 + 8 * j;
+              vis[u][j] = ALL || (key >= lo_[nb][hh] && key < hi_[nb][hh]);
+              const float v = (acc[u][nb][0][2 * j + hh] + acc[u][nb][1][2 * j + hh]) * sl[nb][hh];
+              sc[u][j] = E4M3 ? fmaf(v, ksc[u][j], lv[u][j]) : v;
+              if (!ALL && !vis[u][j]) sc[u][j] = -INFINITY;
+              m = fmaxf(m, sc[u][j]);
+            }
           m = fmaxf(m, __shfl_xor_sync(FULL, m, 4));
           m = fmaxf(m, __shfl_xor_sync(FULL, m, 8));
           m = fmaxf(m, __shfl_xor_sync(FULL, m, 16));
@@ -330,11 +375,14 @@ __global__ void __launch_bounds__(NT, E4M3 ? 3 : 2) paged_tokens_kernel(PagedArg
           rm[nb][hh] = mn;
           float sum = 0.f;
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            p[nb][j][hh] = ALL || vis[j] ? fast_exp2(sc[j] - mu) : 0.f;
-            sum += E4M3 ? (ALL || vis[j] ? p[nb][j][hh] * rv[j] : 0.f) : p[nb][j][hh];
-            if (E4M3 && (ALL || vis[j])) p[nb][j][hh] += vnan[j];
-          }
+          for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              float& pj = p[u][nb][j][hh];
+              pj = ALL || vis[u][j] ? fast_exp2(sc[u][j] - mu) : 0.f;
+              sum += E4M3 ? (ALL || vis[u][j] ? pj * rv[u][j] : 0.f) : pj;
+              if (E4M3 && (ALL || vis[u][j])) pj += vnan[u][j];
+            }
           rl[nb][hh] = fmaf(rl[nb][hh], alpha[nb][hh], sum);
         }
     };
@@ -354,70 +402,75 @@ __global__ void __launch_bounds__(NT, E4M3 ? 3 : 2) paged_tokens_kernel(PagedArg
             oacc[nb][i][2 + hh] *= alpha[nb][hh];
           }
     }
-    // A masked key's value is multiplied by zero below, which a NaN or an
-    // infinity would survive: blocks that not every row sees in full are
-    // looked over, and such a block is added up without the tensor cores.
-    bool odd = false;
-    if (!whole) {
 #pragma unroll
-      for (int j = 0; j < Gm::KB / 512; ++j) {
-        const uint4 v = lds128(vb + (lane + 32 * j) * 16);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    for (int u = 0; u < U; ++u) {
+      const uint32_t vb = kb[u] + Gm::KB;
+      // A masked key's value is multiplied by zero below, which a NaN or an
+      // infinity would survive: blocks that not every row sees in full are
+      // looked over, and such a block is added up without the tensor cores.
+      bool odd = false;
+      if (!whole) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (E4M3) {
+        for (int j = 0; j < Gm::KB / 512; ++j) {
+          const uint4 v = lds128(vb + (lane + 32 * j) * 16);
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-            for (int e = 0; e < 4; ++e) odd |= ((w[i] >> (8 * e)) & 0x7fu) == 0x7fu;
-          } else {
-            const uint32_t ex = std::is_same<T, bf16_t>::value ? 0x7f80u : 0x7c00u;
-            odd |= (w[i] & ex) == ex || ((w[i] >> 16) & ex) == ex;
+          for (int i = 0; i < 4; ++i) {
+            if (E4M3) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) odd |= ((w[i] >> (8 * e)) & 0x7fu) == 0x7fu;
+            } else {
+              const uint32_t ex = std::is_same<T, bf16_t>::value ? 0x7f80u : 0x7c00u;
+              odd |= (w[i] & ex) == ex || ((w[i] >> 16) & ex) == ex;
+            }
           }
         }
+        odd = __any_sync(FULL, odd);
       }
-      odd = __any_sync(FULL, odd);
-    }
-    if (odd) {
+      if (odd) {
 #pragma unroll 1
-      for (int key = 0; key < PG_BLK; ++key) {
+        for (int key = 0; key < PG_BLK; ++key) {
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
+          for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-          for (int hh = 0; hh < 2; ++hh) {
-            const float pk = __shfl_sync(FULL, p[nb][key >> 3][hh], (key & 7) * 4 + t4);
-            if (key0 + key < lo_[nb][hh] || key0 + key >= hi_[nb][hh]) continue;
+            for (int hh = 0; hh < 2; ++hh) {
+              const float pk = __shfl_sync(FULL, key & 8 ? p[u][nb][1][hh] : p[u][nb][0][hh], (key & 7) * 4 + t4);
+              if (key0[u] + key < lo_[nb][hh] || key0[u] + key >= hi_[nb][hh]) continue;
 #pragma unroll
-            for (int i = 0; i < D / 16; ++i)
+              for (int i = 0; i < D / 16; ++i)
 #pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                float v;
-                if (E4M3) {
-                  uint32_t byte;
-                  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(byte) : "r"(vb + Gm::at(key, i) + 2 * g8 + e));
-                  v = Pack<fp16_t>::unpack(widen8(byte)).x;
-                } else {
-                  const int d = 16 * i + g8 + 8 * e;
-                  uint16_t hw;
-                  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(hw) : "r"(vb + Gm::at(key, d >> 3) + (d & 7) * 2));
-                  v = Pack<T>::unpack(hw).x;
+                for (int e = 0; e < 2; ++e) {
+                  float v;
+                  if (E4M3) {
+                    uint32_t byte;
+                    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(byte) : "r"(vb + Gm::at(key, i) + 2 * g8 + e));
+                    v = Pack<fp16_t>::unpack(widen8(byte)).x;
+                  } else {
+                    const int d = 16 * i + g8 + 8 * e;
+                    uint16_t hw;
+                    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(hw) : "r"(vb + Gm::at(key, d >> 3) + (d & 7) * 2));
+                    v = Pack<T>::unpack(hw).x;
+                  }
+                  oacc[nb][i][2 * e + hh] = fmaf(pk, v, oacc[nb][i][2 * e + hh]);
                 }
-                oacc[nb][i][2 * e + hh] = fmaf(pk, v, oacc[nb][i][2 * e + hh]);
-              }
-          }
+            }
+        }
+        continue;
       }
-    } else {
-      // P^T as the B operand (k = key, n = row); for 16-bit caches split into
-      // a 16-bit head and the rounding of the rest, which the HBM-bound loop
-      // has room for
+      // P^T as the B operand (k = key, n = row); over 16-bit caches and for
+      // tiles of eight rows split into a 16-bit head and the rounding of the
+      // rest, which that HBM-bound loop has room for (with 16 rows it cost 6 %)
+      constexpr bool REST = !E4M3 && R == 8;
       uint32_t ph[NB][2], pl[NB][2];
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const uint32_t h = Pack<M16>::pack(p[nb][j][0], p[nb][j][1]);
+          const uint32_t h = Pack<M16>::pack(p[u][nb][j][0], p[u][nb][j][1]);
           ph[nb][j] = movm(h);
-          if (!E4M3) {
+          if (REST) {
             const float2 back = Pack<M16>::unpack(h);
-            pl[nb][j] = movm(Pack<M16>::pack(p[nb][j][0] - back.x, p[nb][j][1] - back.y));
+            pl[nb][j] = movm(Pack<M16>::pack(p[u][nb][j][0] - back.x, p[u][nb][j][1] - back.y));
           }
         }
       if (E4M3) {
@@ -443,13 +496,24 @@ __global__ void __launch_bounds__(NT, E4M3 ? 3 : 2) paged_tokens_kernel(PagedArg
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb) {
             Mma<M16>::run(oacc[nb][i], f, ph[nb][0], ph[nb][1]);
-            Mma<M16>::run(oacc[nb][i], f, pl[nb][0], pl[nb][1]);
+            if (REST) Mma<M16>::run(oacc[nb][i], f, pl[nb][0], pl[nb][1]);
           }
         }
       }
     }
     __syncwarp();
-  }
+#pragma unroll
+    for (int u = 0; u < U; ++u) issue(k + NS + u);   // into the stages that these blocks leave
+  };
+  // Two at a time over e4m3 with tiles of eight rows, whose loop is bound by
+  // the latency of its instructions and has the registers (two sequences of
+  // 131072 keys 100.0 -> 98.9 us, one of 32768 17.8 -> 16.7); with 16 rows it
+  // would spill, and in 16 bits HBM bounds.
+  constexpr int U = E4M3 && R == 8 ? 2 : 1;
+  int k = 0;
+#pragma unroll 1
+  for (; k + U <= mine; k += U) take(std::integral_constant<int, U>(), k);
+  if (U > 1 && k < mine) take(std::integral_constant<int, 1>(), k);
   cp_async_wait_all();
 
   // ---- the warps' partials, merged in shared memory (over the rings)
