@@ -94,14 +94,18 @@ santa::PagedArgs args(const santa_paged_t* p) {
 
 // Which kernel: up to 16 query rows per sequence and KV head the one for few
 // rows; more than that it takes 16 by 16, reading the cache again for each, and
-// starts in 7 us where the kernel for chunks (tiles of 128 rows) takes 13 to
-// 26.  So it also has the calls whose 16-row tiles read at most 2^25 elements
-// of the cache in all.  Measured at that border (8 sequences of 4096 keys, 2 KV
-// heads of 64, 64 rows): 18.3 against 19.2 us, e4m3 21.1 against 23.8; at twice
-// as much (128 rows): 32.6 against 21.6; at half (32 rows): 13.5 against 18.6.
+// starts in 6 us where the kernel for chunks (tiles of 128 rows) takes 13 to
+// 26.  So it also has the calls whose 16-row tiles meet at most 3 * 2^13 blocks
+// of 16 keys in all.  Measured, few rows against chunks: at that border (8
+// sequences of 8191 keys, 2 KV heads of 64, 40 rows) 20.2 against 23.3 us, with
+// 4096 keys and 96 rows 20.5 against 20.9; at two thirds of it (64 rows) 17.0
+// against 19.5, e4m3 19.1 against 24.0, and for heads of 128 (4 sequences of
+// 4096 keys, 8 KV heads, 32 rows) 22.1 against 28.9, e4m3 25.1 against 32.4; at
+// four thirds (128 rows) 29.4 against 21.9, heads of 128 (one sequence of 16384
+// keys, 64 rows) 39 against 31.9.
 bool few_rows(const santa::PagedArgs& a) {
   const int64_t rows = (int64_t)a.max_q * a.G, span = a.window ? std::min<int64_t>(a.nk, (int64_t)a.window + a.max_q) : a.nk;
-  return rows <= 16 || (rows + 15) / 16 <= (int64_t(1) << 25) / (2 * span * a.D) / ((int64_t)a.B * a.Hkv);
+  return rows <= 16 || (rows + 15) / 16 <= 3 * 8192 * 16 / span / ((int64_t)a.B * a.Hkv);
 }
 
 // The attention's plan, and its workspace: header, the chunk attention's notes

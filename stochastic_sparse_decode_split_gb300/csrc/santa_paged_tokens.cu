@@ -708,7 +708,11 @@ cudaError_t merge_type(const PagedArgs& a, const cudaLaunchConfig_t& cfg) {
 
 // Splits: enough CTAs for two on every SM.  Sequences differ in length, and a
 // CTA's share is the longest's, so long tiles are cut finer, into up to four
-// CTAs for every place, while a split keeps 1024 keys.
+// CTAs for every place, while a split keeps 1024 keys.  But not into a few more
+// CTAs than places, which would take two rounds: eight sequences of 8191 keys,
+// 3 tiles and 2 heads of 64, 28.6 us as 384 CTAs, 20.2 as 288 (with lengths from
+// 300 on 17.2 and 20.0); at 1.7 rounds (512, lengths from 300 on, e4m3) 33.4
+// us, 41.9 as 256.
 size_t plan_paged_tokens(PagedArgs& a) {
   a.rows = a.max_q * a.G <= 8 ? 8 : 16;
   a.tokens = 0;
@@ -718,7 +722,8 @@ size_t plan_paged_tokens(PagedArgs& a) {
   const int blks = (span + PG_BLK - 1) / PG_BLK + (a.window ? 1 : 0);
   const long long places = 2ll * a.num_sms;
   long long want = std::max<long long>(1, places / pieces);
-  want = std::max(want, std::min<long long>(4 * places / pieces, blks / 64));
+  const long long fine = std::min<long long>(4 * places / pieces, blks / 64);
+  if (2 * fine * pieces >= 3 * places) want = std::max(want, fine);
   a.split_blk = (int)std::max<long long>(NW, (blks + want - 1) / want);
   a.splits = (blks + a.split_blk - 1) / a.split_blk;
   return a.splits == 1 ? 0 : (size_t)pieces * a.splits;

@@ -1,5 +1,5 @@
-"""The chunk kernel of the paged attention at its edges, on calls large enough to reach it: the call's 16-row tiles would
-read more than 2^25 elements of the cache in all (smaller calls take the kernel for few rows).  Masks, odd values, bad
+"""The chunk kernel of the paged attention at its edges, on calls large enough to reach it (two of many small items take
+the kernel for few rows).  Masks, odd values, bad
 pages, shared items and empty ones, against the definition in 64 bits."""
 import pytest
 import torch

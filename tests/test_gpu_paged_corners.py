@@ -131,3 +131,28 @@ def test_nothing_but_odd_values_in_a_long_chunk():
     assert step.error() == 0 and bool(out.isnan().all()) and bool(one.isnan().all())
     # shared items and whole ones sum in another order
     assert float((lse.view(B, 129, 1) - one_lse).abs().max()) <= 2.0 ** -14
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("kv,n,H,Hkv,D,dtype,page", [
+    ([700] * 150, [20] * 150, 4, 2, 128, BF16, 16), ([300] * 500, [17] * 500, 2, 2, 64, FP16, 16),
+    ([300] * 200, [5] * 199 + [17], 8, 2, 128, FP16, 32), ([2500] * 9, [3] * 8 + [70], 8, 1, 64, BF16, 64)])
+def test_many_small_chunks(kv, n, H, Hkv, D, dtype, page, e4m3):
+    """More items than CTAs, most of one tile of few rows: past the border between the kernels (3 * 2^13 blocks of 16 rows
+    by 16 keys)."""
+    batch = Batch(kv, n, H, Hkv, D, dtype, e4m3, page, seed=len(kv))
+    assert -(-max(n) * (H // Hkv) // 16) * len(kv) * Hkv * max(kv) > 3 * 2 ** 17
+    step = batch.step()
+    out, lse = step.attend(batch.q, return_lse=True)
+    assert step.error() == 0
+    check_attention(batch, out, lse)
+
+
+@pytest.mark.parametrize("nk", [4095, 4096, 4097])
+@pytest.mark.parametrize("n", [12, 13])
+def test_both_sides_of_the_border_between_the_kernels(n, nk):
+    batch = Batch([nk, 4000, 900, 17, 4095, 33, 2048, 16], [n] * 8, 16, 2, 64, BF16, False, 32, seed=n)
+    step = batch.step(nk=nk)
+    out, lse = step.attend(batch.q, return_lse=True)
+    assert step.error() == 0
+    check_attention(batch, out, lse)
