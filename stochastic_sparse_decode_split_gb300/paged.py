@@ -65,7 +65,7 @@ class AppendParams(ctypes.Structure):
 
 
 _APPEND = struct.Struct("@PPPqqqPPPfPqii")   # AppendParams' fields in their order, natively aligned
-_current_device = torch.cuda.current_device
+_current_device, _capturing = torch.cuda.current_device, torch.cuda.is_current_stream_capturing
 
 
 def declare(lib) -> None:
@@ -208,7 +208,7 @@ class PagedStep:
             self.workspace = alloc_workspace(n, self.device)
         # what every call checks and passes again: shapes, the pool (whose tensors the cache keeps), the workspace
         self._index = self.device.index
-        self._outputs = {}
+        self._outputs, self._captured = {}, []
         self._shape = torch.Size((self.total_q, n_q_heads, cache.head_dim))
         self._kv_shape = torch.Size((self.total_q, cache.n_kv_heads, cache.head_dim))
         self._lse_shape, self._weight_shape = self._shape[:2], self._shape[2:]
@@ -322,10 +322,13 @@ class PagedStep:
         elif rows is None:
             rows = self.batch * self.nk
         shape = (rows, self._kv_shape[1], self._kv_shape[2])
+        own = K_out is None or V_out is None
         if K_out is None:
             K_out = self._own("K", raw, shape, self.dtype, stream)
         if V_out is None:
             V_out = self._own("V", raw, shape, self.dtype, stream)
+        if own and _capturing():
+            self._captured.append((K_out, V_out))   # a later call with other rows replaces them; the graph still writes these
         self._check(self._read_fn(self._ref, *self._pool, off_ptr, rows, self._dense(K_out, shape, self.dtype, "K_out"),
                                   self._dense(V_out, shape, self.dtype, "V_out"), *self._ws, raw), "santa_kv_read")
         return K_out, V_out

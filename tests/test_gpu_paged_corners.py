@@ -156,3 +156,27 @@ def test_both_sides_of_the_border_between_the_kernels(n, nk):
     out, lse = step.attend(batch.q, return_lse=True)
     assert step.error() == 0
     check_attention(batch, out, lse)
+
+
+def test_a_captured_reads_outputs_outlive_a_read_of_other_sizes():
+    """The graph writes to the buffers that the step had when it was captured: a read of more rows on that stream makes new
+    ones, and the old ones must not go to anybody else."""
+    batch = Batch([500, 300], [1, 1], 4, 2, 64, BF16, False, 16, seed=11)
+    step = batch.step()
+    offsets = torch.tensor([0, 500, 800], device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step.read(offsets, 800)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            K, V = step.read(offsets, 800)
+        at = (K.data_ptr(), V.data_ptr())
+        del K, V
+        good = [x.clone() for x in step.read(offsets, 900)]
+        others = [torch.full((800, 2, 64), 3.0, dtype=BF16, device="cuda") for _ in range(8)]
+        assert not any(x.data_ptr() in at for x in others)
+        graph.replay()
+        side.synchronize()
+        assert all(bool((x == 3.0).all()) for x in others)
+    assert torch.equal(good[0][:500].double(), batch.rows(0, "K")) and torch.equal(good[1][500:800].double(), batch.rows(1, "V"))
