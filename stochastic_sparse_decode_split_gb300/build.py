@@ -22,7 +22,7 @@ LIB = os.path.join(BUILD, "libsanta.so")
 SOURCES = ["santa_api.cu", "santa_score.cu", "santa_sample.cu", "santa_fused.cu", "santa_fused_bf16.cu", "santa_fused_fp16.cu",
            "santa_flash.cu", "santa_static.cu", "santa_tiled.cu", "santa_bernoulli.cu", "santa_probe.cu",
            "santa_paged_api.cu", "santa_paged_tokens.cu", "santa_paged_chunk.cu", "santa_kv_rows.cu"]
-HEADERS = ["santa_common.cuh", "santa_flash.cuh", "santa_fused.cuh", "santa_grid.cuh", "santa_launch.h", "santa_paged.cuh", "santa_part.cuh",
+HEADERS = ["santa_chunk_share.cuh", "santa_common.cuh", "santa_flash.cuh", "santa_fused.cuh", "santa_grid.cuh", "santa_launch.h", "santa_paged.cuh", "santa_part.cuh",
            "santa_seq.cuh", "santa_stream.cuh", "santa_tcgen05.cuh", "santa_tma.cuh", "santa_window.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

@@ -10,6 +10,9 @@
 
 #include "santa_common.cuh"
 
+// For what the host computes as the kernels do.
+#define SANTA_HD __host__ __device__ __forceinline__
+
 namespace santa {
 
 constexpr int ERR_PAGE = 16;       // a page-table entry outside the pool
@@ -72,7 +75,7 @@ struct Seq {
   bool ok;
 };
 
-__device__ __forceinline__ Seq paged_seq(const PagedArgs& a, int b, bool flag) {
+SANTA_HD Seq paged_seq(const PagedArgs& a, int b, bool flag) {
   Seq s;
   int e = 0;
   if (a.q_offsets) {
@@ -90,12 +93,14 @@ __device__ __forceinline__ Seq paged_seq(const PagedArgs& a, int b, bool flag) {
   s.kv = fine ? kv : 0;
   if (!fine) e |= ERR_NK_BOUND;
   s.ok = e == 0;
+#ifdef __CUDA_ARCH__
   if (e && flag) flag_error(a.err, e);
+#endif
   return s;
 }
 
 // The sequence of token row t (false: padding, or offsets that do not hold it).
-__device__ __forceinline__ bool paged_seq_of(const PagedArgs& a, long long t, int& b) {
+SANTA_HD bool paged_seq_of(const PagedArgs& a, long long t, int& b) {
   if (!a.q_offsets) {
     b = (int)(t / a.max_q);
     return b < a.B;
@@ -111,7 +116,7 @@ __device__ __forceinline__ bool paged_seq_of(const PagedArgs& a, long long t, in
 }
 
 // Keys [lo, hi) that the token at position `pos` sees.
-__device__ __forceinline__ void visible_keys(const PagedArgs& a, int kv, int pos, int& lo, int& hi) {
+SANTA_HD void visible_keys(const PagedArgs& a, int kv, int pos, int& lo, int& hi) {
   hi = a.causal ? min(max(pos + 1, 0), kv) : kv;
   lo = a.window ? min(max(pos - a.window + 1, 0), hi) : 0;
 }
@@ -121,7 +126,7 @@ __device__ __forceinline__ void visible_keys(const PagedArgs& a, int kv, int pos
 struct TileKeys {
   int blk_lo, blk;
 };
-__device__ __forceinline__ TileKeys tile_keys(const PagedArgs& a, const Seq& s, int i0, int i1, int keys) {
+SANTA_HD TileKeys tile_keys(const PagedArgs& a, const Seq& s, int i0, int i1, int keys) {
   int lo0, hi0, lo1, hi1;
   visible_keys(a, s.kv, s.kv - s.n + i0, lo0, hi0);
   visible_keys(a, s.kv, s.kv - s.n + i1, lo1, hi1);
@@ -133,7 +138,7 @@ __device__ __forceinline__ TileKeys tile_keys(const PagedArgs& a, const Seq& s, 
 
 // First and last token of tile `tile` (the rows of a tile need not start at a
 // token's first head unless the tiles keep tokens together).
-__device__ __forceinline__ void tile_tokens(const PagedArgs& a, int n, int tile, int& i0, int& i1) {
+SANTA_HD void tile_tokens(const PagedArgs& a, int n, int tile, int& i0, int& i1) {
   if (a.tokens) {
     i0 = tile * a.tokens;
     i1 = min(n, i0 + a.tokens) - 1;

@@ -45,6 +45,7 @@
 
 #include <cudaTypedefs.h>
 
+#include "santa_chunk_share.cuh"
 #include "santa_launch.h"
 #include "santa_paged.cuh"
 #include "santa_tcgen05.cuh"
@@ -53,11 +54,8 @@ namespace santa {
 
 namespace {
 
-constexpr int BKEYS = PG_CHUNK_KEYS;   // keys per block
 constexpr int TROWS = 128;             // rows per tile (lanes of tensor memory)
 constexpr float RESCALE = 8.f;         // growth of the maximum (base 2) that O is rescaled for
-constexpr int CHUNK_SHARE = 8;         // blocks of time that sharing an item costs
-constexpr int CHUNK_LEAST = 16;        // items of no more blocks are never shared, and no merge is launched for them
 constexpr unsigned long long WAIT_NS = 1000000000ull;
 
 template <bool E4M3, int D>
@@ -181,98 +179,6 @@ __device__ __forceinline__ uint32_t without_odd16(uint32_t w) {
   return w;
 }
 
-// One CTA's share of the batch.  Items in the order (sequence, tile, KV head)
-// weigh their blocks (at least one); CTA c of P takes the blocks
-// [floor(T c / P), floor(T (c + 1) / P)) of the T, or (`split` false) the items
-// that begin in that range.  Every role of the CTA walks the same pieces.
-struct Share {
-  long long lo, hi, T;
-  int P, split;
-  int b, kvh, tile;   // the item that holds block lo
-  long long pos;      // its first block
-};
-__device__ __forceinline__ long long share_begin(long long T, int c, int P) {
-  if (T < (1ll << 24)) return (unsigned)T * (unsigned)c / (unsigned)P;   // c < 256
-  return T * c / P;
-}
-struct Piece {
-  int b, kvh, tile;
-  Seq s;
-  int i0, i1;         // first and last token
-  int blk0, nblk;     // blocks of this piece (0: no key is visible)
-  bool two;           // the second tile holds tokens
-  bool whole, last;   // of the item: all its blocks, its last one
-  long long pos;      // the item's first block
-};
-struct Walk {
-  int b, kvh, tile, of, i0, i1;
-  TileKeys tk;
-  long long pos;
-  Seq s;
-  __device__ __forceinline__ void start(const PagedArgs& a, const Share& sh) {
-    b = sh.b;
-    kvh = sh.kvh;
-    tile = sh.tile;
-    pos = sh.pos;
-    if (b < a.B) load(a);
-  }
-  __device__ __forceinline__ void load(const PagedArgs& a) {   // a sequence and its tile
-    s = paged_seq(a, b, false);
-    keys(a);
-  }
-  __device__ __forceinline__ void keys(const PagedArgs& a) {
-    tile_tokens(a, s.n, tile, i0, i1);
-    tk = tile_keys(a, s, i0, i1, BKEYS);
-  }
-  __device__ __forceinline__ bool next(const PagedArgs& a, const Share& sh, Piece& p) {
-    for (;;) {
-      if (b >= a.B || pos >= sh.hi) return false;
-      if (kvh == a.Hkv || tile * a.tokens >= s.n) {
-        kvh = 0;
-        if (++tile * a.tokens >= s.n) {
-          tile = 0;
-          if (++b < a.B) load(a);
-        } else {
-          keys(a);
-        }
-        continue;
-      }
-      const int w = max(tk.blk, 1);
-      long long begin = max(sh.lo, pos) - pos, end = min(sh.hi, pos + w) - pos;
-      if (!sh.split) {
-        begin = pos >= sh.lo ? 0 : w;
-        end = w;
-      }
-      p.pos = pos;
-      p.kvh = kvh;
-      ++kvh;
-      pos += w;
-      if (begin >= end) continue;
-      p.b = b;
-      p.tile = tile;
-      p.s = s;
-      p.i0 = i0;
-      p.i1 = i1;
-      p.blk0 = tk.blk_lo + (int)begin;
-      p.nblk = tk.blk ? (int)(end - begin) : 0;
-      p.two = i0 + a.tokens / 2 < s.n;
-      p.whole = end - begin == w;
-      p.last = end == w;
-      return true;
-    }
-  }
-};
-
-// Blocks of item i = (sequence, tile), 0 where the tile has no token.
-__device__ __forceinline__ int item_weight(const PagedArgs& a, long long i, bool flag) {
-  if (i >= (long long)a.B * a.tiles) return 0;
-  const int b = (int)(i / a.tiles), tile = (int)(i - (long long)b * a.tiles);
-  const Seq s = paged_seq(a, b, flag && tile == 0);
-  if (tile * a.tokens >= s.n) return 0;
-  int i0, i1;
-  tile_tokens(a, s.n, tile, i0, i1);
-  return max(tile_keys(a, s, i0, i1, BKEYS).blk, 1);
-}
 __device__ __forceinline__ int scan_add(int v, int lane) {   // inclusive, over a warp
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -326,23 +232,10 @@ __device__ __forceinline__ void take_share(const PagedArgs& a, Share& sh, long l
     sh.P = P;
     sh.lo = lo;
     sh.hi = share_begin(T, blockIdx.x + 1, P);
-    // A shared item costs about CHUNK_SHARE blocks of time (its sums out and
-    // in again); without sharing the longest CTA has about ceil(items / P) of
-    // the largest items.
-    all *= a.Hkv;
-    const long long each = all <= P ? 1 : (all + P - 1) / P;
-    sh.split = most > CHUNK_LEAST && each * most > sh.hi - lo + CHUNK_SHARE;
+    sh.split = share_split(T, P, all * a.Hkv, most);
   }
-  auto place = [&](long long i, long long first, int w) {   // item i, whose blocks (of one KV head) begin at `first`
-    const long long pos = first * a.Hkv;
-    if (w == 0 || lo < pos || lo >= pos + (long long)w * a.Hkv) return;
-    sh.b = (int)(i / a.tiles);
-    sh.tile = (int)(i - (long long)sh.b * a.tiles);
-    sh.kvh = (int)(lo - pos) / w;
-    sh.pos = pos + (long long)sh.kvh * w;
-  };
   if (n <= NT) {
-    place(tid, before + incl - mine, mine);
+    share_place(a, sh, lo, tid, before + incl - mine, mine);
     return;
   }
   long long base = 0;   // weight of the items before i0
@@ -358,7 +251,7 @@ __device__ __forceinline__ void take_share(const PagedArgs& a, Share& sh, long l
       if (k < warp) before += s_sum[k];
       base += s_sum[k];
     }
-    place(i0 + tid, before + incl - w, w);
+    share_place(a, sh, lo, i0 + tid, before + incl - w, w);
   }
 }
 
@@ -499,18 +392,8 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
             if (k + 1 < jobs) job(t1, k + 1, done1, used1, done0);
           }
           ++np;
-          if (sh.split && !p.whole && p.last && lane == 0) {        // the merge of this item finds its pieces here
-            int c = (int)(p.pos * sh.P / sh.T);        // the CTA whose share holds the item's first block
-            while (c + 1 < sh.P && share_begin(sh.T, c + 1, sh.P) <= p.pos) ++c;
-            ChunkShare r;
-            r.b = p.b;
-            r.kvh = p.kvh;
-            r.tile = p.tile;
-            r.first = c;
-            r.slot = share_begin(sh.T, c, sh.P) == p.pos ? 0 : 1;
-            r.count = (int)blockIdx.x - c + 1;
-            a.share[blockIdx.x] = r;
-          }
+          // the merge of this item finds its pieces here
+          if (sh.split && !p.whole && p.last && lane == 0) a.share[blockIdx.x] = share_note(sh, p, (int)blockIdx.x);
         }
         if (np > 0) wait_phase(bar(O_DONE), (np - 1) & 1, a.err, dead);   // nothing is in flight when the CTA ends
       }
@@ -1202,13 +1085,6 @@ bool encode(CUtensorMap* tm, const void* base, int es, int d, int heads, long lo
              strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, es == 2 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
-
-// Most blocks of keys of one item.
-int chunk_blocks(const PagedArgs& a) {
-  const int span = a.window ? (int)std::min<long long>(a.nk, (long long)a.window + a.tokens) : a.nk;
-  return (span + BKEYS - 1) / BKEYS + (a.window ? 1 : 0);
-}
-bool chunk_may_share(const PagedArgs& a) { return chunk_blocks(a) > CHUNK_LEAST; }
 
 template <typename T, bool E4M3, int D>
 cudaError_t chunk_inst(const PagedArgs& a) {
