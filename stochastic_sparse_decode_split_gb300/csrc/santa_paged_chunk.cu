@@ -72,7 +72,7 @@ struct ChunkGeom {
 // Barriers.
 enum { Q_FULL, Q_READY, K_FULL, K_READY = K_FULL + 2, K_EMPTY = K_READY + 2, V_FULL = K_EMPTY + 2, V_READY = V_FULL + 2,
        V_EMPTY = V_READY + 2, S_FULL = V_EMPTY + 2, P_FULL = S_FULL + 2, O_FREE = P_FULL + 2, O_DONE = O_FREE + 2, ML_FULL,
-       Q_SEEN, N_BAR };
+       Q_SEEN, PIECE_SEEN, N_BAR };
 
 // Whether a phase is over, without waiting.
 __device__ __forceinline__ bool test_phase(uint32_t bar, unsigned parity) {
@@ -282,7 +282,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
     s_dead = 0;
     for (int i = 0; i < 4; ++i) s_bad[i] = s_odd[i] = 0;
     for (int i = 0; i < N_BAR; ++i) {
-      const int count = i == Q_READY ? 8
+      const int count = i == Q_READY || i == PIECE_SEEN ? 8
                         : i == K_READY || i == K_READY + 1 ? 4
                         : i == V_READY || i == V_READY + 1 ? (E4M3 ? 4 : 2)
                         : i == P_FULL || i == P_FULL + 1 || i == O_FREE || i == O_FREE + 1 || i == ML_FULL || i == Q_SEEN ? 4 : 1;
@@ -451,6 +451,9 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
             }
             __syncwarp();
           }
+          // No piece's sums are complete (its V is not there) before every softmax
+          // warp has seen that the previous one's were: see PIECE_SEEN below.
+          if (j == 0 && np > 0) wait_phase(bar(PIECE_SEEN), (np - 1) & 1, a.err, dead);
           if (n > 1) wait_phase(bar(V_EMPTY + st), ((n >> 1) - 1) & 1, a.err, dead);
           if (lane == 0) mbar_expect_tx(bar(V_FULL + st), bytes);
           __syncwarp();
@@ -797,20 +800,36 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       // ------------------------------------------------------- the result
       const bool join = !two && nblk > 1;          // both groups hold sums of these rows
       const bool mine = t == 0 || two;               // this group writes
+      // A wait can tell a phase from the one before it, but not from the one
+      // after.  O_DONE and ML_FULL are waited for by warps that the next piece
+      // may not need (group 1 where it is one block of one tile; group 0, whose
+      // join the other group's next one could overtake), so each softmax warp
+      // says when it is past a piece's waits: the V of the next piece is loaded,
+      // and group 1 takes part in the next join, after all eight have.  Group 1
+      // waits also where it has no part, or it could arrive twice in one phase.
+      if (!mine && nblk > 0 && np > 0) {
+        wait_phase(bar(PIECE_SEEN), (np - 1) & 1, a.err, dead);
+        __syncwarp();
+      }
       if (join && t == 1) {
         s_ml[joined & 1][0][row] = m;
         s_ml[joined & 1][1][row] = l;
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(ML_FULL));
       }
+      if (!mine && nblk > 0 && lane == 0) mbar_arrive(bar(PIECE_SEEN));
       if (mine) {
         float f0 = 1.f, f1 = 0.f;                      // weights of the two sums
         if (nblk > 0) {
           wait_phase(bar(O_DONE), np & 1, a.err, dead);
           tm_fence_after();
         }
+        if (join) wait_phase(bar(ML_FULL), joined & 1, a.err, dead);
+        if (nblk > 0) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(PIECE_SEEN));
+        }
         if (join) {
-          wait_phase(bar(ML_FULL), joined & 1, a.err, dead);
           const float m1 = s_ml[joined & 1][0][row], l1 = s_ml[joined & 1][1][row], mm = fmaxf(m, m1), mu = mm > -INFINITY ? mm : 0.f;
           f0 = fast_exp2(m - mu);
           f1 = fast_exp2(m1 - mu);

@@ -53,3 +53,20 @@ def test_across_the_border_of_sharing(kv, e4m3):
     ([4100], [1200], 10, 2, 64, torch.bfloat16, 16), ([9000], [90], 8, 1, 128, torch.bfloat16, 64)])
 def test_small_chunks(kv, n, H, Hkv, D, dtype, page, e4m3):
     check(Batch(kv, n, H, Hkv, D, dtype, e4m3, page, seed=len(kv) + kv[0]))
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("H,Hkv,D", [(16, 8, 128), (16, 16, 64)])
+def test_pieces_of_every_kind_follow_each_other(H, Hkv, D, e4m3):
+    """Items of two tiles, of one tile and several blocks (both softmax groups' sums are joined), of one tile and one block
+    (the second group has no part), and of none, in every order on a CTA: no wait may take one piece's end for another's."""
+    kinds = [(300, 90), (20, 20), (260, 30), (128, 128), (500, 200), (127, 3), (0, 2), (40, 40), (250, 250), (90, 1)]
+    order = [kinds[i * j % 11 - 1] for j in range(1, 11) for i in range(1, 11)]
+    batch = Batch([kv for kv, _ in order], [n for _, n in order], H, Hkv, D, torch.bfloat16, e4m3, 16, seed=H)
+    check(batch)
+    step = batch.step()
+    good = [x.clone() for x in step.attend(batch.q, return_lse=True)]
+    for _ in range(100):
+        out, lse = step.attend(batch.q, return_lse=True)
+    assert step.error() == 0
+    assert torch.equal(out, good[0]) and torch.equal(lse, good[1])
