@@ -7,6 +7,7 @@
 #include <stdint.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "santa_common.cuh"
 
@@ -24,6 +25,20 @@ constexpr int ERR_POSITION = 64;   // a position past the rotation table
 // a NaN or an infinity makes its row of values NaN.
 constexpr float V_SCALE_LEAST = 8.673617379884035e-19f / 448.f;
 __device__ __forceinline__ bool odd_scale(float v) { return !(v >= 0.f && v <= 3.402823466e38f); }
+
+// Probabilities that enter their product in fp16 are taken relative to a
+// maximum lowered by this much (base 2).  With the largest at 1, those below
+// 2^-14 (the weights of a context of tens of thousands of keys) would be held in
+// steps of 2^-24, and those below 2^-25 be lost, however many they are.  At 2^15
+// nothing overflows for the kernel for few rows, at 2^7 for chunks, whose
+// probabilities grow by 2^8 before the maximum follows; the rounding of one then
+// is at most 2^-40 or 2^-32 of the largest.  bf16 has the range without.
+constexpr float TOKENS_BIAS = 15.f, CHUNK_BIAS = 7.f;
+template <typename M16> __host__ __device__ constexpr float fp16_bias(float bias) { return std::is_same<M16, fp16_t>::value ? bias : 0.f; }
+// The natural logarithm of sum l relative to maximum m (base 2), which is `bias` below the true one.
+__device__ __forceinline__ float log_sum(float m, float l, float bias) {
+  return (m + bias) * 0.6931471805599453f + __logf(l * __int_as_float((127 - (int)bias) << 23));
+}
 
 constexpr int PG_BLK = 16;         // keys per block: no block crosses a page (the smallest page is one block)
 

@@ -13,7 +13,7 @@
 //   warps 0-3, 4-7  softmax of tile 0 and 1: one thread per row.  S comes out
 //                   of tensor memory, P goes back over it in 16 bits, the sum
 //                   O is rescaled only when the maximum has grown by 2^8
-//                   (probabilities stay below 256, the result is the same)
+//                   (probabilities stay within a factor of 256, the result is the same)
 //   warp 8          issues the products: S_t = Q_t K^T and O_t += P_t V, so
 //                   that one tile's products run during the other's softmax
 //   warp 9          TMA: pages of K and V into two stages each (128-byte swizzle)
@@ -262,6 +262,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                    const __grid_constant__ CUtensorMap tmV, PagedArgs a) {
   using Gm = ChunkGeom<E4M3, D>;
   using M16 = typename std::conditional<E4M3, fp16_t, T>::type;
+  constexpr float BIAS = fp16_bias<M16>(CHUNK_BIAS);
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   __shared__ __align__(8) unsigned long long s_bar[N_BAR];
   __shared__ Share sh;
@@ -741,7 +742,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             mx[e] = fmaxf(fmaxf(mx[e], __uint_as_float(sr[c + 2 * e])), __uint_as_float(sr[c + 2 * e + 1]));
-        const float mn = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * (E4M3 ? 1.f : sl));
+        const float mn = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * (E4M3 ? 1.f : sl) - BIAS);
         if (j == j_first) {
           m = mn;
         } else if (__any_sync(FULL, mn > m + RESCALE)) {
@@ -906,7 +907,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
             a.part_ml[2 * part] = m;
             a.part_ml[2 * part + 1] = bad ? -1.f : l;
           } else if (a.lse) {
-            a.lse[at] = empty ? -INFINITY : m * 0.6931471805599453f + __logf(l);
+            a.lse[at] = empty ? -INFINITY : log_sum(m, l, BIAS);
           }
         }
         if (odd) {
@@ -1075,7 +1076,7 @@ __global__ void __launch_bounds__(512, 2) chunk_merge_kernel(PagedArgs a) {
     uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<T*>(a.out) + at * D + lane * E);
 #pragma unroll
     for (int e = 0; e < E; e += 2) dst[e / 2] = empty ? 0u : pack2h<T>(o[i][e] * inv, o[i][e + 1] * inv);
-    if (a.lse && lane == 0) a.lse[at] = empty ? -INFINITY : m[i] * 0.6931471805599453f + __logf(l[i]);
+    if (a.lse && lane == 0) a.lse[at] = empty ? -INFINITY : log_sum(m[i], l[i], a.e4m3 ? CHUNK_BIAS : fp16_bias<T>(CHUNK_BIAS));
   }
 }
 

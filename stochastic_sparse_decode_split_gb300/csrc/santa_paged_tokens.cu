@@ -23,7 +23,7 @@
 // down to 2^-24 of it (smaller ones lose bits that 32-bit sums do not see
 // either).  A key's score is multiplied by its k_scale; its v_scale enters as
 // log2 v_scale beside the score, so that P = 2^(s + log2 v_scale - m) stays in
-// [0, 1] whatever the scales are, and the sum of the softmax collects
+// range whatever the scales are, and the sum of the softmax collects
 // P / v_scale.
 #include <algorithm>
 #include <type_traits>
@@ -122,6 +122,7 @@ __global__ void __launch_bounds__(NT, E4M3 ? 3 : 2) paged_tokens_kernel(PagedArg
   using Gm = Geom<E4M3, D>;
   using M16 = typename std::conditional<E4M3, fp16_t, T>::type;   // the products' type
   constexpr int NS = Gm::NS, NB = R / 8;
+  constexpr float BIAS = fp16_bias<M16>(TOKENS_BIAS);
   extern __shared__ __align__(128) unsigned char smem_raw[];
   __shared__ float s_m[NW][R], s_l[NW][R];
   __shared__ int s_bad;
@@ -370,7 +371,7 @@ __global__ void __launch_bounds__(NT, E4M3 ? 3 : 2) paged_tokens_kernel(PagedArg
           m = fmaxf(m, __shfl_xor_sync(FULL, m, 4));
           m = fmaxf(m, __shfl_xor_sync(FULL, m, 8));
           m = fmaxf(m, __shfl_xor_sync(FULL, m, 16));
-          const float mn = fmaxf(rm[nb][hh], m), mu = mn > -INFINITY ? mn : 0.f;
+          const float mn = fmaxf(rm[nb][hh], m - BIAS), mu = mn > -INFINITY ? mn : 0.f;
           alpha[nb][hh] = fast_exp2(rm[nb][hh] - mu);
           rm[nb][hh] = mn;
           float sum = 0.f;
@@ -569,7 +570,7 @@ __global__ void __launch_bounds__(NT, E4M3 ? 3 : 2) paged_tokens_kernel(PagedArg
       w.x = bad || l == 0.f ? 0u : Pack<T>::pack(o.x * inv, o.y * inv);
       w.y = bad || l == 0.f ? 0u : Pack<T>::pack(o.z * inv, o.w * inv);
       *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + at * D + d) = w;
-      if (a.lse && d == 0) a.lse[at] = bad || l == 0.f ? -INFINITY : m * 0.6931471805599453f + __logf(l);
+      if (a.lse && d == 0) a.lse[at] = bad || l == 0.f ? -INFINITY : log_sum(m, l, BIAS);
     } else {
       *reinterpret_cast<float4*>(a.part_o + (part + r) * D + d) = o;
       if (d == 0) {
@@ -674,7 +675,7 @@ __global__ void __launch_bounds__(128) paged_merge_kernel(PagedArgs a) {
   uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<T*>(a.out) + at * D + lane * E);
 #pragma unroll
   for (int e = 0; e < E; e += 2) dst[e / 2] = empty ? 0u : Pack<T>::pack(o[e] * inv, o[e + 1] * inv);
-  if (a.lse && lane == 0) a.lse[at] = empty ? -INFINITY : m * 0.6931471805599453f + __logf(l);
+  if (a.lse && lane == 0) a.lse[at] = empty ? -INFINITY : log_sum(m, l, a.e4m3 ? TOKENS_BIAS : fp16_bias<T>(TOKENS_BIAS));
 }
 
 template <typename T, bool E4M3, int D, int R>
