@@ -632,6 +632,11 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       const bool two = pc.two;
       const int step = two ? 1 : 2;
       int lo, hi, lo_last, hi_first;                   // keys that the row sees; that every row of the tile sees
+      // The row's maximum that P and O are relative to.  Infinite for rows past
+      // the tile's tokens, which hold other tokens or whatever was there: so
+      // they never ask for a rescaling, and the rounding of the others does not
+      // depend on them.
+      float m;
       {
         const int first_pos = pc.s.kv - pc.s.n;
         const int ta = pc.i0 + (two ? t * per : 0), tb = min(ta + per, pc.s.n) - 1;   // the tile's tokens
@@ -639,6 +644,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         visible_keys(a, pc.s.kv, first_pos + min(ta + row / a.G, tb), lo, hi);   // rows past the last compute it again, for nothing
         visible_keys(a, pc.s.kv, first_pos + ta, none, hi_first);
         visible_keys(a, pc.s.kv, first_pos + tb, lo_last, none);
+        m = row < (tb - ta + 1) * a.G ? -INFINITY : INFINITY;
       }
       float sl = a.sl2;
       if (E4M3 && nblk > 0) {
@@ -693,7 +699,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
           sl = s_sl[row];
         }
       }
-      float m = -INFINITY, l = 0.f;   // the row's maximum that P and O are relative to, and sum
+      float l = 0.f;                // the row's sum
       const int j_first = two ? 0 : t;
       f2x l2[E4M3 ? 2 : 4];         // chains of additions: one would take longer than the exponentials
 #pragma unroll
