@@ -138,7 +138,16 @@ __global__ void __launch_bounds__(128, sizeof(T) == 4 ? 5 : E4M3 ? 7 : 8) kv_app
   constexpr int U = 4;   // groups in flight; of a key-value run two of each
   const int lane = threadIdx.x & 31, sub = lane % LPR, rr = lane / LPR;
   const long long t = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
-  if (t >= a.total_q) return;
+  if (t >= a.total_q) {
+    // CTAs past the tokens look the sequences over: one without tokens, or
+    // whose offsets no token finds, would be refused by nobody
+    const long long i = ((long long)blockIdx.x - (a.total_q + 3) / 4) * 128 + threadIdx.x;
+    if (blockIdx.y == 0 && i >= 0 && i < a.B) {
+      const Seq s = paged_seq(a, (int)i, true);
+      if (s.ok && s.n > s.kv) flag_error(a.err, ERR_CHUNK);
+    }
+    return;
+  }
   const bool is_q = (int)blockIdx.y < qparts;
   const int part = is_q ? blockIdx.y : blockIdx.y - qparts;
   const int heads = is_q ? a.H : a.Hkv;
@@ -166,12 +175,8 @@ __global__ void __launch_bounds__(128, sizeof(T) == 4 ? 5 : E4M3 ? 7 : 8) kv_app
 
   int b;
   if (!paged_seq_of(a, t, b)) return;
-  const Seq s = paged_seq(a, b, lane == 0);
-  if (!s.ok) return;
-  if (s.n > s.kv) {
-    if (lane == 0) flag_error(a.err, ERR_CHUNK);
-    return;
-  }
+  const Seq s = paged_seq(a, b, false);
+  if (!s.ok || s.n > s.kv) return;
   const int pos = s.kv - s.n + (int)(t - s.q0);
   if (p.rotated && pos >= p.rope_positions) {
     if (lane == 0) flag_error(a.err, ERR_POSITION);
@@ -423,7 +428,7 @@ cudaError_t append_inst(const PagedArgs& a, const AppendArgs& p) {
   const bool many = a.total_q * (gq + 2 * gkv) >= 64ll * a.num_sms;
   const int qparts = many ? (gq + 7) / 8 : gq, kvparts = many ? (gkv + 3) / 4 : gkv;
   const int qg = qparts ? (gq + qparts - 1) / qparts : 1, kvg = (gkv + kvparts - 1) / kvparts;
-  const dim3 grid((unsigned)((a.total_q + 3) / 4), (unsigned)(qparts + kvparts));
+  const dim3 grid((unsigned)((a.total_q + 3) / 4 + (a.B + 127) / 128), (unsigned)(qparts + kvparts));
   if (p.interleaved) kv_append_kernel<T, D, E4M3, true><<<grid, 128, 0, a.stream>>>(a, p, qparts, qg, kvg);
   else kv_append_kernel<T, D, E4M3, false><<<grid, 128, 0, a.stream>>>(a, p, qparts, qg, kvg);
   return cudaGetLastError();
