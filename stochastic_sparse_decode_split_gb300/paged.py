@@ -336,8 +336,13 @@ class PagedStep:
     def sample(self, q, S: int, kv_offsets, rows: int, *, variant: str = "systematic", seed: int = 0, step: int = 0,
                sample_idx=None, stream=None):
         """One S2ANTA / SANTA decode step over the paged cache: its rows read back packed (kv_offsets the exclusive
-        sums of kv_lens), then santa_decode on them.  q [B, n_q_heads, head_dim]; the result is float32."""
+        sums of kv_lens), then santa_decode on them, for steps of one token per sequence that sees all of its keys.
+        q [B, n_q_heads, head_dim]; the result is float32."""
         from . import santa_decode
+        if self.total_q != self.batch:
+            raise ValueError("sample takes steps of one token per sequence")
+        if 0 < self.p.window < self.nk:
+            raise ValueError("sample knows no window: it would draw from keys that the token does not see")
         with torch.cuda.device(self.device), torch.cuda.stream(stream):
             K, V = self.read(kv_offsets, rows)
             return santa_decode(q, K, V, S, variant=variant, seed=seed, step=step, nk=self.nk, kv_offsets=kv_offsets,

@@ -54,3 +54,16 @@ def test_more_tokens_than_keys_of_the_last_of_many():
     assert append(batch, step) == (400, 0)
     batch.kv_t[199] = 1
     assert append(batch, step) == (398, santa.CACHE_DEVERR_CHUNK)
+
+
+def test_sampling_refuses_what_it_would_answer_otherwise_than_the_attention():
+    batch = Batch([40, 30], [1, 1], 2, 2, 64, BF16, False, 16, seed=1)
+    offsets = torch.tensor([0, 40, 70], device="cuda")
+    for window in (1, 39):
+        with pytest.raises(ValueError, match="window"):
+            batch.step(window=window).sample(batch.q, 8, offsets, 70)
+    wide = batch.step(window=40).sample(batch.q, 8, offsets, 70, seed=3)   # no key is outside of it
+    assert torch.equal(wide, batch.step().sample(batch.q, 8, offsets, 70, seed=3))
+    two = Batch([40, 30], [2, 2], 2, 2, 64, BF16, False, 16, seed=1)
+    with pytest.raises(ValueError, match="one token"):
+        two.step().sample(two.q[:2], 8, offsets, 70)
