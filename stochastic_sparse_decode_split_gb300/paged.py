@@ -162,8 +162,9 @@ class PagedStep:
     [B + 1] (None: max_q new tokens each).  All three are read by the GPU when a call runs and may be changed in place
     between calls; nk and max_q bound what they may hold.  Calls of one step share its workspace: order them on one
     stream.  Outputs that a call is not given are the step's own, as ``Decoder``'s: its next such call on that stream
-    overwrites them.  Keep the step while graphs that captured its calls are used.  ``error()`` reports what the device
-    refused."""
+    overwrites them.  Keep the step while graphs that captured its calls are used; otherwise it may go while its calls
+    still run, on whichever streams (tensors given to a call with ``stream=`` are the caller's to keep until it has run).
+    ``error()`` reports what the device refused."""
 
     def __init__(self, cache: PagedCache, page_table, kv_lens=None, *, n_q_heads: int, dtype=None,
                  nk: Optional[int] = None, max_q: int = 1, total_q: Optional[int] = None, q_offsets=None,
@@ -206,6 +207,9 @@ class PagedStep:
             if n == 0:
                 raise ValueError("invalid paged parameters")
             self.workspace = alloc_workspace(n, self.device)
+            # the stream that clears the workspace's error word, and when it has
+            self._streams = {torch._C._cuda_getCurrentRawStream(self.device.index)}
+            self._cleared = None if _capturing() else torch.cuda.current_stream().record_event()
         # what every call checks and passes again: shapes, the pool (whose tensors the cache keeps), the workspace
         self._index = self.device.index
         self._outputs, self._captured = {}, []
@@ -242,7 +246,23 @@ class PagedStep:
         """The raw stream of a call: the given one, or the device's current one."""
         if _current_device() != self._index:
             raise ValueError("make the cache's device the current one for its calls")
-        return torch._C._cuda_getCurrentRawStream(self._index) if stream is None else stream.cuda_stream
+        raw = torch._C._cuda_getCurrentRawStream(self._index) if stream is None else stream.cuda_stream
+        if raw not in self._streams:
+            self._meet(raw, stream)
+        return raw
+
+    def _meet(self, raw, stream):
+        """The first call on a stream other than the step's own: behind the clearing of the error word, and what the step
+        holds goes back to the allocator, when it is dropped, only after what that stream does with it."""
+        with torch.cuda.stream(stream):
+            on = torch.cuda.current_stream()
+            for t in (self.workspace, self.page_table, self.kv_lens, self.q_offsets, *self._kept):
+                if t is not None:
+                    t.record_stream(on)
+            if not _capturing():   # a capture takes no event from outside; it begins with a synchronisation
+                if self._cleared is not None:
+                    on.wait_event(self._cleared)
+                self._streams.add(raw)
 
     def _own(self, name, raw, shape, dtype, stream):
         """The step's own output of that name for calls on that stream (making one anew costs as much as a call)."""
