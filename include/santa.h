@@ -359,7 +359,8 @@ santa_status_t santa_paged_attention(const santa_paged_t* p, const void* q, cons
  * [rows, n_kv_heads, head_dim] in dtype: key n of sequence b in row
  * kv_offsets[b] + n (device int64 [batch + 1]; NULL = b * nk, rows >=
  * batch * nk), e4m3 rows multiplied out and rounded once.  Rows past a
- * sequence's last key are left as they were.  With kv_offsets the exclusive
+ * sequence's last key are left as they were.  A batch of empty sequences has
+ * no rows, and K_out and V_out may then be NULL.  With kv_offsets the exclusive
  * sums of kv_lens, K_out, V_out and kv_offsets are what santa_decode takes. */
 santa_status_t santa_kv_read(const santa_paged_t* p, const void* K, const void* V, const float* k_scale,
                              const float* v_scale, const int64_t* kv_offsets, int64_t rows, void* K_out, void* V_out,

@@ -225,7 +225,8 @@ santa_status_t santa_kv_read(const santa_paged_t* p, const void* K, const void* 
   if (st != SANTA_OK) return st;
   st = check_cache(p, K, V, k_scale, v_scale, workspace, ws_bytes, HEADER);
   if (st != SANTA_OK) return st;
-  if (!K_out || !V_out || !aligned(K_out, 16) || !aligned(V_out, 16) || !aligned(kv_offsets, 8)) return SANTA_ERR_INVALID_ARG;
+  if ((rows != 0 && (!K_out || !V_out)) || !aligned(K_out, 16) || !aligned(V_out, 16) || !aligned(kv_offsets, 8))
+    return SANTA_ERR_INVALID_ARG;
   if (rows < 0 || (!kv_offsets && rows < p->batch * p->nk)) return SANTA_ERR_INVALID_ARG;
   santa::PagedArgs a = args(p);
   a.K = K;
