@@ -18,6 +18,7 @@ import torch
 CACHE_DEVERR_PAGE, CACHE_DEVERR_CHUNK, CACHE_DEVERR_POSITION = 16, 32, 64   # SANTA_CACHE_DEVERR_* in santa.h
 E4M3 = 3                                                                   # SANTA_E4M3
 PAGE_SIZES = (16, 32, 64, 128, 256)
+KEPT_ROWS_BYTES = 1 << 24   # packed rows up to this are the step's own: making them anew costs 3 us, writing them 3 us and more
 
 
 class PagedParams(ctypes.Structure):
@@ -162,7 +163,7 @@ class PagedStep:
     [B + 1] (None: max_q new tokens each).  All three are read by the GPU when a call runs and may be changed in place
     between calls; nk and max_q bound what they may hold.  Calls of one step share its workspace: order them on one
     stream.  Outputs that a call is not given are the step's own, as ``Decoder``'s: its next such call on that stream
-    overwrites them.  Keep the step while graphs that captured its calls are used; otherwise it may go while its calls
+    overwrites them (packed rows of more than 16 MiB are made anew by each ``read``, and are not kept).  Keep the step while graphs that captured its calls are used; otherwise it may go while its calls
     still run, on whichever streams (tensors given to a call with ``stream=`` are the caller's to keep until it has run).
     ``error()`` reports what the device refused."""
 
@@ -264,12 +265,15 @@ class PagedStep:
                     on.wait_event(self._cleared)
                 self._streams.add(raw)
 
-    def _own(self, name, raw, shape, dtype, stream):
-        """The step's own output of that name for calls on that stream (making one anew costs as much as a call)."""
+    def _own(self, name, raw, shape, dtype, stream, most=None):
+        """The step's own output of that name for calls on that stream (making one anew costs as much as a call).  One
+        of more than ``most`` bytes is not kept, and takes the place of the one that was."""
         x = self._outputs.get((name, raw))
         if x is None or x.shape != shape:
             with torch.cuda.stream(stream):
                 x = self._outputs[name, raw] = torch.empty(shape, dtype=dtype, device=self.device)
+            if most is not None and x.nbytes > most:
+                del self._outputs[name, raw]
         return x
 
     @staticmethod
@@ -344,9 +348,9 @@ class PagedStep:
         shape = (rows, self._kv_shape[1], self._kv_shape[2])
         own = K_out is None or V_out is None
         if K_out is None:
-            K_out = self._own("K", raw, shape, self.dtype, stream)
+            K_out = self._own("K", raw, shape, self.dtype, stream, KEPT_ROWS_BYTES)
         if V_out is None:
-            V_out = self._own("V", raw, shape, self.dtype, stream)
+            V_out = self._own("V", raw, shape, self.dtype, stream, KEPT_ROWS_BYTES)
         if own and _capturing():
             self._captured.append((K_out, V_out))   # a later call with other rows replaces them; the graph still writes these
         self._check(self._read_fn(self._ref, *self._pool, off_ptr, rows, self._dense(K_out, shape, self.dtype, "K_out"),

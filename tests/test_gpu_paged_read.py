@@ -28,3 +28,44 @@ def test_a_batch_of_empty_sequences_has_no_rows(e4m3):
     batch.kv_t[1] = 1                      # a key, and no row for it
     step.read(offsets, 0)
     assert step.error() == santa.CACHE_DEVERR_CHUNK
+
+
+@pytest.mark.parametrize("sampled", [True, False])
+def test_packed_copies_of_long_contexts_are_not_kept(sampled):
+    batch = Batch([9000], [1], 8, 8, 128, BF16, False, 64, seed=2)
+    step = batch.step()
+    offsets = torch.tensor([0, 9000], device="cuda")
+
+    def run():
+        return step.sample(batch.q, 8, offsets, 9000) if sampled else step.read(offsets, 9000)
+
+    torch.cuda.synchronize()
+    held = torch.cuda.memory_allocated()
+    first = run()
+    if not sampled:
+        want = [batch.rows(0, "K"), batch.rows(0, "V")]
+        second = run()
+        assert not {x.data_ptr() for x in first} & {x.data_ptr() for x in second}
+        assert all(torch.equal(x.double(), w) and torch.equal(y.double(), w) for x, y, w in zip(first, second, want))
+        del second, want
+    del first
+    torch.cuda.synchronize()
+    assert torch.cuda.memory_allocated() - held < 1 << 20
+
+
+def test_a_captured_read_of_a_long_context_keeps_its_outputs():
+    batch = Batch([9000], [1], 8, 8, 128, BF16, False, 64, seed=2)
+    step = batch.step()
+    offsets = torch.tensor([0, 9000], device="cuda")
+    step.read(offsets, 9000)
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        K, V = step.read(offsets, 9000)
+    at = (K.data_ptr(), V.data_ptr())
+    del K, V
+    others = [torch.full((9000, 8, 128), 3.0, dtype=BF16, device="cuda") for _ in range(6)]
+    assert not any(x.data_ptr() in at for x in others)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(bool((x == 3.0).all()) for x in others) and step.error() == 0
+    assert torch.equal(step._captured[0][0].double(), batch.rows(0, "K"))
