@@ -69,6 +69,14 @@ _APPEND = struct.Struct("@PPPqqqPPPfPqii")   # AppendParams' fields in their ord
 _current_device, _capturing = torch.cuda.current_device, torch.cuda.is_current_stream_capturing
 
 
+def _captures(stream) -> bool:
+    """Whether calls on that stream (None: the current one) go into a graph."""
+    if stream is None:
+        return _capturing()
+    with torch.cuda.stream(stream):
+        return _capturing()
+
+
 def declare(lib) -> None:
     """Argument types of the paged entry points."""
     vp, sz, i64 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int64
@@ -351,7 +359,7 @@ class PagedStep:
             K_out = self._own("K", raw, shape, self.dtype, stream, KEPT_ROWS_BYTES)
         if V_out is None:
             V_out = self._own("V", raw, shape, self.dtype, stream, KEPT_ROWS_BYTES)
-        if own and _capturing():
+        if own and _captures(stream):
             self._captured.append((K_out, V_out))   # a later call with other rows replaces them; the graph still writes these
         self._check(self._read_fn(self._ref, *self._pool, off_ptr, rows, self._dense(K_out, shape, self.dtype, "K_out"),
                                   self._dense(V_out, shape, self.dtype, "V_out"), *self._ws, raw), "santa_kv_read")

@@ -69,3 +69,22 @@ def test_a_captured_read_of_a_long_context_keeps_its_outputs():
     torch.cuda.synchronize()
     assert all(bool((x == 3.0).all()) for x in others) and step.error() == 0
     assert torch.equal(step._captured[0][0].double(), batch.rows(0, "K"))
+
+
+def test_a_read_captured_on_a_stream_that_is_not_the_current_one():
+    """As on the current one: the buffers that the graph writes to stay, though the step makes others."""
+    batch = Batch([500, 300], [1, 1], 4, 2, 64, BF16, False, 16, seed=11)
+    step = batch.step()
+    offsets = torch.tensor([0, 500, 800], device="cuda")
+    side, other, graph = torch.cuda.Stream(), torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    at = {x.data_ptr() for x in step.read(offsets, 800, stream=side)}
+    with torch.cuda.graph(graph, stream=side):
+        with torch.cuda.stream(other):
+            assert {x.data_ptr() for x in step.read(offsets, 800, stream=side)} == at
+    with torch.cuda.stream(side):
+        step.read(offsets, 900)
+        others = [torch.full((800, 2, 64), 3.0, dtype=BF16, device="cuda") for _ in range(8)]
+        assert not {x.data_ptr() for x in others} & at
+        graph.replay()
+        side.synchronize()
+    assert all(bool((x == 3.0).all()) for x in others) and step.error() == 0
