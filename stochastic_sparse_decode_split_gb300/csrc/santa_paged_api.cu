@@ -40,7 +40,7 @@ santa_status_t check(const santa_paged_t* p) {
   if (p->batch < 1 || p->batch > 65535 || p->n_q_heads < 1 || p->n_kv_heads < 1) return SANTA_ERR_INVALID_ARG;
   if (p->n_q_heads > 65535 || p->n_q_heads % p->n_kv_heads) return SANTA_ERR_INVALID_ARG;
   if (p->nk < 1 || p->nk > SANTA_MAX_NK || p->max_q < 1 || p->total_q < 1 || p->total_q > INT32_MAX) return SANTA_ERR_INVALID_ARG;
-  if (p->max_q > p->total_q || (!p->q_offsets && p->total_q != (int64_t)p->batch * p->max_q)) return SANTA_ERR_INVALID_ARG;
+  if (!p->q_offsets && p->total_q != (int64_t)p->batch * p->max_q) return SANTA_ERR_INVALID_ARG;
   if (p->n_pages < 1 || p->max_pages < 1) return SANTA_ERR_INVALID_ARG;
   if (p->page_size < 16 || p->page_size > 256 || (p->page_size & (p->page_size - 1))) return SANTA_ERR_UNSUPPORTED;
   if ((int64_t)p->n_pages * p->page_size > INT32_MAX || (int64_t)p->max_pages * p->page_size < p->nk)
@@ -83,7 +83,7 @@ santa::PagedArgs args(const santa_paged_t* p) {
   a.kv_lens = p->kv_lens;
   a.q_offsets = p->q_offsets;
   a.nk = (int)p->nk;
-  a.max_q = p->max_q;
+  a.max_q = (int)std::min<int64_t>(p->max_q, p->total_q);   // as an upper bound it may be above
   a.total_q = p->total_q;
   a.causal = p->causal;
   a.window = p->window < p->nk ? p->window : 0;   // one that no key is outside of is none

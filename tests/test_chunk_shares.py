@@ -66,7 +66,7 @@ def test_drawn_batches(walk):
         chunk = rng.choice((3, 20, 130, 700, 2100))
         n = [rng.randint(0 if rng.random() < 0.1 else 1, chunk) for _ in range(B)]
         n[0] = max(n[0], 1)
-        H, Hkv = rng.choice(((32, 8), (28, 4), (16, 2), (8, 2), (6, 2), (10, 2), (5, 1), (16, 16), (64, 1), (3, 3)))
+        H, Hkv = rng.choice(((32, 8), (28, 4), (16, 2), (8, 2), (6, 2), (10, 2), (5, 1), (16, 16), (8, 1), (3, 3)))
         causal = rng.random() < 0.8
         calls.append((kv, n, H, Hkv, causal, rng.choice((0, 0, rng.randint(1, top))) if causal else 0,
                       rng.choice((CTAS, CTAS, 148, 132, 7))))

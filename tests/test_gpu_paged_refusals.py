@@ -3,7 +3,7 @@ import pytest
 import torch
 
 import stochastic_sparse_decode_split_gb300 as santa
-from paged_reference import Batch
+from paged_reference import Batch, check_attention
 
 pytestmark = pytest.mark.gpu
 BF16 = torch.bfloat16
@@ -67,3 +67,17 @@ def test_sampling_refuses_what_it_would_answer_otherwise_than_the_attention():
     two = Batch([40, 30], [2, 2], 2, 2, 64, BF16, False, 16, seed=1)
     with pytest.raises(ValueError, match="one token"):
         two.step().sample(two.q[:2], 8, offsets, 70)
+
+
+@pytest.mark.parametrize("n", [3, 150])
+def test_a_bound_above_the_number_of_tokens_is_none(n):
+    batch = Batch([3000, 2000], [n, 0], 8, 4, 64, BF16, False, 16, seed=1)
+    step = santa.PagedStep(batch.cache(), batch.table, batch.kv_t, n_q_heads=8, nk=3000, max_q=4096, total_q=n,
+                           q_offsets=batch.offsets)
+    out, lse = step.attend(batch.q, return_lse=True)
+    assert step.error() == 0
+    check_attention(batch, out, lse)
+    k = torch.ones(n, 4, 64, dtype=BF16, device="cuda")
+    step.append(None, k, k)
+    K, _ = step.read(torch.tensor([0, 3000, 5000], device="cuda"), 5000)
+    assert step.error() == 0 and bool((K[3000 - n:3000] == 1).all())

@@ -1,7 +1,10 @@
 """What the paged cache's binding refuses by itself, without a GPU."""
+import ctypes
+
 import pytest
 
-from stochastic_sparse_decode_split_gb300 import paged
+import stochastic_sparse_decode_split_gb300 as santa
+from stochastic_sparse_decode_split_gb300 import build, paged
 
 
 def bare(batch=2, total_q=2, nk=100, window=0):
@@ -17,3 +20,23 @@ def bare(batch=2, total_q=2, nk=100, window=0):
 def test_sampling_refuses_windows_and_chunks(kw, what):
     with pytest.raises(ValueError, match=what):
         bare(**kw).sample(None, 8, None, 100)
+
+
+def test_a_bound_above_the_number_of_tokens_needs_the_workspace_of_the_tokens():
+    """max_q bounds the tokens of a sequence where q_offsets say how many there are: it may be above all of them."""
+    build.build()
+    lib = santa.library()
+
+    def size(**kw):
+        p = paged.PagedParams()
+        p.batch, p.n_q_heads, p.n_kv_heads, p.head_dim, p.dtype, p.cache_dtype = 2, 32, 8, 128, 0, 0
+        p.page_size, p.n_pages, p.page_table, p.max_pages, p.kv_lens, p.nk = 16, 4096, 4096, 2048, 4096, 30000
+        p.q_offsets, p.max_q, p.total_q, p.causal = 4096, 300, 300, 1
+        for k, v in kw.items():
+            setattr(p, k, v)
+        return lib.santa_paged_workspace_size(ctypes.byref(p))
+
+    assert size() > 0
+    assert {size(max_q=m) for m in (301, 2048, 2 ** 31 - 1)} == {size()}
+    assert size(total_q=5, max_q=2048) == size(total_q=5, max_q=5) > 0
+    assert size(q_offsets=None) == size(q_offsets=None, max_q=301) == 0 < size(q_offsets=None, max_q=150)
