@@ -37,7 +37,7 @@ struct Piece {
   long long pos;      // the item's first block
 };
 struct Walk {
-  int b, kvh, tile, of, i0, i1;
+  int b, kvh, tile, i0, i1;
   TileKeys tk;
   long long pos;
   Seq s;
