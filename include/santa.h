@@ -308,8 +308,8 @@ typedef struct {
 #define SANTA_CACHE_DEVERR_CHUNK 32
 #define SANTA_CACHE_DEVERR_POSITION 64
 
-/* Byte size of the workspace of the three calls (0 when p is invalid).  Of
- * p's pointers it only matters whether q_offsets is NULL. */
+/* Byte size of the workspace of the three calls on the current device (0 when p
+ * is invalid).  Of p's pointers it only matters whether q_offsets is NULL. */
 size_t santa_paged_workspace_size(const santa_paged_t* p);
 
 /* What santa_kv_append does to the new tokens on their way. */
@@ -339,13 +339,16 @@ santa_status_t santa_kv_append(const santa_paged_t* p, const santa_append_t* a, 
 
 /* out = softmax(scale q K^T + mask) V over the pages, exact: the new tokens'
  * queries q [total_q, n_q_heads, head_dim] against the keys of their
- * sequences, which the cache already holds.  dtype SANTA_BF16 or SANTA_FP16.
+ * sequences, which the cache already holds.  dtype SANTA_BF16 or SANTA_FP16
+ * (a cache of fp32 is written and read back only).
  *   out  [total_q, n_q_heads, head_dim] in dtype; may be q itself
  *   lse  optional float32 [total_q, n_q_heads]: the natural logarithm of the
  *        sum of exp(scale q k) over the visible keys
  * A token that sees no key (an empty sequence; more new tokens than keys) gets
  * zeros and -infinity.  Scores, the running maximum and sum, and the sum over
- * the values are float32; probabilities enter the second product in 16 bits.
+ * the values are float32; probabilities enter the second product rounded to
+ * 16 bits (bf16 for a bf16 cache; else fp16, off by 2^-11 of themselves or
+ * 2^-32 of the largest at most).
  * What masked keys hold, NaN and infinities included, does not matter.
  * A v_scale below 2^-60 / 448, the smallest that santa_kv_append writes, is
  * taken as that; a negative, infinite or NaN one makes its row's values NaN

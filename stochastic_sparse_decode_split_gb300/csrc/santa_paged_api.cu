@@ -1,5 +1,5 @@
 // santa_paged_api.cu -- C ABI of the paged cache: host-side validation (all of
-// it before any CUDA call), workspace layout and the launches.
+// it before any launch), workspace layout and the launches.
 #include <limits.h>
 #include <math.h>
 #include <string.h>

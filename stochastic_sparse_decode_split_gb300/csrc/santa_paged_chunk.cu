@@ -8,8 +8,8 @@
 // of K and V the products bound the kernel, then the exponentials, then the
 // L2; HBM does not.  One CTA per SM; each takes an equal share of the blocks
 // of the whole batch, counted from the lengths on the device, so a CTA's share
-// may begin or end inside an item, whose sums then go through memory (see
-// Walk).  Roles:
+// may begin or end inside an item, whose sums then go through memory
+// (santa_chunk_share.cuh has the division).  Roles:
 //   warps 0-3, 4-7  softmax of tile 0 and 1: one thread per row.  S comes out
 //                   of tensor memory, P goes back over it in 16 bits, the sum
 //                   O is rescaled only when the maximum has grown by 2^8
@@ -32,9 +32,9 @@
 // complete therefore says that the O of the same tile is too, which is when
 // the softmax may rescale it.
 //
-// Measured: 2048 tokens at 32768 keys, 32 and 8 heads of 128, bf16: 766 to 788
+// Measured: 2048 tokens at 32768 keys, 32 and 8 heads of 128, bf16: 763 to 788
 // us, 1.35 to 1.39 PFLOP/s (0.70 to 0.72 of a library product's rate; the clock
-// falls from 1.86 to 1.74 GHz as the tensor cores fill); six chunks of up to 700
+// falls from 1.86 to 1.74 GHz as the tensor cores fill, 700 us before); six chunks of up to 700
 // tokens over e4m3 in a window of 4096: 200 us.  There a block takes 4900
 // cycles: softmax 3100, issue of the products 1300, hand-overs 500 one after
 // another for a tile, the other tile in between; K left in e4m3, for products
@@ -711,7 +711,8 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         uint32_t sr[BKEYS];
         if (E4M3) {
           // a key's three factors from shared memory: 96 loads of 16 bytes per
-          // thread, which take 3000 cycles per block (128 bytes a cycle)
+          // thread, at 128 bytes a cycle 3000 cycles for the eight warps of
+          // both tiles, of which one tile waits for 1200 of its 3100
           const uint32_t sc = base + Gm::OFF_SC + ((n + j) & 3) * Gm::SC_STAGE;
           const f2x sl_2 = pack2(sl, sl);
 #pragma unroll

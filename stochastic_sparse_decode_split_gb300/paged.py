@@ -18,7 +18,7 @@ import torch
 CACHE_DEVERR_PAGE, CACHE_DEVERR_CHUNK, CACHE_DEVERR_POSITION = 16, 32, 64   # SANTA_CACHE_DEVERR_* in santa.h
 E4M3 = 3                                                                   # SANTA_E4M3
 PAGE_SIZES = (16, 32, 64, 128, 256)
-KEPT_ROWS_BYTES = 1 << 24   # packed rows up to this are the step's own: making them anew costs 3 us, writing them 3 us and more
+KEPT_ROWS_BYTES = 1 << 24   # packed rows up to this are the step's own: made anew they cost 3 us, as much as writing this many
 
 
 class PagedParams(ctypes.Structure):
@@ -121,8 +121,9 @@ def rope_table(positions: int, rotated: int, base: float = 10000.0, *, linear: f
 
 
 class PagedCache:
-    """A pool of pages: K and V [n_pages, page_size, n_kv_heads, head_dim] and, for an e4m3 cache, the rows' scales
-    k_scale and v_scale [n_pages, n_kv_heads, page_size]."""
+    """A pool of pages: K and V [n_pages, page_size, n_kv_heads, head_dim] in bf16, fp16, fp32 or e4m3 and, for an e4m3
+    cache, the rows' scales k_scale and v_scale [n_pages, n_kv_heads, page_size].  Attention takes bf16 and fp16 tokens;
+    an fp32 cache is written, read back and sampled from."""
 
     def __init__(self, n_pages: int, page_size: int, n_kv_heads: int, head_dim: int, dtype=torch.bfloat16,
                  device="cuda"):
@@ -171,9 +172,10 @@ class PagedStep:
     [B + 1] (None: max_q new tokens each).  All three are read by the GPU when a call runs and may be changed in place
     between calls; nk and max_q bound what they may hold.  Calls of one step share its workspace: order them on one
     stream.  Outputs that a call is not given are the step's own, as ``Decoder``'s: its next such call on that stream
-    overwrites them (packed rows of more than 16 MiB are made anew by each ``read``, and are not kept).  Keep the step while graphs that captured its calls are used; otherwise it may go while its calls
-    still run, on whichever streams (tensors given to a call with ``stream=`` are the caller's to keep until it has run).
-    ``error()`` reports what the device refused."""
+    overwrites them (packed rows of more than 16 MiB are made anew by each ``read``, and are not kept).  Keep the step
+    while graphs that captured its calls are used; otherwise it may go while its calls still run, on whichever streams
+    (tensors given to a call with ``stream=`` are the caller's to keep until it has run).  ``error()`` reports what the
+    device refused."""
 
     def __init__(self, cache: PagedCache, page_table, kv_lens=None, *, n_q_heads: int, dtype=None,
                  nk: Optional[int] = None, max_q: int = 1, total_q: Optional[int] = None, q_offsets=None,
@@ -323,8 +325,8 @@ class PagedStep:
         return q_out
 
     def attend(self, q, *, out=None, lse=None, return_lse: bool = False, stream=None):
-        """softmax(scale q K^T + mask) V over the pages, [total_q, n_q_heads, head_dim] in q's type (out may be q); with
-        return_lse (or an lse to fill) also the float32 [total_q, n_q_heads] logarithms of the softmax sums."""
+        """softmax(scale q K^T + mask) V over the pages, [total_q, n_q_heads, head_dim] in q's type, bf16 or fp16 (out may
+        be q); with return_lse (or an lse to fill) also the float32 [total_q, n_q_heads] logarithms of the softmax sums."""
         raw = self._on(stream)
         q_ptr = self._dense(q, self._shape, self.dtype, "q")
         if out is not None:
@@ -369,7 +371,8 @@ class PagedStep:
                sample_idx=None, stream=None):
         """One S2ANTA / SANTA decode step over the paged cache: its rows read back packed (kv_offsets the exclusive
         sums of kv_lens), then santa_decode on them, for steps of one token per sequence that sees all of its keys.
-        q [B, n_q_heads, head_dim]; the result is float32."""
+        q [B, n_q_heads, head_dim]; the result is float32.  The packed copy costs twice the cache's bytes: ``attend`` is
+        exact and moves them once, so this is for what wants the estimator's draws."""
         from . import santa_decode
         if self.total_q != self.batch:
             raise ValueError("sample takes steps of one token per sequence")

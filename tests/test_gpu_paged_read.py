@@ -88,3 +88,17 @@ def test_a_read_captured_on_a_stream_that_is_not_the_current_one():
         graph.replay()
         side.synchronize()
     assert all(bool((x == 3.0).all()) for x in others) and step.error() == 0
+
+
+def test_a_cache_in_fp32_is_sampled_from():
+    batch = Batch([300, 90], [1, 1], 4, 2, 64, torch.float32, False, 16, seed=4)
+    step = batch.step()
+    offsets = torch.tensor([0, 300, 390], device="cuda")
+    idx, idx2 = (torch.full((2, 4, 32), -1, dtype=torch.int32, device="cuda") for _ in range(2))
+    out = step.sample(batch.q, 32, offsets, 390, seed=7, sample_idx=idx)
+    K, V = (torch.cat([batch.rows(b, x) for b in range(2)]).float() for x in "KV")
+    want = santa.santa_decode(batch.q, K, V, 32, seed=7, nk=300, kv_offsets=offsets, sample_idx=idx2)
+    assert step.error() == 0 and torch.equal(idx, idx2)
+    torch.testing.assert_close(out, want, rtol=1e-5, atol=1e-6)
+    with pytest.raises(santa.SantaError):
+        step.attend(batch.q)
