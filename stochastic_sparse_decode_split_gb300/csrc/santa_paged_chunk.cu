@@ -620,6 +620,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
     if (lane == 0) s_walk[warp].start(a, sh);
     for (;;) {
       int more = 0;
+      __syncwarp();   // the other lanes have read the last piece
       if (lane == 0) {
         Walk w = s_walk[warp];
         more = w.next(a, sh, pc);
