@@ -298,12 +298,13 @@ typedef struct {
   int64_t nk;                 /* upper bound on every kv_lens[b], 1 .. SANTA_MAX_NK */
   const int64_t* q_offsets;   /* device [batch + 1], non-decreasing; NULL = b * max_q */
   int32_t max_q;              /* >= 1: new tokens per sequence; with q_offsets an upper bound (the closer, the fewer idle blocks) */
-  int64_t total_q;            /* >= 1: rows of the token arrays, total_q * n_q_heads < 2^31; batch * max_q without q_offsets */
+  int64_t total_q;            /* 1 .. SANTA_MAX_TOKENS: rows of the token arrays, total_q * n_q_heads < 2^31; batch * max_q without q_offsets */
   int32_t causal;             /* 1: a token sees the keys up to its own position; 0: all of them */
   int32_t window;             /* > 0 (causal only): of those, the last `window`; 0: no window */
   float scale;                /* score scale; <= 0 selects 1/sqrt(head_dim) */
 } santa_paged_t;
 
+#define SANTA_MAX_TOKENS 2147483391 /* 2^31 - 257: the tile of 256 rows behind the last token has a number, too */
 #define SANTA_CACHE_DEVERR_PAGE 16
 #define SANTA_CACHE_DEVERR_CHUNK 32
 #define SANTA_CACHE_DEVERR_POSITION 64

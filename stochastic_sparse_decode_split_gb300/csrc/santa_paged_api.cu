@@ -39,7 +39,8 @@ santa_status_t check(const santa_paged_t* p) {
   if (!p) return SANTA_ERR_INVALID_ARG;
   if (p->batch < 1 || p->batch > 65535 || p->n_q_heads < 1 || p->n_kv_heads < 1) return SANTA_ERR_INVALID_ARG;
   if (p->n_q_heads > 65535 || p->n_q_heads % p->n_kv_heads) return SANTA_ERR_INVALID_ARG;
-  if (p->nk < 1 || p->nk > SANTA_MAX_NK || p->max_q < 1 || p->total_q < 1 || p->total_q > INT32_MAX) return SANTA_ERR_INVALID_ARG;
+  if (p->nk < 1 || p->nk > SANTA_MAX_NK || p->max_q < 1 || p->total_q < 1 || p->total_q > SANTA_MAX_TOKENS)
+    return SANTA_ERR_INVALID_ARG;
   if (!p->q_offsets && p->total_q != (int64_t)p->batch * p->max_q) return SANTA_ERR_INVALID_ARG;
   if (p->n_pages < 1 || p->max_pages < 1) return SANTA_ERR_INVALID_ARG;
   if (p->page_size < 16 || p->page_size > 256 || (p->page_size & (p->page_size - 1))) return SANTA_ERR_UNSUPPORTED;

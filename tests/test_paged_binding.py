@@ -40,3 +40,18 @@ def test_a_bound_above_the_number_of_tokens_needs_the_workspace_of_the_tokens():
     assert {size(max_q=m) for m in (301, 2048, 2 ** 31 - 1)} == {size()}
     assert size(total_q=5, max_q=2048) == size(total_q=5, max_q=5) > 0
     assert size(q_offsets=None) == size(q_offsets=None, max_q=301) == 0 < size(q_offsets=None, max_q=150)
+
+
+def test_the_largest_number_of_tokens():
+    """A CTA per multiprocessor holds the sums of two shared items of 256 rows, whatever the number of tokens; where the
+    number of the tile behind the last one would pass 2^31 the batch is refused."""
+    build.build()
+    p = paged.PagedParams()
+    p.batch, p.n_q_heads, p.n_kv_heads, p.head_dim, p.dtype, p.cache_dtype = 1, 1, 1, 64, 0, 0
+    p.page_size, p.n_pages, p.page_table, p.max_pages, p.kv_lens, p.nk = 16, 4096, 4096, 2048, 4096, 30000
+    p.causal = 1
+    sizes = []
+    for p.total_q in (1 << 20, (1 << 31) - 257, (1 << 31) - 256, (1 << 31) - 1):
+        p.max_q = p.total_q
+        sizes.append(santa.library().santa_paged_workspace_size(ctypes.byref(p)))
+    assert sizes[0] == sizes[1] and 0 < sizes[0] < 1 << 27 and sizes[2:] == [0, 0]
