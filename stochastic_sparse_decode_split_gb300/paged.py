@@ -172,10 +172,10 @@ class PagedStep:
     [B + 1] (None: max_q new tokens each).  All three are read by the GPU when a call runs and may be changed in place
     between calls; nk and max_q bound what they may hold.  Calls of one step share its workspace: order them on one
     stream.  Outputs that a call is not given are the step's own, as ``Decoder``'s: its next such call on that stream
-    overwrites them (packed rows of more than 16 MiB are made anew by each ``read``, and are not kept).  Keep the step
-    while graphs that captured its calls are used; otherwise it may go while its calls still run, on whichever streams
-    (tensors given to a call with ``stream=`` are the caller's to keep until it has run).  ``error()`` reports what the
-    device refused."""
+    overwrites them (packed rows of more than 16 MiB are made anew by each ``read`` outside a capture, and not kept).
+    Keep the step while graphs that captured its calls are used; otherwise it may go while its calls still run, on
+    whichever streams (tensors given to a call with ``stream=`` are the caller's to keep until it has run).  ``error()``
+    reports what the device refused."""
 
     def __init__(self, cache: PagedCache, page_table, kv_lens=None, *, n_q_heads: int, dtype=None,
                  nk: Optional[int] = None, max_q: int = 1, total_q: Optional[int] = None, q_offsets=None,
@@ -356,13 +356,17 @@ class PagedStep:
         elif rows is None:
             rows = self.batch * self.nk
         shape = (rows, self._kv_shape[1], self._kv_shape[2])
-        own = K_out is None or V_out is None
-        if K_out is None:
-            K_out = self._own("K", raw, shape, self.dtype, stream, KEPT_ROWS_BYTES)
-        if V_out is None:
-            V_out = self._own("V", raw, shape, self.dtype, stream, KEPT_ROWS_BYTES)
-        if own and _captures(stream):
-            self._captured.append((K_out, V_out))   # a later call with other rows replaces them; the graph still writes these
+        if K_out is None or V_out is None:
+            # what a graph writes to is kept, and the next capture's; a later call with other rows replaces it as the
+            # step's own, but the graph still writes there
+            captured = _captures(stream)
+            most = None if captured else KEPT_ROWS_BYTES
+            if K_out is None:
+                K_out = self._own("K", raw, shape, self.dtype, stream, most)
+            if V_out is None:
+                V_out = self._own("V", raw, shape, self.dtype, stream, most)
+            if captured and not any(K is K_out and V is V_out for K, V in self._captured):
+                self._captured.append((K_out, V_out))
         self._check(self._read_fn(self._ref, *self._pool, off_ptr, rows, self._dense(K_out, shape, self.dtype, "K_out"),
                                   self._dense(V_out, shape, self.dtype, "V_out"), *self._ws, raw), "santa_kv_read")
         return K_out, V_out

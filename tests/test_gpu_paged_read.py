@@ -102,3 +102,22 @@ def test_a_cache_in_fp32_is_sampled_from():
     torch.testing.assert_close(out, want, rtol=1e-5, atol=1e-6)
     with pytest.raises(santa.SantaError):
         step.attend(batch.q)
+
+
+def test_captures_of_a_long_contexts_read_share_their_outputs():
+    batch = Batch([9000], [1], 8, 8, 128, BF16, False, 64, seed=2)
+    step = batch.step()
+    offsets = torch.tensor([0, 9000], device="cuda")
+    step.read(offsets, 9000)
+    side, graphs, at = torch.cuda.Stream(), [], set()
+    for _ in range(3):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1], stream=side):
+            for _ in range(2):
+                K, V = step.read(offsets, 9000)
+                at.add((K.data_ptr(), V.data_ptr()))
+    assert len(at) == 1 and len(step._captured) == 1
+    for graph in graphs:
+        K.zero_()
+        graph.replay()
+        assert torch.equal(K.double(), batch.rows(0, "K")) and torch.equal(V.double(), batch.rows(0, "V"))
