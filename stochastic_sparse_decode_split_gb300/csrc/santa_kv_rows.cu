@@ -129,8 +129,8 @@ __device__ __forceinline__ f2x mul2(f2x a, f2x b) {
 // As many warps as their registers allow without spilling: 32 per SM in 16
 // bits, 28 over e4m3, 20 in float32.  8192 tokens of 32 and 8 heads of 128:
 // 33.9 us in bf16 (36.5 with 24 warps), 32.7 over e4m3 (35.0; 34.0 with 32 and
-// a few spills), 5.6 TB/s, 62.3 us in float32 (6.5 TB/s; 57.6 over e4m3); twice the rows in flight per warp and fewer warps
-// were slower (34.8 to 38.5).
+// a few spills), 5.6 TB/s; twice the rows in flight per warp and fewer warps
+// were slower (34.8 to 38.5).  In float32 62.3 us, 6.5 TB/s; 57.6 over e4m3.
 template <typename T, int D, bool E4M3, bool INTER>
 __global__ void __launch_bounds__(128, sizeof(T) == 4 ? 5 : E4M3 ? 7 : 8) kv_append_kernel(PagedArgs a, AppendArgs p, int qparts, int qg, int kvg) {
   using F = Four<T>;

@@ -809,13 +809,14 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       // ------------------------------------------------------- the result
       const bool join = !two && nblk > 1;          // both groups hold sums of these rows
       const bool mine = t == 0 || two;               // this group writes
-      // A wait can tell a phase from the one before it, but not from the one
-      // after.  O_DONE and ML_FULL are waited for by warps that the next piece
-      // may not need (group 1 where it is one block of one tile; group 0, whose
-      // join the other group's next one could overtake), so each softmax warp
-      // says when it is past a piece's waits: the V of the next piece is loaded,
-      // and group 1 takes part in the next join, after all eight have.  Group 1
-      // waits also where it has no part, or it could arrive twice in one phase.
+      // A wait knows a phase by its parity: once the next one is over as well,
+      // the phase looks as if it were still to come.  O_DONE and ML_FULL are
+      // waited for by warps that the next piece may not need (group 1 where it
+      // is one block of one tile; group 0, whose join the other group's next
+      // one could overtake), so each softmax warp says when it is past a
+      // piece's waits: the V of the next piece is loaded, and group 1 takes
+      // part in the next join, after all eight have.  Group 1 waits also where
+      // it has no part, or it could arrive twice in one phase.
       if (!mine && nblk > 0 && np > 0) {
         wait_phase(bar(PIECE_SEEN), (np - 1) & 1, a.err, dead);
         __syncwarp();
