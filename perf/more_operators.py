@@ -212,7 +212,7 @@ def prepare(case, seed):
         cache = santa.PagedCache.of(s["K"], s["V"], s["ks"], s["vs"])
         s["step"] = santa.PagedStep(cache, s["table"], s["lens"], n_q_heads=H, dtype=t, nk=most_keys(s), max_q=max(n),
                                     total_q=s["tokens"], q_offsets=None if min(n) == max(n) else s["offsets"],
-                                    causal=case["causal"], window=case["window"], **more)
+                                    causal=case["causal"], window=case["window"], diff=case["diff"], **more)
     return s
 
 
