@@ -308,6 +308,7 @@ typedef struct {
 #define SANTA_CACHE_DEVERR_PAGE 16
 #define SANTA_CACHE_DEVERR_CHUNK 32
 #define SANTA_CACHE_DEVERR_POSITION 64
+#define SANTA_CACHE_DEVERR_PREFIX 128
 
 /* Byte size of the workspace of the three calls on the current device (0 when p
  * is invalid).  Of p's pointers it only matters whether q_offsets is NULL. */
@@ -358,6 +359,66 @@ santa_status_t santa_kv_append(const santa_paged_t* p, const santa_append_t* a, 
 santa_status_t santa_paged_attention(const santa_paged_t* p, const void* q, const void* K, const void* V,
                                      const float* k_scale, const float* v_scale, void* out, float* lse,
                                      void* workspace, size_t ws_bytes, santa_stream_t stream);
+
+/* What the sequences of a batch have in common.  A group is consecutive
+ * sequences whose first prefix_lens[g] keys are the same: group g is the
+ * sequences group_offsets[g] .. group_offsets[g+1], and its prefix is read once
+ * for all of them, through the table row of its first sequence (the other rows'
+ * entries for pages that lie wholly inside the prefix are not read).  Every
+ * sequence's new tokens stand behind its group's prefix; a prefix may end
+ * anywhere in a page, whose further keys each sequence then has in a page of
+ * its own table row.  A prefix of 0 shares nothing.
+ *
+ * SANTA_CACHE_DEVERR_PREFIX: a group with bad offsets, more new tokens than
+ * max_group * max_q, or prefix_lens[g] outside [0, max_prefix]; a sequence in no
+ * group, whose new tokens begin inside the prefix (not causal: of fewer keys), or
+ * with more than max_own keys behind it.  The attention rows of the sequences
+ * that it concerns come out zero. */
+typedef struct {
+  int32_t n_groups;              /* 1 .. batch */
+  const int32_t* group_offsets;  /* device [n_groups + 1]; NULL (n_groups 1): all sequences */
+  const int32_t* prefix_lens;    /* device [n_groups] */
+  int64_t max_prefix;            /* upper bound on every prefix_lens[g], >= 1 */
+  int64_t max_own;               /* upper bound on the keys that a sequence has behind its prefix, >= 1 */
+  int32_t max_group;             /* upper bound on the sequences of a group, >= 1 */
+} santa_prefix_t;
+
+/* Byte size of santa_shared_attention's workspace (0 when p or x is invalid; of
+ * their pointers it only matters whether q_offsets is NULL). */
+size_t santa_shared_workspace_size(const santa_paged_t* p, const santa_prefix_t* x);
+
+/* santa_paged_attention for a batch whose sequences share prefixes: the same
+ * result, with a group's prefix read once.  No window (SANTA_ERR_UNSUPPORTED):
+ * what a group sees of its prefix would differ from token to token. */
+santa_status_t santa_shared_attention(const santa_paged_t* p, const santa_prefix_t* x, const void* q, const void* K, const void* V,
+                                      const float* k_scale, const float* v_scale, void* out, float* lse, void* workspace,
+                                      size_t ws_bytes, santa_stream_t stream);
+
+/* Differential heads: the weights of the second maps and the norm behind them. */
+typedef struct {
+  const float* lambda;           /* device, one weight for each pair of query heads, and with lambda_stride of each token */
+  int64_t lambda_stride;         /* floats from token to token, at least n_q_heads / 2; 0: the weights are the same for all */
+  const void* norm;              /* device [2 * head_dim] in dtype, 16-byte aligned, or NULL: no norm */
+  float eps;                     /* of the norm, >= 0 */
+  float gain;                    /* multiplies the result */
+} santa_diff_t;
+
+/* Byte size of santa_diff_attention's workspace, x NULL where nothing is shared. */
+size_t santa_diff_workspace_size(const santa_paged_t* p, const santa_prefix_t* x);
+
+/* Differential attention over the pages (Ye et al., "Differential Transformer",
+ * arXiv:2410.05258): heads come in pairs, n_q_heads / 2 of queries and
+ * n_kv_heads / 2 of keys and values, and pair h of the queries meets pair
+ * j = h / (n_q_heads / n_kv_heads) of the keys:
+ *   y = (softmax(scale q[2h] K[2j]^T + mask) - lambda_h softmax(scale q[2h+1] K[2j+1]^T + mask)) [V[2j] V[2j+1]]
+ *   out[h] = gain * y / sqrt(mean y^2 + eps) * norm    (gain * y without norm)
+ *   out  [total_q, n_q_heads / 2, 2 * head_dim] in dtype; may be q itself
+ *   lse  optional float32 [total_q, n_q_heads], as santa_paged_attention's
+ * Layouts, masks, empty rows (zeros), and x (or NULL) as above; n_kv_heads is
+ * even.  The difference and the norm are taken of float32 sums. */
+santa_status_t santa_diff_attention(const santa_paged_t* p, const santa_prefix_t* x, const santa_diff_t* d, const void* q,
+                                    const void* K, const void* V, const float* k_scale, const float* v_scale, void* out, float* lse,
+                                    void* workspace, size_t ws_bytes, santa_stream_t stream);
 
 /* The cache's keys and values as packed rows, K_out and V_out
  * [rows, n_kv_heads, head_dim] in dtype: key n of sequence b in row

@@ -25,7 +25,8 @@ import torch
 
 from . import paged as _paged
 from .build import LIB as _LIB_PATH
-from .paged import CACHE_DEVERR_CHUNK, CACHE_DEVERR_PAGE, CACHE_DEVERR_POSITION, PagedCache, PagedStep, rope_table
+from .paged import (CACHE_DEVERR_CHUNK, CACHE_DEVERR_PAGE, CACHE_DEVERR_POSITION, CACHE_DEVERR_PREFIX, PagedCache, PagedStep,
+                    diff_weights, rope_table)
 
 __all__ = [
     "SantaError", "Params", "library", "santa_decode", "santa_decode_host_kv", "santa_decode_with_uniforms",
@@ -33,7 +34,7 @@ __all__ = [
     "workspace_size", "dense_workspace_size", "workspace_layout", "get_error", "Decoder", "exported_symbols",
     "VARIANTS", "DTYPES", "santa_decode_static", "static_warmup", "static_scratch_bytes", "SAMPLERS", "santa_decode_tiled",
     "tiled_workspace_size", "tiled_max_draws", "santa_decode_bernoulli", "bernoulli_workspace_size",
-    "PagedCache", "PagedStep", "rope_table",
+    "PagedCache", "PagedStep", "rope_table", "diff_weights",
 ]
 
 VARIANTS = {"iid": 0, "stratified": 1, "systematic": 2}

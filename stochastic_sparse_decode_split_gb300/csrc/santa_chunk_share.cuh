@@ -41,25 +41,29 @@ struct Walk {
   TileKeys tk;
   long long pos;
   Seq s;
-  SANTA_HD void start(const PagedArgs& a, const Share& sh) {
+  template <typename A>
+  SANTA_HD void start(const A& a, const Share& sh) {
     b = sh.b;
     kvh = sh.kvh;
     tile = sh.tile;
     pos = sh.pos;
     if (b < a.B) load(a);
   }
-  SANTA_HD void load(const PagedArgs& a) {   // a sequence and its tile
+  template <typename A>
+  SANTA_HD void load(const A& a) {   // a sequence and its tile
     s = paged_seq(a, b, false);
     keys(a);
   }
-  SANTA_HD void keys(const PagedArgs& a) {
+  template <typename A>
+  SANTA_HD void keys(const A& a) {
     tile_tokens(a, s.n, tile, i0, i1);
     tk = tile_keys(a, s, i0, i1, BKEYS);
   }
-  SANTA_HD bool next(const PagedArgs& a, const Share& sh, Piece& p) {
+  template <typename A>
+  SANTA_HD bool next(const A& a, const Share& sh, Piece& p) {
     for (;;) {
       if (b >= a.B || pos >= sh.hi) return false;
-      if (kvh == a.Hkv || tile * a.tokens >= s.n) {
+      if (kvh == item_heads(a) || tile * a.tokens >= s.n) {
         kvh = 0;
         if (++tile * a.tokens >= s.n) {
           tile = 0;
@@ -96,7 +100,8 @@ struct Walk {
 };
 
 // Blocks of item i = (sequence, tile), 0 where the tile has no token.
-SANTA_HD int item_weight(const PagedArgs& a, long long i, bool flag) {
+template <typename A>
+SANTA_HD int item_weight(const A& a, long long i, bool flag) {
   if (i >= (long long)a.B * a.tiles) return 0;
   const int b = (int)(i / a.tiles), tile = (int)(i - (long long)b * a.tiles);
   const Seq s = paged_seq(a, b, flag && tile == 0);
@@ -116,11 +121,13 @@ SANTA_HD bool share_split(long long T, int P, long long items, int most) {
   const long long each = items <= P ? 1 : (items + P - 1) / P;
   return most > CHUNK_LEAST && each * most > T / P + CHUNK_SHARE;
 }
+SANTA_HD bool item_split(const PagedArgs&, long long T, int P, long long items, int most) { return share_split(T, P, items, most); }
 // The item that holds block lo, if it is item i = (sequence, tile), of w blocks
 // per KV head, whose blocks of one head begin at `first`.
-SANTA_HD void share_place(const PagedArgs& a, Share& sh, long long lo, long long i, long long first, int w) {
-  const long long pos = first * a.Hkv;
-  if (w == 0 || lo < pos || lo >= pos + (long long)w * a.Hkv) return;
+template <typename A>
+SANTA_HD void share_place(const A& a, Share& sh, long long lo, long long i, long long first, int w) {
+  const long long pos = first * item_heads(a);
+  if (w == 0 || lo < pos || lo >= pos + (long long)w * item_heads(a)) return;
   sh.b = (int)(i / a.tiles);
   sh.tile = (int)(i - (long long)sh.b * a.tiles);
   sh.kvh = (int)(lo - pos) / w;

@@ -88,6 +88,7 @@ struct Seq {
   long long q0;
   int n, kv;
   bool ok;
+  int from;   // keys before this one are another pass's (0 but in a pass over what a sequence does not share)
 };
 
 SANTA_HD Seq paged_seq(const PagedArgs& a, int b, bool flag) {
@@ -108,6 +109,7 @@ SANTA_HD Seq paged_seq(const PagedArgs& a, int b, bool flag) {
   s.kv = fine ? kv : 0;
   if (!fine) e |= ERR_NK_BOUND;
   s.ok = e == 0;
+  s.from = 0;
 #ifdef __CUDA_ARCH__
   if (e && flag) flag_error(a.err, e);
 #endif
@@ -135,16 +137,22 @@ SANTA_HD void visible_keys(const PagedArgs& a, int kv, int pos, int& lo, int& hi
   hi = a.causal ? min(max(pos + 1, 0), kv) : kv;
   lo = a.window ? min(max(pos - a.window + 1, 0), hi) : 0;
 }
+// The kernels take the batch's description as a type A, PagedArgs or one made
+// from it (santa_join.cuh), and ask for these; so does what the host computes.
+SANTA_HD void visible_keys(const PagedArgs& a, const Seq& s, int pos, int& lo, int& hi) { visible_keys(a, s.kv, pos, lo, hi); }
+SANTA_HD int item_heads(const PagedArgs& a) { return a.Hkv; }   // items of a tile: one per KV head
+SANTA_HD const int32_t* page_row(const PagedArgs& a, int b) { return a.table + (long long)b * a.max_pages; }
 
 // The key blocks of a tile whose first and last token are i0 and i1 (of n):
 // blk blocks of `keys` keys from block blk_lo on.
 struct TileKeys {
   int blk_lo, blk;
 };
-SANTA_HD TileKeys tile_keys(const PagedArgs& a, const Seq& s, int i0, int i1, int keys) {
+template <typename A>
+SANTA_HD TileKeys tile_keys(const A& a, const Seq& s, int i0, int i1, int keys) {
   int lo0, hi0, lo1, hi1;
-  visible_keys(a, s.kv, s.kv - s.n + i0, lo0, hi0);
-  visible_keys(a, s.kv, s.kv - s.n + i1, lo1, hi1);
+  visible_keys(a, s, s.kv - s.n + i0, lo0, hi0);
+  visible_keys(a, s, s.kv - s.n + i1, lo1, hi1);
   TileKeys t;
   t.blk_lo = lo0 / keys;
   t.blk = hi1 > lo0 ? (hi1 + keys - 1) / keys - t.blk_lo : 0;

@@ -8,11 +8,13 @@
 #include <atomic>
 
 #include "../../include/santa.h"
+#include "santa_join.cuh"
 #include "santa_launch.h"
 #include "santa_paged.cuh"
 
 static_assert(SANTA_CACHE_DEVERR_PAGE == santa::ERR_PAGE && SANTA_CACHE_DEVERR_CHUNK == santa::ERR_CHUNK &&
-                  SANTA_CACHE_DEVERR_POSITION == santa::ERR_POSITION,
+                  SANTA_CACHE_DEVERR_POSITION == santa::ERR_POSITION &&
+                  SANTA_CACHE_DEVERR_PREFIX == santa::ERR_PREFIX,
               "device error bits");
 
 namespace {
@@ -104,10 +106,12 @@ santa::PagedArgs args(const santa_paged_t* p) {
 // 4096 keys, 8 KV heads, 32 rows) 22.1 against 28.9, e4m3 25.1 against 32.4; at
 // four thirds (128 rows) 29.4 against 21.9, heads of 128 (one sequence of 16384
 // keys, 64 rows) 39 against 31.9.
-bool few_rows(const santa::PagedArgs& a) {
-  const int64_t rows = (int64_t)a.max_q * a.G, span = a.window ? std::min<int64_t>(a.nk, (int64_t)a.window + a.max_q) : a.nk;
+bool few_rows(const santa::PagedArgs& a, int64_t span) {
+  const int64_t rows = (int64_t)a.max_q * a.G;
   return rows <= 16 || (rows + 15) / 16 <= 3 * 8192 * 16 / span / ((int64_t)a.B * a.Hkv);
 }
+int64_t span_of(const santa::PagedArgs& a) { return a.window ? std::min<int64_t>(a.nk, (int64_t)a.window + a.max_q) : a.nk; }
+bool few_rows(const santa::PagedArgs& a) { return few_rows(a, span_of(a)); }
 
 // The attention's plan, and its workspace: header, the chunk attention's notes
 // of shared items, the pieces' sums.
@@ -125,9 +129,184 @@ Plan plan(santa::PagedArgs& a) {
   return p;
 }
 
+// Differential heads: as above; the kernel for few rows takes eight at a time.
+bool few_diff(const santa::PagedArgs& a, int64_t span) {
+  const int64_t rows = (int64_t)a.max_q * a.G;
+  return rows <= 8 || (rows + 7) / 8 <= 3 * 8192 * 16 / span / ((int64_t)a.B * a.Hkv);
+}
+
+// ---- attention in passes: a shared prefix, differential heads
+
+santa_status_t check_join(const santa_paged_t* p, const santa_prefix_t* x, bool diff) {
+  santa_status_t st = check(p);
+  if (st != SANTA_OK) return st;
+  if (p->dtype == SANTA_FP32) return SANTA_ERR_UNSUPPORTED;
+  if (diff && (p->n_kv_heads % 2)) return SANTA_ERR_INVALID_ARG;
+  if (!x) return SANTA_OK;
+  if (x->n_groups < 1 || x->n_groups > p->batch || x->max_group < 1) return SANTA_ERR_INVALID_ARG;
+  if (x->max_prefix < 1 || x->max_own < 1) return SANTA_ERR_INVALID_ARG;
+  if (p->window && p->window < p->nk) return SANTA_ERR_UNSUPPORTED;   // what a group sees of its prefix would differ by token
+  return SANTA_OK;
+}
+
+// A pass's kernel and the sizes of its sums; `span` keys, that may begin inside a block.
+void plan_pass(santa::JoinArgs& a, int64_t span, bool inside) {
+  if (a.diff) {
+    a.chunk = !few_diff(a, span);
+    if (a.chunk) a.tokens = santa::CHUNK_ROWS / a.G;
+    else santa::plan_diff_tokens(a, (int)span, inside);
+  } else {
+    a.chunk = !few_rows(a, span);
+    if (a.chunk) a.tokens = 2 * (santa::CHUNK_ROWS / a.G);
+    else santa::plan_tokens(a, (int)span, inside);
+  }
+  a.heads = santa::x_items(a);
+  if (a.chunk) {
+    if (a.diff && (a.e4m3 || a.D == 128)) a.heads *= 2;   // an item for each value head
+    a.rows = 2 * santa::CHUNK_ROWS;
+    a.tiles = (a.max_q + a.tokens - 1) / a.tokens;
+    const int64_t items = (int64_t)a.B * a.heads * a.tiles, blocks = (span + santa::BKEYS - 1) / santa::BKEYS + inside;
+    a.splits = (int)std::min<int64_t>(a.num_sms, items * blocks);
+    a.sources = (int)(a.splits / items) + 1;
+  } else {
+    a.sources = a.splits;
+  }
+}
+
+struct JoinPlan {
+  santa::JoinArgs prefix, own;
+  size_t total;
+};
+
+// Lays one pass's sums out from byte `at` of the workspace on.
+void lay_out(santa::JoinArgs& a, unsigned char* ws, size_t& at) {
+  const size_t wide = a.diff ? 2 * a.D : a.D, all = (size_t)a.total_q * a.H;
+  auto take = [&](size_t bytes) {
+    unsigned char* const p = ws + at;
+    at += up(bytes);
+    return p;
+  };
+  if (a.chunk) {
+    const size_t rows = (size_t)a.splits * 2 * a.rows, cols = wide * santa::x_items(a) / a.heads;
+    a.part_o = reinterpret_cast<float*>(take(rows * cols * sizeof(float)));
+    a.part_ml = reinterpret_cast<float*>(take(rows * 2 * sizeof(float)));
+    a.row_o = reinterpret_cast<float*>(take(all * wide * sizeof(float)));
+    a.row_ml = reinterpret_cast<float*>(take(all * 2 * (wide / cols) * sizeof(float)));
+    a.notes = reinterpret_cast<santa::PieceNote*>(take((size_t)a.B * a.tiles * a.heads * sizeof(santa::PieceNote)));
+  } else {
+    const size_t rows = (size_t)a.B * a.tiles * a.heads * a.splits * a.rows * (a.diff ? 2 : 1);
+    a.part_o = reinterpret_cast<float*>(take(rows * wide * sizeof(float)));
+    a.part_ml = reinterpret_cast<float*>(take(rows * 2 * (a.diff ? 2 : 1) * sizeof(float)));
+  }
+}
+
+JoinPlan join_plan(const santa_paged_t* p, const santa_prefix_t* x, bool diff, void* ws) {
+  JoinPlan l;
+  memset(&l, 0, sizeof l);
+  static_cast<santa::PagedArgs&>(l.own) = args(p);
+  l.own.diff = diff;
+  l.own.seqs = l.own.B;
+  l.own.seq_q = l.own.max_q;
+  l.prefix = l.own;
+  if (x) {
+    l.own.phase = 2;
+    l.own.n_groups = x->n_groups;
+    l.own.group_q = (int)std::min<int64_t>((int64_t)x->max_group * l.own.max_q, p->total_q);
+    l.own.group_offsets = x->group_offsets;
+    l.own.prefix_lens = x->prefix_lens;
+    l.own.max_prefix = (int)std::min(x->max_prefix, p->nk);   // upper bounds may be above what there can be
+    l.own.max_own = (int)std::min(x->max_own, p->nk);
+    l.prefix = l.own;
+    l.prefix.phase = 1;
+    l.prefix.B = x->n_groups;
+    l.prefix.max_q = l.own.group_q;
+    plan_pass(l.prefix, l.own.max_prefix, false);
+    plan_pass(l.own, l.own.max_own, true);
+  } else {
+    plan_pass(l.own, span_of(l.own), l.own.window != 0);
+  }
+  size_t at = HEADER;
+  unsigned char* const w = static_cast<unsigned char*>(ws);
+  if (x) lay_out(l.prefix, w, at);
+  lay_out(l.own, w, at);
+  l.total = at;
+  return l;
+}
+
+// Whether the grid of a pass has a number.
+bool fits(const santa::JoinArgs& a) { return a.chunk || (int64_t)a.B * a.tiles * a.heads <= INT32_MAX / a.splits; }
+
+santa_status_t join(const santa_paged_t* p, const santa_prefix_t* x, const santa_diff_t* d, const void* q, const void* K,
+                    const void* V, const float* ks, const float* vs, void* out, float* lse, void* ws, size_t ws_bytes,
+                    santa_stream_t stream) {
+  santa_status_t st = check_join(p, x, d != nullptr);
+  if (st != SANTA_OK) return st;
+  if (!q || !out || !aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4)) return SANTA_ERR_INVALID_ARG;
+  if (x && (!x->prefix_lens || !aligned(x->prefix_lens, 4) || !aligned(x->group_offsets, 4) || (!x->group_offsets && x->n_groups != 1)))
+    return SANTA_ERR_INVALID_ARG;
+  if (d && (!d->lambda || !aligned(d->lambda, 4) || !aligned(d->norm, 16) || d->lambda_stride < 0 ||
+            (d->lambda_stride && d->lambda_stride < p->n_q_heads / 2) || (d->norm && !(d->eps >= 0.f && !isinf(d->eps))) ||
+            !(d->gain == d->gain) || isinf(d->gain)))
+    return SANTA_ERR_INVALID_ARG;
+  JoinPlan l = join_plan(p, x, d != nullptr, ws);
+  st = check_cache(p, K, V, ks, vs, ws, ws_bytes, l.total);
+  if (st != SANTA_OK) return st;
+  if ((x && !fits(l.prefix)) || !fits(l.own)) return SANTA_ERR_UNSUPPORTED;
+  for (santa::JoinArgs* a : {&l.prefix, &l.own}) {
+    a->q = q;
+    a->K = K;
+    a->V = V;
+    a->ks = ks;
+    a->vs = vs;
+    a->out = out;
+    a->lse = lse;
+    a->err = static_cast<int*>(ws);
+    a->stream = (cudaStream_t)stream;
+    if (d) {
+      a->lambda = d->lambda;
+      a->lambda_stride = d->lambda_stride;
+      a->norm = d->norm;
+      a->eps = d->eps;
+      a->gain = d->gain;
+    }
+  }
+  auto launch = [&](const santa::JoinArgs& a, bool behind) {
+    if (a.diff) return a.chunk ? santa::launch_diff_chunk(a, behind) : santa::launch_diff_tokens(a, behind);
+    return a.chunk ? santa::launch_join_chunk(a, behind) : santa::launch_join_tokens(a, behind);
+  };
+  cudaError_t e = x ? launch(l.prefix, false) : cudaSuccess;
+  if (e == cudaSuccess) e = launch(l.own, x != nullptr);
+  if (e == cudaSuccess) e = santa::launch_join(l.prefix, l.own);
+  return e == cudaSuccess ? SANTA_OK : SANTA_ERR_CUDA;
+}
+
 }  // namespace
 
 extern "C" {
+
+size_t santa_shared_workspace_size(const santa_paged_t* p, const santa_prefix_t* x) {
+  if (!x || check_join(p, x, false) != SANTA_OK) return 0;
+  return join_plan(p, x, false, nullptr).total;
+}
+
+size_t santa_diff_workspace_size(const santa_paged_t* p, const santa_prefix_t* x) {
+  if (check_join(p, x, true) != SANTA_OK) return 0;
+  return join_plan(p, x, true, nullptr).total;
+}
+
+santa_status_t santa_shared_attention(const santa_paged_t* p, const santa_prefix_t* x, const void* q, const void* K, const void* V,
+                                      const float* k_scale, const float* v_scale, void* out, float* lse, void* workspace,
+                                      size_t ws_bytes, santa_stream_t stream) {
+  if (!x) return SANTA_ERR_INVALID_ARG;
+  return join(p, x, nullptr, q, K, V, k_scale, v_scale, out, lse, workspace, ws_bytes, stream);
+}
+
+santa_status_t santa_diff_attention(const santa_paged_t* p, const santa_prefix_t* x, const santa_diff_t* d, const void* q,
+                                    const void* K, const void* V, const float* k_scale, const float* v_scale, void* out, float* lse,
+                                    void* workspace, size_t ws_bytes, santa_stream_t stream) {
+  if (!d) return SANTA_ERR_INVALID_ARG;
+  return join(p, x, d, q, K, V, k_scale, v_scale, out, lse, workspace, ws_bytes, stream);
+}
 
 size_t santa_paged_workspace_size(const santa_paged_t* p) {
   if (check(p) != SANTA_OK) return 0;

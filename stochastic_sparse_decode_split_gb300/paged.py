@@ -1,7 +1,9 @@
-"""The paged cache: new tokens written into it, exact attention over it, and
-its rows back in the packed layout that ``santa_decode`` reads.
+"""The paged cache: new tokens written into it, exact attention over it (also
+over prefixes that sequences share, and of differential heads), and its rows
+back in the packed layout that ``santa_decode`` reads.
 
-Binding of ``santa_kv_append``, ``santa_paged_attention`` and ``santa_kv_read``
+Binding of ``santa_kv_append``, ``santa_paged_attention``,
+``santa_shared_attention``, ``santa_diff_attention`` and ``santa_kv_read``
 (``include/santa.h`` states the layouts, the mask and the device-side checks).
 ``PagedCache`` holds the pool, ``PagedStep`` a batch's description and the
 workspace, so that each operator of a step is one C-ABI call.
@@ -15,7 +17,7 @@ from typing import Optional
 
 import torch
 
-CACHE_DEVERR_PAGE, CACHE_DEVERR_CHUNK, CACHE_DEVERR_POSITION = 16, 32, 64   # SANTA_CACHE_DEVERR_* in santa.h
+CACHE_DEVERR_PAGE, CACHE_DEVERR_CHUNK, CACHE_DEVERR_POSITION, CACHE_DEVERR_PREFIX = 16, 32, 64, 128   # SANTA_CACHE_DEVERR_* in santa.h
 E4M3 = 3                                                                   # SANTA_E4M3
 PAGE_SIZES = (16, 32, 64, 128, 256)
 KEPT_ROWS_BYTES = 1 << 24   # packed rows up to this are the step's own: made anew they cost 3 us, as much as writing this many
@@ -45,6 +47,29 @@ class PagedParams(ctypes.Structure):
     ]
 
 
+class PrefixParams(ctypes.Structure):
+    """Mirror of santa_prefix_t."""
+    _fields_ = [
+        ("n_groups", ctypes.c_int32),
+        ("group_offsets", ctypes.c_void_p),
+        ("prefix_lens", ctypes.c_void_p),
+        ("max_prefix", ctypes.c_int64),
+        ("max_own", ctypes.c_int64),
+        ("max_group", ctypes.c_int32),
+    ]
+
+
+class DiffParams(ctypes.Structure):
+    """Mirror of santa_diff_t (calls pack it with _DIFF)."""
+    _fields_ = [
+        ("lambda_", ctypes.c_void_p),
+        ("lambda_stride", ctypes.c_int64),
+        ("norm", ctypes.c_void_p),
+        ("eps", ctypes.c_float),
+        ("gain", ctypes.c_float),
+    ]
+
+
 class AppendParams(ctypes.Structure):
     """Mirror of santa_append_t (calls pack it with _APPEND, in a quarter of the time)."""
     _fields_ = [
@@ -66,6 +91,7 @@ class AppendParams(ctypes.Structure):
 
 
 _APPEND = struct.Struct("@PPPqqqPPPfPqii")   # AppendParams' fields in their order, natively aligned
+_DIFF = struct.Struct("@PqPff")              # DiffParams'
 _current_device, _capturing = torch.cuda.current_device, torch.cuda.is_current_stream_capturing
 
 
@@ -86,7 +112,12 @@ def declare(lib) -> None:
     lib.santa_kv_append.argtypes = [P, A, vp, vp, vp, vp, vp, sz, vp]
     lib.santa_paged_attention.argtypes = [P, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
     lib.santa_kv_read.argtypes = [P, vp, vp, vp, vp, vp, i64, vp, vp, vp, sz, vp]
-    for fn in ("santa_kv_append", "santa_paged_attention", "santa_kv_read"):
+    X, d = ctypes.POINTER(PrefixParams), vp   # a packed santa_diff_t
+    for fn in ("santa_shared_workspace_size", "santa_diff_workspace_size"):
+        getattr(lib, fn).argtypes, getattr(lib, fn).restype = [P, X], sz
+    lib.santa_shared_attention.argtypes = [P, X, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.santa_diff_attention.argtypes = [P, X, d, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    for fn in ("santa_kv_append", "santa_paged_attention", "santa_kv_read", "santa_shared_attention", "santa_diff_attention"):
         getattr(lib, fn).restype = ctypes.c_int32
 
 
@@ -118,6 +149,13 @@ def rope_table(positions: int, rotated: int, base: float = 10000.0, *, linear: f
         freq = freq * keep + freq / factor * (1 - keep)
     angle = torch.arange(positions, dtype=torch.float64, device=device)[:, None] * freq
     return (torch.stack((angle.cos(), angle.sin()), -1) * attention_factor).to(torch.float32)
+
+
+def diff_weights(q1, k1, q2, k2, init: float) -> torch.Tensor:
+    """The weights of differential heads from their learned vectors, float32: exp(q1 . k1) - exp(q2 . k2) + init over the
+    last dimension, [H / 2, d] to the [H / 2] that ``PagedStep.attend_diff`` takes."""
+    q1, k1, q2, k2 = (x.float() for x in (q1, k1, q2, k2))
+    return (q1 * k1).sum(-1).exp() - (q2 * k2).sum(-1).exp() + init
 
 
 class PagedCache:
@@ -175,11 +213,20 @@ class PagedStep:
     overwrites them (packed rows of more than 16 MiB are made anew by each ``read`` outside a capture, and not kept).
     Keep the step while graphs that captured its calls are used; otherwise it may go while its calls still run, on
     whichever streams (tensors given to a call with ``stream=`` are the caller's to keep until it has run).  ``error()``
-    reports what the device refused."""
+    reports what the device refused.
+
+    Sequences that have their first keys in common: ``prefix_lens`` int32 [groups] and, with more than one group,
+    ``group_offsets`` int32 [groups + 1], group g being the sequences group_offsets[g] .. group_offsets[g + 1] (also read
+    by the GPU when a call runs).  Attention then reads a group's prefix once, through its first sequence's row of the
+    table; the new tokens stand behind it, and there is no window.  ``max_prefix`` bounds the prefixes, ``max_own`` the
+    keys that a sequence has behind its own, ``max_group`` the sequences of a group: the closer, the better the work is
+    divided.  ``diff``: the step's heads are differential (``attend_diff``, whose workspace it then holds)."""
 
     def __init__(self, cache: PagedCache, page_table, kv_lens=None, *, n_q_heads: int, dtype=None,
                  nk: Optional[int] = None, max_q: int = 1, total_q: Optional[int] = None, q_offsets=None,
-                 causal: bool = True, window: int = 0, scale: float = 0.0):
+                 causal: bool = True, window: int = 0, scale: float = 0.0, prefix_lens=None, group_offsets=None,
+                 max_prefix: Optional[int] = None, max_own: Optional[int] = None, max_group: Optional[int] = None,
+                 diff: bool = False):
         from . import DTYPES, alloc_workspace, library
         dtype = dtype if dtype is not None else (torch.bfloat16 if cache.quantized else cache.K.dtype)
         if dtype not in DTYPES:
@@ -213,9 +260,19 @@ class PagedStep:
         p.nk, p.max_q, p.total_q = self.nk, int(max_q), self.total_q
         p.causal, p.window, p.scale = int(bool(causal)), int(window), float(scale)
         self.p, self._ref = p, ctypes.byref(p)
+        self.prefix_lens, self.group_offsets, self.diff = prefix_lens, group_offsets, bool(diff)
+        self._prefix = self._prefix_ref = None
+        if prefix_lens is not None:
+            self._groups(max_prefix, max_own, max_group)
+        elif any(x is not None for x in (group_offsets, max_prefix, max_own, max_group)):
+            raise ValueError("group_offsets, max_prefix, max_own and max_group go with prefix_lens")
         with torch.cuda.device(self.device):
-            n = library().santa_paged_workspace_size(self._ref)
-            if n == 0:
+            sizes = [library().santa_paged_workspace_size(self._ref) if self._prefix is None
+                     else library().santa_shared_workspace_size(self._ref, self._prefix_ref)]
+            if self.diff:
+                sizes.append(library().santa_diff_workspace_size(self._ref, self._prefix_ref))
+            n = max(sizes)
+            if min(sizes) == 0:
                 raise ValueError("invalid paged parameters")
             self.workspace = alloc_workspace(n, self.device)
             # the stream that clears the workspace's error word, and when it has
@@ -227,11 +284,32 @@ class PagedStep:
         self._shape = torch.Size((self.total_q, n_q_heads, cache.head_dim))
         self._kv_shape = torch.Size((self.total_q, cache.n_kv_heads, cache.head_dim))
         self._lse_shape, self._weight_shape = self._shape[:2], self._shape[2:]
+        self._diff_shape = torch.Size((self.total_q, n_q_heads // 2, 2 * cache.head_dim))
         self._kept = (cache.K, cache.V, cache.k_scale, cache.v_scale)
         self._pool = tuple(ctypes.c_void_p(None if t is None else t.data_ptr()) for t in self._kept)
         self._ws = (ctypes.c_void_p(self.workspace.data_ptr()), ctypes.c_size_t(n))
         lib = library()
         self._append_fn, self._attend_fn, self._read_fn = lib.santa_kv_append, lib.santa_paged_attention, lib.santa_kv_read
+        self._shared_fn, self._diff_fn = lib.santa_shared_attention, lib.santa_diff_attention
+
+    def _groups(self, max_prefix, max_own, max_group):
+        """The santa_prefix_t of prefix_lens and group_offsets."""
+        n = self.prefix_lens.shape[0] if self.prefix_lens.dim() == 1 else 0
+        self._tensor(self.prefix_lens, torch.int32, "prefix_lens", 1, n)
+        if self.group_offsets is not None:
+            self._tensor(self.group_offsets, torch.int32, "group_offsets", 1, n + 1)
+        elif n != 1:
+            raise ValueError("give group_offsets with more than one group")
+        bounds = (self.nk if max_prefix is None else max_prefix, self.nk if max_own is None else max_own,
+                  self.batch if max_group is None else max_group)
+        for name, x in zip(("max_prefix", "max_own", "max_group"), bounds):
+            if not 1 <= x < 1 << 31:
+                raise ValueError(f"{name} = {x} is out of range")
+        x = self._prefix = PrefixParams()
+        x.n_groups, x.prefix_lens = n, self.prefix_lens.data_ptr()
+        x.group_offsets = None if self.group_offsets is None else self.group_offsets.data_ptr()
+        x.max_prefix, x.max_own, x.max_group = (int(b) for b in bounds)
+        self._prefix_ref = ctypes.byref(x)
 
     def _tensor(self, t, dtype, name, dim, size=None):
         if t.dtype != dtype or t.dim() != dim or (size is not None and t.shape[0] != size):
@@ -267,7 +345,8 @@ class PagedStep:
         holds goes back to the allocator, when it is dropped, only after what that stream does with it."""
         with torch.cuda.stream(stream):
             on = torch.cuda.current_stream()
-            for t in (self.workspace, self.page_table, self.kv_lens, self.q_offsets, *self._kept):
+            for t in (self.workspace, self.page_table, self.kv_lens, self.q_offsets, self.prefix_lens, self.group_offsets,
+                      *self._kept):
                 if t is not None:
                     t.record_stream(on)
             if not _capturing():   # a capture takes no event from outside; it begins with a synchronisation
@@ -340,7 +419,48 @@ class PagedStep:
         elif return_lse:
             lse = self._own("lse", raw, self._lse_shape, torch.float32, stream)
             lse_ptr = lse.data_ptr()
-        self._check(self._attend_fn(self._ref, q_ptr, *self._pool, out_ptr, lse_ptr, *self._ws, raw), "santa_paged_attention")
+        if self._prefix is None:
+            self._check(self._attend_fn(self._ref, q_ptr, *self._pool, out_ptr, lse_ptr, *self._ws, raw), "santa_paged_attention")
+        else:
+            self._check(self._shared_fn(self._ref, self._prefix_ref, q_ptr, *self._pool, out_ptr, lse_ptr, *self._ws, raw),
+                        "santa_shared_attention")
+        return out if lse is None else (out, lse)
+
+    def attend_diff(self, q, weights, *, norm=None, eps: float = 1e-5, gain: float = 1.0, out=None, lse=None,
+                    return_lse: bool = False, stream=None):
+        """Differential attention, [total_q, n_q_heads / 2, 2 head_dim] in q's type: query heads 2h and 2h + 1 against key
+        heads 2j and 2j + 1 (j = h / (n_q_heads / n_kv_heads)), the first map less ``weights`` times the second over the
+        values of both, divided by the root of its mean square (+ eps) and multiplied by ``norm`` [2 head_dim] where that
+        is given, and by ``gain``.  weights: float32 [n_q_heads / 2], or [total_q, n_q_heads / 2] with dense rows.  out may
+        lie over q; with return_lse (or an lse to fill) also the float32 [total_q, n_q_heads] logarithms of the maps' sums."""
+        raw = self._on(stream)
+        if not self.diff:
+            raise ValueError("make the step with diff=True")
+        q_ptr = self._dense(q, self._shape, self.dtype, "q")
+        pairs = self._diff_shape[1]
+        stride = 0
+        if weights.dim() == 2 and weights.shape[0] == self.total_q and self.total_q > 1:
+            stride = weights.stride(0)
+        elif weights.dim() != 1 and not (weights.dim() == 2 and weights.shape[0] == self.total_q):
+            raise ValueError("weights must be [n_q_heads / 2] or [total_q, n_q_heads / 2]")
+        if weights.dtype is not torch.float32 or weights.device != self.device or weights.shape[-1] != pairs or (
+                pairs > 1 and weights.stride(-1) != 1) or (stride and stride < pairs):
+            raise ValueError("weights must be float32 [.., n_q_heads / 2] with dense rows on the cache's device")
+        if out is not None:
+            out_ptr = self._dense(out, self._diff_shape, self.dtype, "out")
+        else:
+            out = self._own("diff", raw, self._diff_shape, self.dtype, stream)
+            out_ptr = out.data_ptr()
+        lse_ptr = None
+        if lse is not None:
+            lse_ptr = self._dense(lse, self._lse_shape, torch.float32, "lse")
+        elif return_lse:
+            lse = self._own("lse", raw, self._lse_shape, torch.float32, stream)
+            lse_ptr = lse.data_ptr()
+        norm_ptr = 0 if norm is None else self._dense(norm, self._diff_shape[2:], self.dtype, "norm")
+        d = _DIFF.pack(weights.data_ptr(), stride, norm_ptr, eps, gain)
+        self._check(self._diff_fn(self._ref, self._prefix_ref, d, q_ptr, *self._pool, out_ptr, lse_ptr, *self._ws, raw),
+                    "santa_diff_attention")
         return out if lse is None else (out, lse)
 
     def read(self, kv_offsets=None, rows: Optional[int] = None, *, K_out=None, V_out=None, stream=None):
