@@ -5,6 +5,7 @@
 // Bound by the reads of the pieces (D + 2 floats each, which the passes have
 // just left in the L2) and, for single tokens, by the chain of look-ups before
 // them; those of the batch are made while the last pass still runs.
+#include <algorithm>
 #include <type_traits>
 
 #include "santa_join.cuh"
@@ -34,77 +35,116 @@ template <> __device__ __forceinline__ float2 unpack16<fp16_t>(uint32_t r) {
   return __half22float2(h);
 }
 
-// Where the sums of one row in one pass are: `count` pieces; piece k at row
-// at0 (k = 0) or at1 + k step of arrays whose rows have `width` columns.
-struct Source {
-  const float *o, *ml;
-  long long at0, at1, step;
-  int count, width, column, parts, part;
+// A set of rows is up to R query heads of one token and KV head (differential:
+// one pair of heads, whose two maps follow each other).  In a pass of few rows
+// every lane looks for the row of head lane % R: its first piece and their
+// number; in one of chunks for the place of the set's note and the first row.
+struct Place {
+  unsigned at;
+  int count;
 };
-
-// Of row `i` of the pass's sequence vb, whose tokens are s: query head `head`
-// (its KV item `item`, g-th of the group, differential map e), columns from
-// `column` on.
-template <int D, bool DIFF>
-__device__ __forceinline__ Source find(const JoinArgs& a, int vb, const Seq& s, int i, int unit, int e, int column, long long row_at) {
-  Source r;
-  const int x = unit / a.G, g = unit - x * a.G;   // KV head (differential: pair of them), place in its group
-  constexpr int W = DIFF ? 2 * D : D;
-  const int dv = a.chunk ? W * x_items(a) / a.heads : W, parts = DIFF && a.e4m3 ? 2 : W / dv;
-  r.parts = parts;
-  r.part = parts == 2 ? column / D : 0;
+template <int D, bool DIFF, int R>
+__device__ __forceinline__ Place locate(const JoinArgs& a, int vb, const Seq& s, int i, int x, int g0, int lane) {
+  Place l;
   if (!a.chunk) {
-    const int rows = a.rows * (DIFF ? 2 : 1), pr = i * a.G + g, tile = pr / a.rows;
-    int i0, i1;
-    tile_tokens(a, s.n, tile, i0, i1);
-    r.count = max(1, (tile_keys(a, s, i0, i1, PG_BLK).blk + a.split_blk - 1) / a.split_blk);
-    r.o = a.part_o;
-    r.ml = a.part_ml;
-    r.width = W;
-    r.column = column;
-    r.at0 = r.at1 = ((((long long)vb * a.tiles + tile) * x_items(a) + x) * a.splits) * rows + e * a.rows + pr % a.rows;
-    r.step = rows;
-    return r;
+    const int shift = a.rows == 8 ? 3 : 4, pr = i * a.G + g0 + lane % R, tile = pr >> shift;
+    const unsigned i0 = (unsigned)(tile << shift) / (unsigned)a.G, i1 = (unsigned)((tile << shift) + a.rows - 1) / (unsigned)a.G;
+    const int blk = tile_keys(a, s, (int)i0, min((int)i1, s.n - 1), PG_BLK).blk;
+    l.count = max(1, (int)((unsigned)(blk + a.split_blk - 1) / (unsigned)a.split_blk));
+    const unsigned piece = ((unsigned)vb * a.tiles + tile) * x_items(a) + x;
+    l.at = (piece * a.splits << (DIFF ? shift + 1 : shift)) + (unsigned)(pr - (tile << shift));
+    return l;
   }
-  const int per = CHUNK_ROWS / a.G, tile = i / a.tokens, in = i - tile * a.tokens;
-  const int row = (DIFF ? e : in / per) * CHUNK_ROWS + in % per * a.G + g;
-  const int item = W == dv ? x : 2 * x + r.part;
-  const PieceNote n = a.notes[((long long)vb * a.tiles + tile) * a.heads + item];
-  if (n.count == 0) {
-    r.count = 1;
-    r.o = a.row_o;
-    r.ml = a.row_ml;
-    r.width = W;
-    r.column = column;
-    r.at0 = row_at;
-    r.at1 = r.step = 0;
-    return r;
-  }
-  r.count = n.count;
-  r.o = a.part_o;
-  r.ml = a.part_ml;
-  r.width = dv;
-  r.column = column % dv;
-  r.parts = 1;
-  r.part = 0;
-  r.at0 = ((long long)n.first * 2 + n.slot) * a.rows + row;
-  r.at1 = (long long)n.first * 2 * a.rows + row;
-  r.step = 2ll * a.rows;
-  return r;
+  const unsigned per = CHUNK_ROWS / (unsigned)a.G, tile = (unsigned)i / (unsigned)a.tokens, in = i - tile * a.tokens, sub = DIFF ? 0 : in / per;
+  const int part = a.heads == x_items(a) ? 0 : lane >> 4;   // columns of the second value head
+  l.at = ((unsigned)vb * a.tiles + tile) * a.heads + (a.heads == x_items(a) ? x : 2 * x + part);
+  l.count = (int)(sub * CHUNK_ROWS + (in - sub * per) * a.G) + g0;
+  return l;
 }
 
-// One warp per output row, or WPR = 4 where a row has many pieces: a running
-// maximum, U pieces requested at a time.
-template <typename T, int D, bool DIFF, int WPR>
-__global__ void __launch_bounds__(128) join_kernel(JoinArgs p, JoinArgs a) {
-  constexpr int W = DIFF ? 2 * D : D, E = W / 32, NE = DIFF ? 2 : 1, U = DIFF ? 4 : 8;
-  __shared__ float s_o[WPR][NE][W], s_ml[WPR][NE][32][2];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = WPR == 1 ? 0 : warp;
-  const int units = DIFF ? a.H / 2 : a.H, column = lane * E;
-  const long long w = (long long)blockIdx.x * (4 / WPR) + warp / WPR, t = w / units;
-  const int unit = (int)(w - t * units);
+// Where a pass left the sums of a set for this lane's columns: piece k at row
+// `at` (k = 0) or at + next + k step of arrays of `width` columns, the set's
+// further rows `rise` behind (few rows: looked up among the lanes).
+struct Sums {
+  const float *o, *ml;
+  unsigned at, next, step, rise;
+  int count, width, ml_step, map;   // map: from the first to the second map
+};
+template <int D, bool DIFF>
+__device__ __forceinline__ Sums sums(const JoinArgs& a, const Place& l, int column, unsigned row_at, bool there) {
+  Sums f;
+  constexpr int W = DIFF ? 2 * D : D;
+  if (!a.chunk) {
+    const int halves = DIFF && a.e4m3 ? 2 : 1;
+    f.o = a.part_o + column;
+    f.ml = a.part_ml + (halves == 2 && column >= D ? 2 : 0);
+    f.width = W;
+    f.ml_step = 2 * halves;
+    f.at = l.at;
+    f.count = l.count;
+    f.next = f.rise = 0;
+    f.step = a.rows * (DIFF ? 2 : 1);
+    f.map = a.rows;
+  } else {
+    const PieceNote n = there ? a.notes[l.at] : PieceNote{0, 0, 0, 0};
+    const bool whole = n.count == 0, halves = DIFF && a.heads != x_items(a);
+    const int dv = halves ? D : W;
+    f.o = whole ? a.row_o + column : a.part_o + (halves && column >= D ? column - D : column);
+    f.ml = whole ? a.row_ml + (halves && column >= D ? 2 : 0) : a.part_ml;
+    f.width = whole ? W : dv;
+    f.ml_step = whole && halves ? 4 : 2;
+    f.at = whole ? row_at : (unsigned)((n.first * 2 + n.slot) * a.rows + l.count);
+    f.count = max(n.count, 1);
+    f.next = 0u - (unsigned)(n.slot * a.rows);
+    f.step = 2 * a.rows;
+    f.rise = whole && DIFF ? 2 : 1;
+    f.map = whole ? 1 : CHUNK_ROWS;
+  }
+  if (!there) f.count = 0;
+  return f;
+}
+
+__device__ __forceinline__ int last_at_most(const int64_t* v, int n, long long t, int lane) {   // the last of n with v[i] <= t; the same in every lane
+  int lo = 0;
+  for (int stride = 1;;) {
+    for (stride = 1; (long long)stride * 32 < n - lo; stride *= 32);
+    const int i = lo + lane * stride;
+    const unsigned hit = __ballot_sync(FULL, i < n && v[i] <= t);
+    if (hit) lo += (31 - __clz(hit)) * stride;
+    if (stride == 1) return lo;
+    n = min(n, lo + stride);
+  }
+}
+
+struct Passes {
+  JoinArgs p[2];   // over the prefixes (n_groups 0: none), over what each sequence has of its own
+};
+
+// WARPS warps of a CTA share the pieces of a set, or (WARPS = 1) each of its
+// four warps has sets of its own.  A CTA has `sets` sets of a token, whose
+// look-ups are made once for them: one round for the sequence (32 offsets at a
+// time), one for its lengths, one for the notes, one for U pieces of RS rows.
+template <int WARPS> constexpr int join_threads() { return WARPS == 1 ? 128 : WARPS * 32; }
+
+template <typename T, int D, bool DIFF, int WARPS, int RS>
+__global__ void __launch_bounds__(join_threads<WARPS>(), WARPS == 16 ? 1 : 4) join_kernel(const __grid_constant__ Passes ps, int sets, int ctas) {
+  constexpr int W = DIFF ? 2 * D : D, E = W / 32, ROWS = DIFF ? 2 : RS, U = ROWS == 1 ? 4 : 2;
+  static_assert(!DIFF || RS == 1, "a pair at a time");
+  const JoinArgs &p = ps.p[0], &a = ps.p[1];
+  __shared__ float s_o[WARPS][ROWS][W], s_ml[WARPS][ROWS][32][2];
+  __shared__ int s_bad[WARPS];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = WARPS == 1 ? 0 : warp, column = lane * E;
+  const int units = DIFF ? a.H / 2 : a.H, per_x = (int)((unsigned)(a.G + RS - 1) / RS), all = x_items(a) * per_x;   // sets of a token
+  const unsigned t = blockIdx.x / (unsigned)ctas;
+  const int set0 = (int)(blockIdx.x - t * ctas) * sets, set_end = min(all, set0 + sets);
   int b;
-  if (t >= a.total_q || !paged_seq_of(a, t, b)) return wait_for_predecessor();
+  if (a.q_offsets) {
+    b = last_at_most(a.q_offsets, a.B, t, lane);
+    if (!(a.q_offsets[b] <= t && t < a.q_offsets[b + 1])) return wait_for_predecessor();
+  } else {
+    b = (int)(t / (unsigned)a.max_q);
+    if (b >= a.B) return wait_for_predecessor();
+  }
   const Seq s = paged_seq(a, b, false);
   const int i = (int)(t - s.q0);
   if (i >= s.n) return wait_for_predecessor();
@@ -115,137 +155,189 @@ __global__ void __launch_bounds__(128) join_kernel(JoinArgs p, JoinArgs a) {
     sp = paged_seq(p, g, false);
   }
   const bool prefix = s.ok && sp.kv > 0;
+  const int ip = prefix ? (int)(t - sp.q0) : 0;
+  const int first = set0 + (WARPS == 1 ? warp : 0);
+  Place own = {}, pre = {};
+  auto look = [&](int set) {
+    const int x = (int)((unsigned)set / (unsigned)per_x), g0 = (set - x * per_x) * RS;
+    own = locate<D, DIFF, RS>(a, b, s, i, x, g0, lane);
+    if (prefix) pre = locate<D, DIFF, RS>(p, g, sp, ip, x, g0, lane);
+  };
+  if (first < set_end) look(first);
   wait_for_predecessor();
-  float m[NE], l[NE], o[NE][E];
-  bool bad = false;
-#pragma unroll
-  for (int e = 0; e < NE; ++e) {
-    m[e] = -INFINITY;
-    l[e] = 0.f;
-#pragma unroll
-    for (int c = 0; c < E; ++c) o[e][c] = 0.f;
-    if (!s.ok) continue;
-    const long long row_at = t * a.H + (DIFF ? 2 * unit + e : unit);
-    const Source own = find<D, DIFF>(a, b, s, i, unit, e, column, row_at);
-    Source pre = own;
-    pre.count = 0;
-    if (prefix) pre = find<D, DIFF>(p, g, sp, (int)(t - sp.q0), unit, e, column, row_at);
-    const int count = own.count + pre.count;
 #pragma unroll 1
-    for (int k0 = part * U; k0 < count; k0 += WPR * U) {
-      float2 ml[U];
-      float y[U][E];
+  for (int set = first; set < set_end; set += WARPS == 1 ? 4 : 1) {
+    if (set != first) look(set);
+    const int x = (int)((unsigned)set / (unsigned)per_x), g0 = (set - x * per_x) * RS, rows = DIFF ? 2 : min(RS, a.G - g0), unit0 = x * a.G + g0;
+    const unsigned row_at = t * (unsigned)a.H + (DIFF ? 2 * unit0 : unit0);
+    const Sums f0 = sums<D, DIFF>(p, pre, column, row_at, prefix), f1 = sums<D, DIFF>(a, own, column, row_at, s.ok);
+    float m[ROWS], l[ROWS], o[ROWS][E];
+    unsigned at0[ROWS], at1[ROWS];
+    int n0[ROWS], n1[ROWS], most = 0;
+    bool bad = !s.ok;
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int k = k0 + u;
-        if (k >= count) continue;
-        const bool first = k < pre.count;
-        const Source& r = first ? pre : own;
-        const int kk = first ? k : k - pre.count;
-        const long long at = kk == 0 ? r.at0 : r.at1 + kk * r.step;
-        ml[u] = *reinterpret_cast<const float2*>(r.ml + (at * r.parts + r.part) * 2);
-        const float* const src = r.o + at * r.width + r.column;
+    for (int r = 0; r < ROWS; ++r) {
+      m[r] = -INFINITY;
+      l[r] = 0.f;
 #pragma unroll
-        for (int c = 0; c < E; c += 2) *reinterpret_cast<float2*>(&y[u][c]) = *reinterpret_cast<const float2*>(src + c);
+      for (int c = 0; c < E; ++c) o[r][c] = 0.f;
+      if (DIFF) {
+        at0[r] = f0.at + r * f0.map;
+        at1[r] = f1.at + r * f1.map;
+        n0[r] = f0.count;
+        n1[r] = f1.count;
+      } else {
+        const int from = p.chunk ? lane : r, from1 = a.chunk ? lane : r;   // few rows: the lane that looked for it
+        at0[r] = __shfl_sync(FULL, f0.at, from) + r * f0.rise;
+        at1[r] = __shfl_sync(FULL, f1.at, from1) + r * f1.rise;
+        n0[r] = __shfl_sync(FULL, f0.count, from);
+        n1[r] = __shfl_sync(FULL, f1.count, from1);
+        if (r >= rows) n0[r] = n1[r] = 0;
       }
-      float mn = m[e];
+      most = max(most, n0[r] + n1[r]);
+    }
+    // the pieces of both passes, one after the other, under a running maximum
+#pragma unroll 1
+    for (int k0 = part * U; k0 < most; k0 += WARPS * U) {
+      float2 ml[U][ROWS];
+      float y[U][ROWS][E];
 #pragma unroll
       for (int u = 0; u < U; ++u)
-        if (k0 + u < count) mn = fmaxf(mn, ml[u].x);
-      const float mu = mn > -INFINITY ? mn : 0.f, f0 = fast_exp2(m[e] - mu);
-      m[e] = mn;
-      l[e] *= f0;
 #pragma unroll
-      for (int c = 0; c < E; ++c) o[e][c] *= f0;
+        for (int r = 0; r < ROWS; ++r) {
+          ml[u][r] = make_float2(-INFINITY, 0.f);
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (k0 + u >= count) continue;
-        bad |= ml[u].y < 0.f;
-        const float f = fast_exp2(ml[u].x - mu);
-        l[e] = fmaf(ml[u].y, f, l[e]);
+          for (int c = 0; c < E; ++c) y[u][r][c] = 0.f;
+          const int k = k0 + u;
+          if (k >= n0[r] + n1[r]) continue;
+          const bool in0 = k < n0[r];
+          const int kk = in0 ? k : k - n0[r];
+          const unsigned at = (in0 ? at0[r] : at1[r]) + (kk == 0 ? 0u : (in0 ? f0.next : f1.next) + (unsigned)kk * (in0 ? f0.step : f1.step));
+          ml[u][r] = *reinterpret_cast<const float2*>((in0 ? f0.ml : f1.ml) + (size_t)at * (in0 ? f0.ml_step : f1.ml_step));
+          const float* const src = (in0 ? f0.o : f1.o) + (size_t)at * (in0 ? f0.width : f1.width);
+          if constexpr (E == 2) *reinterpret_cast<float2*>(y[u][r]) = *reinterpret_cast<const float2*>(src);
 #pragma unroll
-        for (int c = 0; c < E; ++c) o[e][c] = fmaf(y[u][c], f, o[e][c]);
+          for (int c = 0; c + 3 < E; c += 4) *reinterpret_cast<float4*>(&y[u][r][c]) = *reinterpret_cast<const float4*>(src + c);
+        }
+#pragma unroll
+      for (int r = 0; r < ROWS; ++r) {
+        float mn = m[r];
+#pragma unroll
+        for (int u = 0; u < U; ++u) mn = fmaxf(mn, ml[u][r].x);
+        const float mu = mn > -INFINITY ? mn : 0.f, old = fast_exp2(m[r] - mu);
+        m[r] = mn;
+        l[r] *= old;
+#pragma unroll
+        for (int c = 0; c < E; ++c) o[r][c] *= old;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          bad |= ml[u][r].y < 0.f;
+          const float w = fast_exp2(ml[u][r].x - mu);
+          l[r] = fmaf(ml[u][r].y, w, l[r]);
+#pragma unroll
+          for (int c = 0; c < E; ++c) o[r][c] = fmaf(y[u][r][c], w, o[r][c]);
+        }
       }
     }
-  }
-  if (WPR > 1) {   // a row's warps: the whole CTA came here
+    bad = __any_sync(FULL, bad);
+    if (WARPS > 1) {
+      if (set > first) __syncthreads();
 #pragma unroll
-    for (int e = 0; e < NE; ++e) {
-      s_ml[part][e][lane][0] = m[e];
-      s_ml[part][e][lane][1] = bad ? -1.f : l[e];
+      for (int r = 0; r < ROWS; ++r) {
+        s_ml[part][r][lane][0] = m[r];
+        s_ml[part][r][lane][1] = l[r];
 #pragma unroll
-      for (int c = 0; c < E; ++c) s_o[part][e][column + c] = o[e][c];
-    }
-    __syncthreads();
-    if (part) return;
-#pragma unroll
-    for (int e = 0; e < NE; ++e) {
-      float mn = m[e];
-#pragma unroll
-      for (int u = 1; u < WPR; ++u) mn = fmaxf(mn, s_ml[u][e][lane][0]);
-      const float mu = mn > -INFINITY ? mn : 0.f, f0 = fast_exp2(m[e] - mu);
-      m[e] = mn;
-      l[e] *= f0;
-#pragma unroll
-      for (int c = 0; c < E; ++c) o[e][c] *= f0;
-#pragma unroll
-      for (int u = 1; u < WPR; ++u) {
-        const float f = fast_exp2(s_ml[u][e][lane][0] - mu), lu = s_ml[u][e][lane][1];
-        bad |= lu < 0.f;
-        l[e] = fmaf(lu, f, l[e]);
-#pragma unroll
-        for (int c = 0; c < E; ++c) o[e][c] = fmaf(s_o[u][e][column + c], f, o[e][c]);
+        for (int c = 0; c < E; ++c) s_o[part][r][column + c] = o[r][c];
       }
+      if (lane == 0) s_bad[part] = bad;
+      __syncthreads();
+#pragma unroll
+      for (int u = 0; u < WARPS; ++u) bad |= s_bad[u] != 0;
+    }
+    float y[E];
+    bool empty = false;
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+      const int e = DIFF ? r : 0, unit = DIFF ? unit0 : unit0 + r;
+      if (r >= rows || (WARPS > 1 && (DIFF ? 0 : r % WARPS) != part)) continue;   // one warp has a row's end
+      float mm = m[r], ll = l[r], z[E];
+#pragma unroll
+      for (int c = 0; c < E; ++c) z[c] = o[r][c];
+      if (WARPS > 1) {
+        mm = -INFINITY;
+        ll = 0.f;
+#pragma unroll
+        for (int u = 0; u < WARPS; ++u) mm = fmaxf(mm, s_ml[u][r][lane][0]);
+        const float mu = mm > -INFINITY ? mm : 0.f;
+#pragma unroll
+        for (int c = 0; c < E; ++c) z[c] = 0.f;
+#pragma unroll
+        for (int u = 0; u < WARPS; ++u) {
+          const float w = fast_exp2(s_ml[u][r][lane][0] - mu);
+          ll = fmaf(s_ml[u][r][lane][1], w, ll);
+#pragma unroll
+          for (int c = 0; c < E; ++c) z[c] = fmaf(s_o[u][r][column + c], w, z[c]);
+        }
+      }
+      const bool none = bad || ll == 0.f;
+      empty = (e && empty) || none;
+      if (a.lse && lane == 0) {
+        // the sum's exponent goes to the maximum's side, so that the logarithm's argument is near 1
+        const int ex = (int)(__float_as_uint(ll) >> 23) - 127;
+        const float near1 = __uint_as_float((__float_as_uint(ll) & 0x7fffffu) | 0x3f800000u);
+        const float v = ll <= 3.402823466e38f ? (mm + (float)ex) * 0.6931471805599453f + __logf(near1) : ll;
+        a.lse[(size_t)t * a.H + (DIFF ? 2 * unit + e : unit)] = none ? -INFINITY : v;
+      }
+      float f = none ? 0.f : __fdividef(1.f, ll);
+      if (DIFF && e == 1) f *= -a.lambda[t * a.lambda_stride + unit];
+#pragma unroll
+      for (int c = 0; c < E; ++c) y[c] = e == 0 ? z[c] * f : fmaf(z[c], f, y[c]);
+      if (DIFF && e == 0) continue;
+      if (DIFF) {
+        float k = a.gain;
+        if (a.norm) {
+          float sq = 0.f;
+#pragma unroll
+          for (int c = 0; c < E; ++c) sq = fmaf(y[c], y[c], sq);
+#pragma unroll
+          for (int v = 16; v; v >>= 1) sq += __shfl_xor_sync(FULL, sq, v);
+          k *= 1.f / sqrtf(sq * (1.f / W) + a.eps);
+        }
+#pragma unroll
+        for (int c = 0; c < E; c += 2) {
+          float2 wt = make_float2(1.f, 1.f);
+          if (a.norm) wt = unpack16<T>(reinterpret_cast<const uint32_t*>(a.norm)[(column + c) / 2]);
+          y[c] *= k * wt.x;
+          y[c + 1] *= k * wt.y;
+        }
+      }
+      uint32_t w[E / 2];
+#pragma unroll
+      for (int c = 0; c < E; c += 2) w[c / 2] = empty ? 0u : pack16<T>(y[c], y[c + 1]);
+      T* const dst = static_cast<T*>(a.out) + ((size_t)t * units + unit) * W + column;
+      if constexpr (E == 2) *reinterpret_cast<uint32_t*>(dst) = w[0];
+      else if constexpr (E == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+      else *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
-  bad = __any_sync(FULL, bad) || !s.ok;
-  float y[E];
-  bool empty = false;
-#pragma unroll
-  for (int e = 0; e < NE; ++e) {
-    const bool none = bad || l[e] == 0.f;
-    empty |= none;
-    if (a.lse && lane == 0) {
-      // the sum's exponent goes to the maximum's side, so that the logarithm's argument is near 1
-      const int ex = (int)(__float_as_uint(l[e]) >> 23) - 127;
-      const float near1 = __uint_as_float((__float_as_uint(l[e]) & 0x7fffffu) | 0x3f800000u);
-      const float v = l[e] <= 3.402823466e38f ? (m[e] + (float)ex) * 0.6931471805599453f + __logf(near1) : l[e];
-      a.lse[t * a.H + (DIFF ? 2 * unit + e : unit)] = none ? -INFINITY : v;
-    }
-    float f = none ? 0.f : __fdividef(1.f, l[e]);
-    if (DIFF && e == 1) f *= -a.lambda[t * a.lambda_stride + unit];
-#pragma unroll
-    for (int c = 0; c < E; ++c) y[c] = e == 0 ? o[e][c] * f : fmaf(o[e][c], f, y[c]);
-  }
-  if (DIFF) {
-    float f = a.gain;
-    if (a.norm) {
-      float sq = 0.f;
-#pragma unroll
-      for (int c = 0; c < E; ++c) sq = fmaf(y[c], y[c], sq);
-#pragma unroll
-      for (int x = 16; x; x >>= 1) sq += __shfl_xor_sync(FULL, sq, x);
-      f *= 1.f / sqrtf(sq * (1.f / W) + a.eps);
-    }
-#pragma unroll
-    for (int c = 0; c < E; c += 2) {
-      float2 wt = make_float2(1.f, 1.f);
-      if (a.norm) wt = unpack16<T>(reinterpret_cast<const uint32_t*>(a.norm)[(column + c) / 2]);
-      y[c] *= f * wt.x;
-      y[c + 1] *= f * wt.y;
-    }
-  }
-  uint32_t* const dst = reinterpret_cast<uint32_t*>(static_cast<T*>(a.out) + (t * units + unit) * W + column);
-#pragma unroll
-  for (int c = 0; c < E; c += 2) dst[c / 2] = empty ? 0u : pack16<T>(y[c], y[c + 1]);
 }
 
+// How many warps share a set of rows, and how many sets a CTA has.
+template <typename T, int D, bool DIFF, int WARPS, int RS>
+cudaError_t sized(const JoinArgs& p, const JoinArgs& a) {
+  const int all = x_items(a) * ((a.G + RS - 1) / RS), least = WARPS == 1 ? 4 : 1;
+  const long long want = std::max<long long>(1, a.total_q * all / least / (12ll * a.num_sms));   // CTAs for about two rounds
+  const int ctas = (int)((all + least - 1) / least / std::min<long long>(want, (all + least - 1) / least));
+  const int sets = ((all + ctas - 1) / ctas + least - 1) / least * least, n = (all + sets - 1) / sets;
+  return launch_pass(join_kernel<T, D, DIFF, WARPS, RS>, (unsigned)(a.total_q * n), join_threads<WARPS>(), 0, a.stream, true, Passes{{p, a}}, sets, n);
+}
 template <typename T, int D, bool DIFF>
 cudaError_t rows(const JoinArgs& p, const JoinArgs& a) {
+  const int sources = (p.n_groups ? p.sources : 0) + a.sources;
   const long long n = a.total_q * (DIFF ? a.H / 2 : a.H);
-  if ((p.n_groups ? p.sources : 0) + a.sources > 8)
-    return launch_pass(join_kernel<T, D, DIFF, 4>, (unsigned)n, 128, 0, a.stream, true, p, a);
-  return launch_pass(join_kernel<T, D, DIFF, 1>, (unsigned)((n + 3) / 4), 128, 0, a.stream, true, p, a);
+  constexpr int RS = DIFF ? 1 : 4;
+  if (sources > 16 && n <= 2ll * a.num_sms) return sized<T, D, DIFF, 16, 1>(p, a);
+  return sources > 4 ? sized<T, D, DIFF, 4, RS>(p, a) : sized<T, D, DIFF, 1, RS>(p, a);
 }
 template <typename T>
 cudaError_t shape(const JoinArgs& p, const JoinArgs& a) {
