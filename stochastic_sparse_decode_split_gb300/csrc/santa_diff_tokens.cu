@@ -500,7 +500,8 @@ void plan_diff_tokens(JoinArgs& a, int span, int more_blocks) {
   a.rows = 8;
   a.tokens = 0;
   a.tiles = (int)(((long long)a.max_q * a.G + 7) / 8);
-  plan_splits(a, (long long)a.B * (a.Hkv / 2) * a.tiles, (long long)ctas * a.num_sms, (span + PG_BLK - 1) / PG_BLK + more_blocks);
+  const int blks = (span + PG_BLK - 1) / PG_BLK + more_blocks;
+  plan_splits(a, (long long)a.B * (a.Hkv / 2) * a.tiles, (long long)ctas * a.num_sms, blks, blks + 32);
 }
 
 cudaError_t launch_diff_tokens(const JoinArgs& a, bool behind) {

@@ -148,8 +148,8 @@ cudaError_t launch_pass(void (*kern)(P...), unsigned grid, int block, size_t sme
 }
 
 // Plans and launches of one pass, and of the kernel that joins two (prefixes.B = 0: none).
-void plan_tokens(PagedArgs& a, int span, int more_blocks);        // sets rows, tiles, splits, split_blk
-void plan_splits(PagedArgs& a, long long pieces, long long places, int blks);
+void plan_tokens(PagedArgs& a, int span, int more_blocks, int round = 0);   // sets rows, tiles, splits, split_blk
+void plan_splits(PagedArgs& a, long long pieces, long long places, int blks, int fine_blks);
 cudaError_t launch_join_tokens(const JoinArgs& a, bool behind);   // `behind`: starts under the pass before it
 cudaError_t launch_join_chunk(const JoinArgs& a, bool behind);
 void plan_diff_tokens(JoinArgs& a, int span, int more_blocks);

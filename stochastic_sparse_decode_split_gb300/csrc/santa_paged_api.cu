@@ -129,10 +129,17 @@ Plan plan(santa::PagedArgs& a) {
   return p;
 }
 
-// Differential heads: as above; the kernel for few rows takes eight at a time.
+// Differential heads: the kernel for few rows takes eight rows of both maps at a
+// time, and has the calls whose tiles meet at most 9216 blocks of 16 keys.
+// Measured, few rows against chunks, 32 and 8 heads of 128: at 4096 blocks (one
+// sequence of 2048 keys, 16 tokens) 20.6 against 26.7 us, of 8192 keys and 4
+// tokens 22.6 against 26.9; at 8192 blocks (8192 keys, 8 tokens) 28.8 against
+// 28.8, e4m3 28.8 against 32.9; at 16384 (16 tokens) 51.3 against 34.8, e4m3 43.1
+// against 37.0; 16 and 2 heads of 64, 16384 blocks (32768 keys, 8 tokens) 26.7
+// against 24.7, e4m3 34.9 against 29.9.
 bool few_diff(const santa::PagedArgs& a, int64_t span) {
   const int64_t rows = (int64_t)a.max_q * a.G;
-  return rows <= 8 || (rows + 7) / 8 <= 3 * 8192 * 16 / span / ((int64_t)a.B * a.Hkv);
+  return rows <= 8 || (rows + 7) / 8 <= 9216 * 16 / span / ((int64_t)a.B * (a.Hkv / 2));
 }
 
 // ---- attention in passes: a shared prefix, differential heads
@@ -158,7 +165,7 @@ void plan_pass(santa::JoinArgs& a, int64_t span, bool inside) {
   } else {
     a.chunk = !few_rows(a, span);
     if (a.chunk) a.tokens = 2 * (santa::CHUNK_ROWS / a.G);
-    else santa::plan_tokens(a, (int)span, inside);
+    else santa::plan_tokens(a, (int)span, inside, 32);   // sums are joined in any case: finer splits cost little
   }
   a.heads = santa::x_items(a);
   if (a.chunk) {
@@ -167,10 +174,44 @@ void plan_pass(santa::JoinArgs& a, int64_t span, bool inside) {
     a.tiles = (a.max_q + a.tokens - 1) / a.tokens;
     const int64_t items = (int64_t)a.B * a.heads * a.tiles, blocks = (span + santa::BKEYS - 1) / santa::BKEYS + inside;
     a.splits = (int)std::min<int64_t>(a.num_sms, items * blocks);
-    a.sources = (int)(a.splits / items) + 1;
+    a.sources = (int)(a.splits / items) + 1;   // of a pass that has the GPU for itself
   } else {
     a.sources = a.splits;
   }
+}
+
+// CTAs of a pass of chunks over the prefixes when the pass behind it is one of
+// few rows: that one, which HBM bounds, then runs on the other SMs from the
+// start on, under the start, the products and the stores of the first.  The
+// division is the best of a few by an estimate of both: a block of 256 rows and
+// 128 keys is 1.9 us of an SM (e4m3 2.6; heads of 64 0.7 of that, one tile of
+// rows half), and 15 us are start and end; the other pass's CTAs take 4 us and
+// their keys (half of what may be) at 45 GB/s per SM; what it has not done when
+// the first is over it does on all SMs.  Several prefixes count as 0.6 of their
+// bound each, and the first pass keeps at least 10 sixteenths.  Measured, 64 sequences of 100 to 2000
+// keys behind 32768, 32 and 8 heads of 128: 118 us on all SMs one after the
+// other, 99 with 120, 91 with 90, 92 with 76, 100 with 60.
+int prefix_ctas(const santa::JoinArgs& p, const santa::JoinArgs& own) {
+  const double tiles = std::min((double)p.B * p.tiles, (double)p.total_q / p.tokens + 0.5 * p.B);
+  const double blocks = tiles * p.heads * p.max_prefix / santa::BKEYS * (p.B > 1 ? 0.6 : 1.0);
+  const bool one = !p.diff && p.max_q <= p.tokens / 2;
+  const double first = blocks * (p.e4m3 ? 2.6 : 1.9) * (p.D == 64 ? 0.7 : 1.0) * (one ? 0.5 : 1.0);
+  const int per_sm = p.diff && !p.e4m3 && p.D == 128 ? 1 : 2;
+  const double ctas = (double)own.B * own.tiles * own.heads * own.splits, row = p.e4m3 ? p.D + 4.0 : 2.0 * p.D;
+  const double each = 4 + 0.5 * own.max_own / own.splits * 2 * row * (p.diff ? 2 : 1) * per_sm / 45e3;
+  int best = p.splits;
+  double least = 1e30;
+  for (int sixteenths = 16; sixteenths >= 10; --sixteenths) {
+    const int x = std::min(p.splits, p.num_sms * sixteenths / 16), rest = p.num_sms - x;
+    const double t1 = 15 + first / x, t2 = rest ? each * std::max(1.0, ctas / (rest * per_sm)) : 1e9;
+    const double all = each * std::max(1.0, ctas / (p.num_sms * per_sm));
+    const double t = t2 <= t1 ? t1 : t1 + std::max(each, all * (rest ? 1 - t1 / t2 : 1));
+    if (t < least) {
+      least = t;
+      best = x;
+    }
+  }
+  return best;
 }
 
 struct JoinPlan {
@@ -222,6 +263,7 @@ JoinPlan join_plan(const santa_paged_t* p, const santa_prefix_t* x, bool diff, v
     l.prefix.max_q = l.own.group_q;
     plan_pass(l.prefix, l.own.max_prefix, false);
     plan_pass(l.own, l.own.max_own, true);
+    if (l.prefix.chunk && !l.own.chunk) l.prefix.splits = prefix_ctas(l.prefix, l.own);
   } else {
     plan_pass(l.own, span_of(l.own), l.own.window != 0);
   }

@@ -141,18 +141,19 @@ cudaError_t merge_type(const PagedArgs& a, const cudaLaunchConfig_t& cfg) {
 // 3 tiles and 2 heads of 64, 28.6 us as 384 CTAs, 20.2 as 288 (with lengths from
 // 300 on 17.2 and 20.0); at 1.7 rounds (512, lengths from 300 on, e4m3) 33.4
 // us, 41.9 as 256.
-void plan_splits(PagedArgs& a, long long pieces, long long places, int blks) {
+void plan_splits(PagedArgs& a, long long pieces, long long places, int blks, int fine_blks) {
   long long want = std::max<long long>(1, places / pieces);
-  const long long fine = std::min<long long>(4 * places / pieces, blks / 64);
+  const long long fine = std::min<long long>(4 * places / pieces, fine_blks / 64);
   if (2 * fine * pieces >= 3 * places) want = std::max(want, fine);
   a.split_blk = (int)std::max<long long>(NW, (blks + want - 1) / want);
   a.splits = (blks + a.split_blk - 1) / a.split_blk;
 }
-void plan_tokens(PagedArgs& a, int span, int more_blocks) {
+void plan_tokens(PagedArgs& a, int span, int more_blocks, int round) {
   a.rows = a.max_q * a.G <= 8 ? 8 : 16;
   a.tokens = 0;
   a.tiles = (int)(((long long)a.max_q * a.G + a.rows - 1) / a.rows);
-  plan_splits(a, (long long)a.B * a.Hkv * a.tiles, 2ll * a.num_sms, (span + PG_BLK - 1) / PG_BLK + more_blocks);
+  const int blks = (span + PG_BLK - 1) / PG_BLK + more_blocks;
+  plan_splits(a, (long long)a.B * a.Hkv * a.tiles, 2ll * a.num_sms, blks, blks + round);
 }
 
 size_t plan_paged_tokens(PagedArgs& a) {
