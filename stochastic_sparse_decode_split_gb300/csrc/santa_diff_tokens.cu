@@ -30,7 +30,7 @@ struct DiffGeom {
 static_assert(NW * 16 * 256 * 4 <= DiffGeom<true, 128>::RING && NW * 16 * 128 * 4 <= DiffGeom<true, 64>::RING, "the merge lies over the rings");
 
 template <typename T, bool E4M3, int D>
-__global__ void __launch_bounds__(NT, DiffGeom<E4M3, D>::CTAS) diff_tokens_kernel(JoinArgs a) {
+__device__ __forceinline__ void diff_tokens(const JoinArgs& a, unsigned x, bool behind) {
   using Gm = Geom<E4M3, D>;
   using Dg = DiffGeom<E4M3, D>;
   using M16 = typename std::conditional<E4M3, fp16_t, T>::type;
@@ -43,11 +43,10 @@ __global__ void __launch_bounds__(NT, DiffGeom<E4M3, D>::CTAS) diff_tokens_kerne
   const int g8 = lane >> 2, t4 = lane & 3;
   allow_dependents();
   auto done = [&] {   // not over before the pass that it may have started under
-    if (blockIdx.x == 0) wait_for_predecessor();
+    if (behind) wait_for_predecessor();
   };
 
   // ---- which tile, which of its splits
-  unsigned x = blockIdx.x;
   const int split = x % a.splits;
   x /= a.splits;
   const int pair = x % a.heads;
@@ -479,18 +478,31 @@ __global__ void __launch_bounds__(NT, DiffGeom<E4M3, D>::CTAS) diff_tokens_kerne
 }
 
 template <typename T, bool E4M3, int D>
-cudaError_t inst(const JoinArgs& a, bool behind) {
-  auto kern = diff_tokens_kernel<T, E4M3, D>;
+__global__ void __launch_bounds__(NT, DiffGeom<E4M3, D>::CTAS) diff_tokens_kernel(const __grid_constant__ JoinArgs a) {
+  diff_tokens<T, E4M3, D>(a, blockIdx.x, blockIdx.x == 0);
+}
+// Both passes, `first` CTAs of the one over the prefixes.
+template <typename T, bool E4M3, int D>
+__global__ void __launch_bounds__(NT, DiffGeom<E4M3, D>::CTAS) diff_both_kernel(const __grid_constant__ Passes p, unsigned first) {
+  const bool own = blockIdx.x >= first;
+  diff_tokens<T, E4M3, D>(p.p[own], own ? blockIdx.x - first : blockIdx.x, false);
+}
+
+template <typename T, bool E4M3, int D>
+cudaError_t inst(const JoinArgs* p, const JoinArgs& a, bool behind) {
   constexpr int smem = DiffGeom<E4M3, D>::SMEM;
-  static std::atomic<unsigned long long> raised{0};
-  const cudaError_t e = raise_smem((const void*)kern, smem, raised);
+  const void* const kern = p ? (const void*)diff_both_kernel<T, E4M3, D> : (const void*)diff_tokens_kernel<T, E4M3, D>;
+  static std::atomic<unsigned long long> raised[2] = {{0}, {0}};
+  const cudaError_t e = raise_smem(kern, smem, raised[p != nullptr]);
   if (e != cudaSuccess) return e;
-  return launch_pass(kern, (unsigned)((long long)a.B * a.tiles * a.heads * a.splits), NT, smem, a.stream, behind, a);
+  if (!p) return launch_pass(diff_tokens_kernel<T, E4M3, D>, (unsigned)tokens_grid(a), NT, smem, a.stream, behind, a);
+  const unsigned first = (unsigned)tokens_grid(*p);
+  return launch_pass(diff_both_kernel<T, E4M3, D>, first + (unsigned)tokens_grid(a), NT, smem, a.stream, false, Passes{{*p, a}}, first);
 }
 template <typename T>
-cudaError_t type(const JoinArgs& a, bool behind) {
-  if (a.D == 128) return a.e4m3 ? inst<T, true, 128>(a, behind) : inst<T, false, 128>(a, behind);
-  return a.e4m3 ? inst<T, true, 64>(a, behind) : inst<T, false, 64>(a, behind);
+cudaError_t type(const JoinArgs* p, const JoinArgs& a, bool behind) {
+  if (a.D == 128) return a.e4m3 ? inst<T, true, 128>(p, a, behind) : inst<T, false, 128>(p, a, behind);
+  return a.e4m3 ? inst<T, true, 64>(p, a, behind) : inst<T, false, 64>(p, a, behind);
 }
 
 }  // namespace
@@ -504,8 +516,8 @@ void plan_diff_tokens(JoinArgs& a, int span, int more_blocks) {
   plan_splits(a, (long long)a.B * (a.Hkv / 2) * a.tiles, (long long)ctas * a.num_sms, blks, blks + 32);
 }
 
-cudaError_t launch_diff_tokens(const JoinArgs& a, bool behind) {
-  return a.dtype == 0 ? type<bf16_t>(a, behind) : type<fp16_t>(a, behind);
+cudaError_t launch_diff_tokens(const JoinArgs* prefixes, const JoinArgs& a, bool behind) {
+  return a.dtype == 0 ? type<bf16_t>(prefixes, a, behind) : type<fp16_t>(prefixes, a, behind);
 }
 
 }  // namespace santa

@@ -116,10 +116,6 @@ __device__ __forceinline__ int last_at_most(const int64_t* v, int n, long long t
   }
 }
 
-struct Passes {
-  JoinArgs p[2];   // over the prefixes (n_groups 0: none), over what each sequence has of its own
-};
-
 // WARPS warps of a CTA share the pieces of a set, or (WARPS = 1) each of its
 // four warps has sets of its own.  A CTA has `sets` sets of a token, whose
 // look-ups are made once for them: one round for the sequence (32 offsets at a

@@ -131,6 +131,12 @@ SANTA_HD const int32_t* page_row(const JoinArgs& a, int b) {
   return a.table + (long long)row * a.max_pages;
 }
 
+struct Passes {
+  JoinArgs p[2];   // over the prefixes (n_groups 0: none), over what each sequence has of its own
+};
+// CTAs of a pass of few rows.
+inline long long tokens_grid(const JoinArgs& a) { return (long long)a.B * a.tiles * a.heads * a.splits; }
+
 // A launch that may start while the kernel before it in the stream still runs (`behind`; programmatic dependent launch).
 template <typename... P, typename... X>
 cudaError_t launch_pass(void (*kern)(P...), unsigned grid, int block, size_t smem, cudaStream_t stream, bool behind, const X&... x) {
@@ -150,10 +156,11 @@ cudaError_t launch_pass(void (*kern)(P...), unsigned grid, int block, size_t sme
 // Plans and launches of one pass, and of the kernel that joins two (prefixes.B = 0: none).
 void plan_tokens(PagedArgs& a, int span, int more_blocks, int round = 0);   // sets rows, tiles, splits, split_blk
 void plan_splits(PagedArgs& a, long long pieces, long long places, int blks, int fine_blks);
-cudaError_t launch_join_tokens(const JoinArgs& a, bool behind);   // `behind`: starts under the pass before it
+// `behind`: starts under the pass before it; `prefixes`: in the same launch, of few rows too
+cudaError_t launch_join_tokens(const JoinArgs* prefixes, const JoinArgs& a, bool behind);
 cudaError_t launch_join_chunk(const JoinArgs& a, bool behind);
 void plan_diff_tokens(JoinArgs& a, int span, int more_blocks);
-cudaError_t launch_diff_tokens(const JoinArgs& a, bool behind);
+cudaError_t launch_diff_tokens(const JoinArgs* prefixes, const JoinArgs& a, bool behind);
 cudaError_t launch_diff_chunk(const JoinArgs& a, bool behind);
 cudaError_t launch_join(const JoinArgs& prefixes, const JoinArgs& own);
 

@@ -275,8 +275,8 @@ JoinPlan join_plan(const santa_paged_t* p, const santa_prefix_t* x, bool diff, v
   return l;
 }
 
-// Whether the grid of a pass has a number.
-bool fits(const santa::JoinArgs& a) { return a.chunk || (int64_t)a.B * a.tiles * a.heads <= INT32_MAX / a.splits; }
+// Whether the grid of a pass has a number, of two of them as well.
+bool fits(const santa::JoinArgs& a) { return a.chunk || (int64_t)a.B * a.tiles * a.heads <= INT32_MAX / 2 / a.splits; }
 
 santa_status_t join(const santa_paged_t* p, const santa_prefix_t* x, const santa_diff_t* d, const void* q, const void* K,
                     const void* V, const float* ks, const float* vs, void* out, float* lse, void* ws, size_t ws_bytes,
@@ -293,7 +293,7 @@ santa_status_t join(const santa_paged_t* p, const santa_prefix_t* x, const santa
   JoinPlan l = join_plan(p, x, d != nullptr, ws);
   st = check_cache(p, K, V, ks, vs, ws, ws_bytes, l.total);
   if (st != SANTA_OK) return st;
-  if ((x && !fits(l.prefix)) || !fits(l.own)) return SANTA_ERR_UNSUPPORTED;
+  if ((x && !fits(l.prefix)) || !fits(l.own)) return SANTA_ERR_UNSUPPORTED;   // their sum has a number, too
   for (santa::JoinArgs* a : {&l.prefix, &l.own}) {
     a->q = q;
     a->K = K;
@@ -312,12 +312,14 @@ santa_status_t join(const santa_paged_t* p, const santa_prefix_t* x, const santa
       a->gain = d->gain;
     }
   }
+  const bool both = x && !l.prefix.chunk && !l.own.chunk;   // in one launch
   auto launch = [&](const santa::JoinArgs& a, bool behind) {
-    if (a.diff) return a.chunk ? santa::launch_diff_chunk(a, behind) : santa::launch_diff_tokens(a, behind);
-    return a.chunk ? santa::launch_join_chunk(a, behind) : santa::launch_join_tokens(a, behind);
+    const santa::JoinArgs* const first = both ? &l.prefix : nullptr;
+    if (a.diff) return a.chunk ? santa::launch_diff_chunk(a, behind) : santa::launch_diff_tokens(first, a, behind);
+    return a.chunk ? santa::launch_join_chunk(a, behind) : santa::launch_join_tokens(first, a, behind);
   };
-  cudaError_t e = x ? launch(l.prefix, false) : cudaSuccess;
-  if (e == cudaSuccess) e = launch(l.own, x != nullptr);
+  cudaError_t e = x && !both ? launch(l.prefix, false) : cudaSuccess;
+  if (e == cudaSuccess) e = launch(l.own, x && !both);
   if (e == cudaSuccess) e = santa::launch_join(l.prefix, l.own);
   return e == cudaSuccess ? SANTA_OK : SANTA_ERR_CUDA;
 }

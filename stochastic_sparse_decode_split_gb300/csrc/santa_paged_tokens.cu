@@ -107,7 +107,7 @@ __global__ void __launch_bounds__(128) paged_merge_kernel(PagedArgs a) {
 
 template <typename T, bool E4M3, int D, int R>
 cudaError_t tokens_inst(const PagedArgs& a) {
-  auto kern = paged_tokens_kernel<T, E4M3, D, R, PagedArgs>;
+  auto kern = paged_tokens_kernel<T, E4M3, D, R>;
   constexpr int smem = (int)smem_bytes<E4M3, D, R>();
   static std::atomic<unsigned long long> raised{0};
   const cudaError_t e = raise_smem((const void*)kern, smem, raised);

@@ -118,8 +118,10 @@ constexpr size_t smem_bytes() {
 }
 
 // R: query rows per tile (8 or 16).
+// x: which split of which tile and KV head; `behind`: this CTA sees to it that the
+// pass that the launch may have started under is over before this one is.
 template <typename T, bool E4M3, int D, int R, typename A>
-__global__ void __launch_bounds__(NT, E4M3 ? 3 : 2) paged_tokens_kernel(A a) {
+__device__ __forceinline__ void paged_tokens(const A& a, unsigned x, bool behind) {
   constexpr bool JOIN = !std::is_same<A, PagedArgs>::value;   // all sums go to the pass's pieces
   using Gm = Geom<E4M3, D>;
   using M16 = typename std::conditional<E4M3, fp16_t, T>::type;   // the products' type
@@ -131,14 +133,11 @@ __global__ void __launch_bounds__(NT, E4M3 ? 3 : 2) paged_tokens_kernel(A a) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g8 = lane >> 2, t4 = lane & 3;
   allow_dependents();
-  // A pass may start under the one before it, whose sums the join needs as
-  // well: it is not over before that one is.
   auto done = [&] {
-    if (JOIN && blockIdx.x == 0) wait_for_predecessor();
+    if (JOIN && behind) wait_for_predecessor();
   };
 
   // ---- which tile, which of its splits
-  unsigned x = blockIdx.x;
   const int split = x % a.splits;
   x /= a.splits;
   const int kvh = x % a.Hkv;
@@ -588,6 +587,11 @@ __global__ void __launch_bounds__(NT, E4M3 ? 3 : 2) paged_tokens_kernel(A a) {
     }
   }
   done();
+}
+
+template <typename T, bool E4M3, int D, int R>
+__global__ void __launch_bounds__(NT, E4M3 ? 3 : 2) paged_tokens_kernel(PagedArgs a) {
+  paged_tokens<T, E4M3, D, R>(a, blockIdx.x, false);
 }
 
 }  // namespace
