@@ -286,6 +286,14 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
   constexpr bool JOIN = !std::is_same<A, PagedArgs>::value;
   static_assert(JOIN || !DIFF, "differential heads are joined");
   constexpr int DV = diff_columns<E4M3, D, DIFF>(), PARTS = DIFF ? 2 * D / DV : 1;   // items per pair of KV heads
+  // A row's scores 32 at a time, read from tensor memory once for the maximum and
+  // once for the exponentials, in loops: a quarter of the instructions, which
+  // a pass of few blocks waits for (they come from HBM, in competition with K and
+  // V: the first block's softmax took 7 us), and no spilled registers over e4m3.
+  // 64 tokens behind 32768 keys 87.5 -> 85.9 us, six e4m3 chunks in a window
+  // of 4096 202.7 -> 187.2.  All 128 at once where a CTA has many blocks of a
+  // 16-bit cache: 2048 tokens at 32768 keys 779 against 796 us.
+  constexpr bool SHORT = E4M3 || JOIN;
   using Gm = ChunkGeom<E4M3, D, DV, DIFF>;
   using M16 = typename std::conditional<E4M3, fp16_t, T>::type;
   constexpr float BIAS = fp16_bias<M16>(CHUNK_BIAS);
@@ -772,47 +780,76 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         const int key0 = (blk0 + j) * BKEYS;
         wait_phase(bar(S_FULL + t), jobs & 1, a.err, dead);
         tm_fence_after();
-        uint32_t sr[BKEYS];
-        if (E4M3) {
+        // 32 scores at a time: their scales (e4m3), the mask, the largest
+        const uint32_t sc = base + Gm::OFF_SC + ((n + j) & 3) * Gm::SC_STAGE;
+        const f2x sl_2 = pack2(sl, sl);
+        auto scale32 = [&](int c0, uint32_t* x) {
           // a key's three factors from shared memory: 96 loads of 16 bytes per
           // thread, at 128 bytes a cycle 3000 cycles for the eight warps of
           // both tiles, of which one tile waits for 1200 of its 3100
-          const uint32_t sc = base + Gm::OFF_SC + ((n + j) & 3) * Gm::SC_STAGE;
-          const f2x sl_2 = pack2(sl, sl);
 #pragma unroll
-          for (int c0 = 0; c0 < BKEYS; c0 += 32) {
-            tm_ld32(mS + c0, sr + c0);
+          for (int c = 0; c < 32; c += 4) {
+            const uint4 k4 = lds128(sc + ((DIFF ? t * 3 * BKEYS : 0) + c0 + c) * 4), v4 = lds128(sc + (BKEYS + c0 + c) * 4);
+            const f2x x0 = mul2(pack2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), sl_2);
+            const f2x x1 = mul2(pack2(__uint_as_float(x[c + 2]), __uint_as_float(x[c + 3])), sl_2);
+            const float2 y0 = unpack2(ffma2(x0, pack2(__uint_as_float(k4.x), __uint_as_float(k4.y)), pack2(__uint_as_float(v4.x), __uint_as_float(v4.y))));
+            const float2 y1 = unpack2(ffma2(x1, pack2(__uint_as_float(k4.z), __uint_as_float(k4.w)), pack2(__uint_as_float(v4.z), __uint_as_float(v4.w))));
+            x[c] = __float_as_uint(y0.x);
+            x[c + 1] = __float_as_uint(y0.y);
+            x[c + 2] = __float_as_uint(y1.x);
+            x[c + 3] = __float_as_uint(y1.y);
+          }
+        };
+        const bool partial = key0 < lo_last || key0 + BKEYS > hi_first;
+        auto mask32 = [&](int c0, uint32_t* x) {
+          const int from = lo - key0 - c0, cn = hi - lo;
+#pragma unroll
+          for (int c = 0; c < 32; ++c)
+            if ((unsigned)(c - from) >= (unsigned)cn) x[c] = 0xff800000u;
+        };
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        auto top32 = [&](const uint32_t* x) {
+#pragma unroll
+          for (int c = 0; c < 32; c += 8)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              mx[e] = fmaxf(fmaxf(mx[e], __uint_as_float(x[c + 2 * e])), __uint_as_float(x[c + 2 * e + 1]));
+        };
+        uint32_t sr[SHORT ? 32 : BKEYS];
+        if constexpr (SHORT) {
+#pragma unroll 1
+          for (int c = 0; c < BKEYS; c += 32) {
+            tm_ld32(mS + c, sr);
             tm_wait_ld();
-#pragma unroll
-            for (int c = c0; c < c0 + 32; c += 4) {
-              const uint4 k4 = lds128(sc + (DIFF ? t * 3 * BKEYS : 0) * 4 + c * 4), v4 = lds128(sc + (BKEYS + c) * 4);
-              const f2x x0 = mul2(pack2(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), sl_2);
-              const f2x x1 = mul2(pack2(__uint_as_float(sr[c + 2]), __uint_as_float(sr[c + 3])), sl_2);
-              const float2 y0 = unpack2(ffma2(x0, pack2(__uint_as_float(k4.x), __uint_as_float(k4.y)), pack2(__uint_as_float(v4.x), __uint_as_float(v4.y))));
-              const float2 y1 = unpack2(ffma2(x1, pack2(__uint_as_float(k4.z), __uint_as_float(k4.w)), pack2(__uint_as_float(v4.z), __uint_as_float(v4.w))));
-              sr[c] = __float_as_uint(y0.x);
-              sr[c + 1] = __float_as_uint(y0.y);
-              sr[c + 2] = __float_as_uint(y1.x);
-              sr[c + 3] = __float_as_uint(y1.y);
+            if (E4M3) scale32(c, sr);
+            if (partial) mask32(c, sr);
+            top32(sr);
+            if (E4M3) {   // the scores as they are now, for the second time
+              tm_st16(mS + c, sr);
+              tm_st16(mS + c + 16, sr + 16);
             }
           }
+          if (E4M3) tm_wait_st();
         } else {
+          if (E4M3) {
 #pragma unroll
-          for (int c = 0; c < BKEYS; c += 32) tm_ld32(mS + c, sr + c);
-          tm_wait_ld();
+            for (int c = 0; c < BKEYS; c += 32) {
+              tm_ld32(mS + c, sr + c);
+              tm_wait_ld();
+              scale32(c, sr + c);
+            }
+          } else {
+#pragma unroll
+            for (int c = 0; c < BKEYS; c += 32) tm_ld32(mS + c, sr + c);
+            tm_wait_ld();
+          }
+          if (partial) {
+#pragma unroll
+            for (int c = 0; c < BKEYS; c += 32) mask32(c, sr + c);
+          }
+#pragma unroll
+          for (int c = 0; c < BKEYS; c += 32) top32(sr + c);
         }
-        if (key0 < lo_last || key0 + BKEYS > hi_first) {
-          const int c0 = lo - key0, cn = hi - lo;
-#pragma unroll
-          for (int c = 0; c < BKEYS; ++c)
-            if ((unsigned)(c - c0) >= (unsigned)cn) sr[c] = 0xff800000u;
-        }
-        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-        for (int c = 0; c < BKEYS; c += 8)
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            mx[e] = fmaxf(fmaxf(mx[e], __uint_as_float(sr[c + 2 * e])), __uint_as_float(sr[c + 2 * e + 1]));
         const float mn = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * (E4M3 ? 1.f : sl) - BIAS);
         if (j == j_first) {
           m = mn;
@@ -832,20 +869,18 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
           }
         }
         const float neg = m > -INFINITY ? -m : 0.f;
-        const f2x neg2 = pack2(neg, neg), sl_2 = pack2(sl, sl);
-        const uint32_t sc = base + Gm::OFF_SC + ((n + j) & 3) * Gm::SC_STAGE + 2 * BKEYS * 4;
-#pragma unroll
-        for (int c = 0; c < BKEYS; c += 32) {
+        const f2x neg2 = pack2(neg, neg);
+        auto weigh32 = [&](int c, const uint32_t* x) {   // P of columns c .. c + 31
           uint32_t pk[16];
 #pragma unroll
           for (int e = 0; e < 32; e += 4) {
-            f2x x0 = pack2(__uint_as_float(sr[c + e]), __uint_as_float(sr[c + e + 1]));
-            f2x x1 = pack2(__uint_as_float(sr[c + e + 2]), __uint_as_float(sr[c + e + 3]));
+            f2x x0 = pack2(__uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+            f2x x1 = pack2(__uint_as_float(x[e + 2]), __uint_as_float(x[e + 3]));
             const float2 y0 = unpack2(E4M3 ? add2(x0, neg2) : ffma2(x0, sl_2, neg2));
             const float2 y1 = unpack2(E4M3 ? add2(x1, neg2) : ffma2(x1, sl_2, neg2));
             const float p0 = fast_exp2(y0.x), p1 = fast_exp2(y0.y), p2 = fast_exp2(y1.x), p3 = fast_exp2(y1.y);
             if (E4M3) {
-              const uint4 r4 = lds128(sc + (c + e) * 4);
+              const uint4 r4 = lds128(sc + (2 * BKEYS + c + e) * 4);
               l2[0] = ffma2(pack2(p0, p1), pack2(__uint_as_float(r4.x), __uint_as_float(r4.y)), l2[0]);
               l2[1] = ffma2(pack2(p2, p3), pack2(__uint_as_float(r4.z), __uint_as_float(r4.w)), l2[1]);
             } else {
@@ -857,6 +892,18 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
             pk[e / 2 + 1] = pack2h<M16>(p2, p3);
           }
           tm_st16(mS + c / 2, pk);
+        };
+        if constexpr (SHORT) {
+#pragma unroll 1
+          for (int c = 0; c < BKEYS; c += 32) {
+            tm_ld32(mS + c, sr);
+            tm_wait_ld();
+            if (!E4M3 && partial) mask32(c, sr);
+            weigh32(c, sr);
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < BKEYS; c += 32) weigh32(c, sr + c);
         }
         tm_wait_st();
         tm_fence_before();
@@ -937,7 +984,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         // all of the row's sums at once, so that the next piece's products may
         // overwrite them while this one is stored; 32 at a time over an e4m3
         // cache, where registers are fewer
-        constexpr int EC = E4M3 ? 32 : DV;
+        constexpr int EC = E4M3 || SHORT ? 32 : DV;
 #pragma unroll 1
         for (int c0 = 0; c0 < DV; c0 += EC) {
           float f[EC];
