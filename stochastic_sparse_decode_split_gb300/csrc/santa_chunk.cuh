@@ -16,7 +16,12 @@
 //                   (probabilities stay within a factor of 256, the result is the same)
 //   warp 8          issues the products: S_t = Q_t K^T and O_t += P_t V, so
 //                   that one tile's products run during the other's softmax
-//   warp 9          TMA: pages of K and V into two stages each (128-byte swizzle)
+//   warp 9          TMA: pages of K and V into two stages each (128-byte swizzle).
+//                   A box is a page's rows of 128 bytes, and what the unit can
+//                   take is 70 cycles a box of 16 rows: bringing later blocks
+//                   into the L2 beside it cost more than it gave (with
+//                   pages of 16, 1500 tokens of heads of 64 267 -> 214 us
+//                   without; of 64, 2048 tokens at 32768 keys 780 -> 761)
 //   warps 10, 11    16-bit caches: V rows past the last key become zeros, and
 //                   in blocks that not every row sees NaN and infinities, whose
 //                   product with a masked probability would not be zero, are
@@ -170,11 +175,6 @@ __device__ __forceinline__ void tma_load4(uint32_t dst, const CUtensorMap* tm, i
           dst),
       "l"((uint64_t)tm), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
       : "memory");
-}
-// The same box into the L2 only.
-__device__ __forceinline__ void tma_prefetch(const CUtensorMap* tm, int x, int y, int z) {
-  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"((uint64_t)tm), "r"(x), "r"(y), "r"(z)
-               : "memory");
 }
 // NaN or infinity among the eight 16-bit elements of a chunk.
 template <typename T>
@@ -466,7 +466,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         auto row_of = [&](int pid, int j) {   // first row of a lane's box
           return (pid << a.page_shift) + (((p.blk0 + j) * BKEYS + lane * rows) & ((1 << a.page_shift) - 1));
         };
-        int pid = page_of(0), pid1 = page_of(1), pid2 = page_of(2);
+        int pid = page_of(0), pid1 = page_of(1);
         for (int j = 0; j < p.nblk; ++j, ++n) {
           const int st = n & 1;
           const bool ok = pid != INT32_MIN && (unsigned)pid < (unsigned)a.n_pages;
@@ -526,21 +526,8 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                 tma_load(vd + h * Gm::HALF + lane * rows * 128, &tmV, 64 * h % D, v_head + 64 * h / D, row, bar(V_FULL + st));
             }
           }
-          // Two stages are less than HBM's latency: what comes two blocks on
-          // is brought into the L2 now.
-          if (pid2 != INT32_MIN && (unsigned)pid2 < (unsigned)a.n_pages) {
-            const int row2 = row_of(pid2, j + 2);
-#pragma unroll
-            for (int h = 0; h < (E4M3 ? 1 : D / 64); ++h) {
-              tma_prefetch(&tmK, 64 * h, k_head, row2);
-              if (DIFF) tma_prefetch(&tmK, 64 * h, k_head + 1, row2);
-            }
-#pragma unroll
-            for (int h = 0; h < (E4M3 ? 1 : DV / 64); ++h) tma_prefetch(&tmV, 64 * h % D, v_head + 64 * h / D, row2);
-          }
-          pid = pid1;
-          pid1 = pid2;
-          pid2 = page_of(j + 3);
+          pid = pid1;   // looked up two blocks ahead
+          pid1 = page_of(j + 2);
         }
         ++np;
       }
