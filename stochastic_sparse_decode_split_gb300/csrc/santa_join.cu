@@ -71,7 +71,7 @@ struct Sums {
   int count, width, ml_step, map;   // map: from the first to the second map
 };
 template <int D, bool DIFF>
-__device__ __forceinline__ Sums sums(const JoinArgs& a, const Place& l, int column, unsigned row_at, bool there) {
+__device__ __forceinline__ Sums sums(const JoinArgs& a, const Place& l, const PieceNote& n, int column, unsigned row_at, bool there) {
   Sums f;
   constexpr int W = DIFF ? 2 * D : D;
   if (!a.chunk) {
@@ -86,7 +86,6 @@ __device__ __forceinline__ Sums sums(const JoinArgs& a, const Place& l, int colu
     f.step = a.rows * (DIFF ? 2 : 1);
     f.map = a.rows;
   } else {
-    const PieceNote n = there ? a.notes[l.at] : PieceNote{0, 0, 0, 0};
     const bool whole = n.count == 0, halves = DIFF && a.heads != x_items(a);
     const int dv = halves ? D : W;
     f.o = whole ? a.row_o + column : a.part_o + (halves && column >= D ? column - D : column);
@@ -123,8 +122,8 @@ __device__ __forceinline__ int last_at_most(const int64_t* v, int n, long long t
 template <int WARPS> constexpr int join_threads() { return WARPS == 1 ? 128 : WARPS * 32; }
 
 template <typename T, int D, bool DIFF, int WARPS, int RS>
-__global__ void __launch_bounds__(join_threads<WARPS>(), WARPS == 16 ? 1 : 4) join_kernel(const __grid_constant__ Passes ps, int sets, int ctas) {
-  constexpr int W = DIFF ? 2 * D : D, E = W / 32, ROWS = DIFF ? 2 : RS, U = ROWS == 1 ? 4 : 2;
+__global__ void __launch_bounds__(join_threads<WARPS>(), WARPS == 16 ? 1 : WARPS == 1 && DIFF ? 6 : 4) join_kernel(const __grid_constant__ Passes ps, int sets, int ctas) {
+  constexpr int W = DIFF ? 2 * D : D, E = W / 32, ROWS = DIFF ? 2 : RS, U = WARPS == 1 && DIFF ? 1 : ROWS == 1 ? 4 : 2;
   static_assert(!DIFF || RS == 1, "a pair at a time");
   const JoinArgs &p = ps.p[0], &a = ps.p[1];
   __shared__ float s_o[WARPS][ROWS][W], s_ml[WARPS][ROWS][32][2];
@@ -159,14 +158,21 @@ __global__ void __launch_bounds__(join_threads<WARPS>(), WARPS == 16 ? 1 : 4) jo
     own = locate<D, DIFF, RS>(a, b, s, i, x, g0, lane);
     if (prefix) pre = locate<D, DIFF, RS>(p, g, sp, ip, x, g0, lane);
   };
+  // the notes of the next set are on their way while this one's sums are read
+  PieceNote own_note = {}, pre_note = {};
+  auto notes = [&] {
+    if (a.chunk && s.ok) own_note = a.notes[own.at];
+    if (p.chunk && prefix) pre_note = p.notes[pre.at];
+  };
   if (first < set_end) look(first);
   wait_for_predecessor();
+  if (first < set_end) notes();
 #pragma unroll 1
-  for (int set = first; set < set_end; set += WARPS == 1 ? 4 : 1) {
-    if (set != first) look(set);
+  for (int set = first; set < set_end; set += WARPS == 1 ? 4 : 1) {   // `own`, `pre` and the notes are this set's
     const int x = (int)((unsigned)set / (unsigned)per_x), g0 = (set - x * per_x) * RS, rows = DIFF ? 2 : min(RS, a.G - g0), unit0 = x * a.G + g0;
     const unsigned row_at = t * (unsigned)a.H + (DIFF ? 2 * unit0 : unit0);
-    const Sums f0 = sums<D, DIFF>(p, pre, column, row_at, prefix), f1 = sums<D, DIFF>(a, own, column, row_at, s.ok);
+    const Sums f0 = sums<D, DIFF>(p, pre, pre_note, column, row_at, prefix), f1 = sums<D, DIFF>(a, own, own_note, column, row_at, s.ok);
+    const int next = set + (WARPS == 1 ? 4 : 1);
     float m[ROWS], l[ROWS], o[ROWS][E];
     unsigned at0[ROWS], at1[ROWS];
     int n0[ROWS], n1[ROWS], most = 0;
@@ -191,6 +197,10 @@ __global__ void __launch_bounds__(join_threads<WARPS>(), WARPS == 16 ? 1 : 4) jo
         if (r >= rows) n0[r] = n1[r] = 0;
       }
       most = max(most, n0[r] + n1[r]);
+    }
+    if (next < set_end) {
+      look(next);
+      notes();
     }
     // the pieces of both passes, one after the other, under a running maximum
 #pragma unroll 1

@@ -106,9 +106,9 @@ santa::PagedArgs args(const santa_paged_t* p) {
 // 4096 keys, 8 KV heads, 32 rows) 22.1 against 28.9, e4m3 25.1 against 32.4; at
 // four thirds (128 rows) 29.4 against 21.9, heads of 128 (one sequence of 16384
 // keys, 64 rows) 39 against 31.9.
-bool few_rows(const santa::PagedArgs& a, int64_t span) {
+bool few_rows(const santa::PagedArgs& a, int64_t span, int64_t blocks = 3 * 8192) {
   const int64_t rows = (int64_t)a.max_q * a.G;
-  return rows <= 16 || (rows + 15) / 16 <= 3 * 8192 * 16 / span / ((int64_t)a.B * a.Hkv);
+  return rows <= 16 || (rows + 15) / 16 <= blocks * 16 / span / ((int64_t)a.B * a.Hkv);
 }
 int64_t span_of(const santa::PagedArgs& a) { return a.window ? std::min<int64_t>(a.nk, (int64_t)a.window + a.max_q) : a.nk; }
 bool few_rows(const santa::PagedArgs& a) { return few_rows(a, span_of(a)); }
@@ -137,9 +137,21 @@ Plan plan(santa::PagedArgs& a) {
 // 28.8, e4m3 28.8 against 32.9; at 16384 (16 tokens) 51.3 against 34.8, e4m3 43.1
 // against 37.0; 16 and 2 heads of 64, 16384 blocks (32768 keys, 8 tokens) 26.7
 // against 24.7, e4m3 34.9 against 29.9.
-bool few_diff(const santa::PagedArgs& a, int64_t span) {
+bool few_diff(const santa::PagedArgs& a, int64_t span, int64_t blocks) {
   const int64_t rows = (int64_t)a.max_q * a.G;
-  return rows <= 8 || (rows + 7) / 8 <= 9216 * 16 / span / ((int64_t)a.B * (a.Hkv / 2));
+  return rows <= 8 || (rows + 7) / 8 <= blocks * 16 / span / ((int64_t)a.B * (a.Hkv / 2));
+}
+// The borders of a pass over prefixes, whose chunks run beside the other pass.
+// Measured, few rows against chunks, one group, 1 to 300 keys of their own: 28
+// and 4 heads of 128 over 16 bits, 8192 blocks (8 sequences, 8192 keys) 22.3
+// against 22.2 us, 14336 (16 sequences) 25.1 against 24.4, 28672 (32) 35.2
+// against 30.5; 32 and 8 heads, e4m3, 16384 (16, 8192 keys) 31.5 against 33.0, 32768
+// 55.7 against 34.5.  Differential, 32 and 8 heads, 4096 blocks 26.5 against 29.9
+// and 25.6 against 26.2, 8192 33.0 against 27.5; e4m3 28.2 against 34.5, 35.6
+// against 33.7.
+int64_t border(const santa::JoinArgs& a) {
+  if (a.phase == 1) return a.diff ? 5120 : a.e4m3 ? 20480 : 12288;
+  return a.diff ? 9216 : 3 * 8192;
 }
 
 // ---- attention in passes: a shared prefix, differential heads
@@ -159,11 +171,11 @@ santa_status_t check_join(const santa_paged_t* p, const santa_prefix_t* x, bool 
 // A pass's kernel and the sizes of its sums; `span` keys, that may begin inside a block.
 void plan_pass(santa::JoinArgs& a, int64_t span, bool inside) {
   if (a.diff) {
-    a.chunk = !few_diff(a, span);
+    a.chunk = !few_diff(a, span, border(a));
     if (a.chunk) a.tokens = santa::CHUNK_ROWS / a.G;
     else santa::plan_diff_tokens(a, (int)span, inside);
   } else {
-    a.chunk = !few_rows(a, span);
+    a.chunk = !few_rows(a, span, border(a));
     if (a.chunk) a.tokens = 2 * (santa::CHUNK_ROWS / a.G);
     else santa::plan_tokens(a, (int)span, inside, 32);   // sums are joined in any case: finer splits cost little
   }
