@@ -237,7 +237,7 @@ __device__ __forceinline__ void take_share(const A& a, Share& sh, long long* s_s
   }
   const int heads = item_heads(a);
   const long long T = total * heads;
-  const int P = (int)min((long long)gridDim.x, T);
+  const int P = share_ctas(a, T, (int)min((long long)gridDim.x, T), all * heads, most);
   if ((int)blockIdx.x >= P) {
     if (tid == 0) sh.lo = sh.hi = sh.pos = 0;
     return;
@@ -366,7 +366,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                 note.slot = r.slot;
                 note.count = r.count;
               }
-              a.notes[((long long)p.b * a.tiles + p.tile) * item_heads(a) + p.kvh] = note;
+              a.notes[(p.s.q0 + p.i0) * item_heads(a) + p.kvh] = note;
             }
           }
           if (nblk == 0) continue;

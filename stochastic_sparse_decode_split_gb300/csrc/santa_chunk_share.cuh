@@ -121,6 +121,8 @@ SANTA_HD bool share_split(long long T, int P, long long items, int most) {
   const long long each = items <= P ? 1 : (items + P - 1) / P;
   return most > CHUNK_LEAST && each * most > T / P + CHUNK_SHARE;
 }
+// Of P CTAs those that take part.
+SANTA_HD int share_ctas(const PagedArgs&, long long, int P, long long, int) { return P; }
 SANTA_HD bool item_split(const PagedArgs&, long long T, int P, long long items, int most) { return share_split(T, P, items, most); }
 // The item that holds block lo, if it is item i = (sequence, tile), of w blocks
 // per KV head, whose blocks of one head begin at `first`.

@@ -5,7 +5,11 @@
 // hold here, with both heads of a pair at once: S_e^T = K_e q_e^T for the first
 // and the second map (e = 0, 1), a running softmax of each, and O_e^T +=
 // [V_0 V_1]^T P_e^T, so that every K and V row is read once; HBM bounds it.  A
-// block is 16 keys of four heads; a tile is eight query rows of each map.  The
+// block is 16 keys of four heads; a tile is eight query rows of each map, or,
+// where a sequence has no more than four of them (PACK), four of each, which
+// then share the eight columns of a product: half the exponentials and products
+// with V.  LATER
+// The
 // sums of the two maps stay apart (their difference is taken where all pieces
 // of a row are known, in santa_join.cu).  Over an e4m3 cache the two value
 // heads' scales differ, so each map has a maximum and probabilities for each.
@@ -18,23 +22,27 @@ namespace santa {
 
 namespace {
 
+// Stages are large, and CTAs start, merge and end: with one CTA of four warps
+// per SM and three stages a warp, 16 sequences of 1024 to 32768 keys took 119 us,
+// with two of two warps 109, with two of three warps and two stages 102.
 template <bool E4M3, int D>
 struct DiffGeom {
   using Gm = Geom<E4M3, D>;
   static constexpr int STAGE = 4 * Gm::KB + (E4M3 ? 4 * PG_BLK * 4 : 0);   // K_0, K_1, V_0, V_1, their scales
-  static constexpr int NS = STAGE >= 8192 ? 3 : 6;                         // stages per warp
-  static constexpr int CTAS = STAGE >= 16384 ? 1 : 2;                      // per SM
-  static constexpr int RING = NW * NS * STAGE;
+  static constexpr int WARPS = STAGE >= 16384 ? 3 : 4;                     // of a CTA
+  static constexpr int NS = STAGE >= 16384 ? 2 : STAGE >= 8192 ? 3 : 6;    // stages per warp
+  static constexpr int CTAS = 2;                                           // per SM
+  static constexpr int RING = WARPS * NS * STAGE, THREADS = WARPS * 32;
   static constexpr int SMEM = RING + 128;
 };
-static_assert(NW * 16 * 256 * 4 <= DiffGeom<true, 128>::RING && NW * 16 * 128 * 4 <= DiffGeom<true, 64>::RING, "the merge lies over the rings");
+static_assert(DiffGeom<true, 128>::WARPS * 16 * 256 * 4 <= DiffGeom<true, 128>::RING && DiffGeom<true, 64>::WARPS * 16 * 128 * 4 <= DiffGeom<true, 64>::RING, "the merge lies over the rings");
 
-template <typename T, bool E4M3, int D>
+template <typename T, bool E4M3, int D, bool PACK>
 __device__ __forceinline__ void diff_tokens(const JoinArgs& a, unsigned x, bool behind) {
   using Gm = Geom<E4M3, D>;
   using Dg = DiffGeom<E4M3, D>;
   using M16 = typename std::conditional<E4M3, fp16_t, T>::type;
-  constexpr int NS = Dg::NS, R = 8, F = E4M3 ? 2 : 1, NI = 2 * D / 16, W = 2 * D;   // F: maxima of a map
+  constexpr int NW = Dg::WARPS, NT = Dg::THREADS, NS = Dg::NS, R = PACK ? 4 : 8, NB = PACK ? 1 : 2, F = E4M3 ? 2 : 1, NI = 2 * D / 16, W = 2 * D;   // F: maxima of a map
   constexpr float BIAS = fp16_bias<M16>(TOKENS_BIAS);
   extern __shared__ __align__(128) unsigned char smem_raw[];
   __shared__ float s_m[NW][2][R][F], s_l[NW][2][R][F];
@@ -136,26 +144,29 @@ __device__ __forceinline__ void diff_tokens(const JoinArgs& a, unsigned x, bool 
 
   // ---- query fragments of both maps; rows past the last read as zero
   const T* const qp = static_cast<const T*>(a.q);
-  uint32_t bq[2][D / 16][2];
-  float sl[2][2];      // score factor of rows 2 t4 + hh
+  // columns of the products: 8 nb + c is row c of map nb, or row c % 4 of map c / 4
+  uint32_t bq[NB][D / 16][2];
+  float sl[NB][2];     // score factor of columns 2 t4 + hh
   int lo_[2], hi_[2];  // the keys they see
   int lo_all = 0, hi_all = INT32_MAX;   // keys that every row sees
   {
-    const int pr = row0 + g8;
+    const int pr = row0 + g8 % R;
+    const bool there = g8 % R < nrows;
     const long long tok = s.q0 + pr / a.G;
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
+    for (int nb = 0; nb < NB; ++nb) {
+      const int e = PACK ? g8 / 4 : nb;
       const uint32_t* q2 = reinterpret_cast<const uint32_t*>(qp + (tok * a.H + 2 * ((long long)pair * a.G + pr % a.G) + e) * D);
       float mx = 0.f;
 #pragma unroll
       for (int ks = 0; ks < D / 16; ++ks) {
         const int w0 = E4M3 ? 8 * ks + 2 * t4 : 8 * ks + t4, w1 = E4M3 ? w0 + 1 : w0 + 4;
-        bq[e][ks][0] = g8 < nrows ? __ldg(q2 + w0) : 0u;
-        bq[e][ks][1] = g8 < nrows ? __ldg(q2 + w1) : 0u;
+        bq[nb][ks][0] = there ? __ldg(q2 + w0) : 0u;
+        bq[nb][ks][1] = there ? __ldg(q2 + w1) : 0u;
         if (E4M3) {
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const float2 f = Pack<T>::unpack(bq[e][ks][i]);
+            const float2 f = Pack<T>::unpack(bq[nb][ks][i]);
             mx = fmaxf(mx, fmaxf(fabsf(f.x), fabsf(f.y)));
           }
         }
@@ -173,16 +184,16 @@ __device__ __forceinline__ void diff_tokens(const JoinArgs& a, unsigned x, bool 
         for (int ks = 0; ks < D / 16; ++ks)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const float2 f = Pack<T>::unpack(bq[e][ks][i]);
-            bq[e][ks][i] = Pack<M16>::pack(f.x * up, f.y * up);
+            const float2 f = Pack<T>::unpack(bq[nb][ks][i]);
+            bq[nb][ks][i] = Pack<M16>::pack(f.x * up, f.y * up);
           }
       }
 #pragma unroll
-      for (int hh = 0; hh < 2; ++hh) sl[e][hh] = a.sl2 * __shfl_sync(FULL, down, (2 * t4 + hh) * 4);
+      for (int hh = 0; hh < 2; ++hh) sl[nb][hh] = a.sl2 * __shfl_sync(FULL, down, (2 * t4 + hh) * 4);
     }
 #pragma unroll
     for (int hh = 0; hh < 2; ++hh) {
-      visible_keys(a, s, first_pos + (row0 + min(2 * t4 + hh, nrows - 1)) / a.G, lo_[hh], hi_[hh]);
+      visible_keys(a, s, first_pos + (row0 + min((2 * t4 + hh) % R, nrows - 1)) / a.G, lo_[hh], hi_[hh]);
       lo_all = max(lo_all, lo_[hh]);
       hi_all = min(hi_all, hi_[hh]);
     }
@@ -194,9 +205,9 @@ __device__ __forceinline__ void diff_tokens(const JoinArgs& a, unsigned x, bool 
   }
 
   // ---- the pass over the keys
-  float rm[2][F][2], rl[2][F][2], oacc[2][NI][4];
+  float rm[NB][F][2], rl[NB][F][2], oacc[NB][NI][4];
 #pragma unroll
-  for (int e = 0; e < 2; ++e) {
+  for (int e = 0; e < NB; ++e) {
 #pragma unroll
     for (int f = 0; f < F; ++f) {
       rm[e][f][0] = rm[e][f][1] = -INFINITY;
@@ -233,13 +244,17 @@ __device__ __forceinline__ void diff_tokens(const JoinArgs& a, unsigned x, bool 
           asm("rcp.approx.f32 %0, %1;" : "=f"(rv[f][j]) : "f"(v));
         }
     }
-    float p[2][F][2][2];   // [map][maximum][key g8 + 8 j][row hh]
-    float alpha[2][F][2];
-    bool moved = false;    // most blocks leave the maxima where they are
+    float p[NB][F][2][2];   // [columns][maximum][key g8 + 8 j][column hh]
+    float alpha[NB][F][2];
+    bool moved = false;     // most blocks leave the maxima where they are
+    float acc[2][2][4];
+    const bool second = t4 >> 1;   // PACK: the lane's columns are the second map's
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      float acc[2][4] = {};
+    for (int e = 0; e < 2; ++e) {   // scores with K_e; PACK: of all columns, half of which are taken
+      const int nb = PACK ? 0 : e;
       const uint32_t ke = kb + e * Gm::KB;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) acc[e][i][0] = acc[e][i][1] = acc[e][i][2] = acc[e][i][3] = 0.f;
       if (E4M3) {
 #pragma unroll
         for (int c = 0; c < D / 16; c += 2) {
@@ -248,7 +263,7 @@ __device__ __forceinline__ void diff_tokens(const JoinArgs& a, unsigned x, bool 
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const uint32_t fa[4] = {widen8(f[2 * i]), widen8(f[2 * i + 1]), widen8(f[2 * i] >> 16), widen8(f[2 * i + 1] >> 16)};
-            Mma<M16>::run(acc[i], fa, bq[e][c + i][0], bq[e][c + i][1]);
+            Mma<M16>::run(acc[e][i], fa, bq[nb][c + i][0], bq[nb][c + i][1]);
           }
         }
       } else {
@@ -256,13 +271,16 @@ __device__ __forceinline__ void diff_tokens(const JoinArgs& a, unsigned x, bool 
         for (int ks = 0; ks < D / 16; ++ks) {
           uint32_t f[4];
           ldmatrix_x4(ke + Gm::at(lrow, ks * 2 + lhalf), f);
-          Mma<M16>::run(acc[ks & 1], f, bq[e][ks][0], bq[e][ks][1]);
+          Mma<M16>::run(acc[e][ks & 1], f, bq[nb][ks][0], bq[nb][ks][1]);
         }
       }
+    }
+#pragma unroll
+    for (int e = 0; e < NB; ++e) {
       float ksc[2] = {1.f, 1.f};
       if (E4M3) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j) asm volatile("ld.shared.f32 %0, [%1];" : "=f"(ksc[j]) : "r"(sc + 64 * e + (g8 + 8 * j) * 4));
+        for (int j = 0; j < 2; ++j) asm volatile("ld.shared.f32 %0, [%1];" : "=f"(ksc[j]) : "r"(sc + 64 * (PACK ? (int)second : e) + (g8 + 8 * j) * 4));
       }
 #pragma unroll
       for (int f = 0; f < F; ++f)
@@ -274,7 +292,8 @@ __device__ __forceinline__ void diff_tokens(const JoinArgs& a, unsigned x, bool 
           for (int j = 0; j < 2; ++j) {
             const int key = key0 + g8 + 8 * j;
             vis[j] = whole || (key >= lo_[hh] && key < hi_[hh]);
-            const float v = (acc[0][2 * j + hh] + acc[1][2 * j + hh]) * sl[e][hh];
+            const float v0 = acc[e][0][2 * j + hh] + acc[e][1][2 * j + hh], v1 = acc[1][0][2 * j + hh] + acc[1][1][2 * j + hh];
+            const float v = (PACK && second ? v1 : v0) * sl[e][hh];
             y[j] = E4M3 ? fmaf(v, ksc[j], lv[f][j]) : v;
             if (!vis[j]) y[j] = -INFINITY;
             m = fmaxf(m, y[j]);
@@ -299,7 +318,7 @@ __device__ __forceinline__ void diff_tokens(const JoinArgs& a, unsigned x, bool 
     }
     if (__any_sync(FULL, moved)) {
 #pragma unroll
-      for (int e = 0; e < 2; ++e)
+      for (int e = 0; e < NB; ++e)
 #pragma unroll
         for (int i = 0; i < NI; ++i)
 #pragma unroll
@@ -334,7 +353,7 @@ __device__ __forceinline__ void diff_tokens(const JoinArgs& a, unsigned x, bool 
 #pragma unroll 1
       for (int key = 0; key < PG_BLK; ++key) {
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
+        for (int e = 0; e < NB; ++e)
 #pragma unroll
           for (int hh = 0; hh < 2; ++hh) {
             float pk[F];
@@ -370,9 +389,9 @@ __device__ __forceinline__ void diff_tokens(const JoinArgs& a, unsigned x, bool 
     // 16-bit head and the rounding of the rest: the difference of the maps
     // leaves less of the result than of its rounding
     constexpr bool REST = !E4M3;
-    uint32_t ph[2][F][2], pl[2][2];
+    uint32_t ph[NB][F][2], pl[NB][2];
 #pragma unroll
-    for (int e = 0; e < 2; ++e)
+    for (int e = 0; e < NB; ++e)
 #pragma unroll
       for (int f = 0; f < F; ++f)
 #pragma unroll
@@ -397,7 +416,7 @@ __device__ __forceinline__ void diff_tokens(const JoinArgs& a, unsigned x, bool 
             const uint32_t lo = __byte_perm(x4[2 * i], 0, 0x3120), hi = __byte_perm(x4[2 * i + 1], 0, 0x3120);
             const uint32_t fa[4] = {widen8(lo), widen8(lo >> 16), widen8(hi), widen8(hi >> 16)};
 #pragma unroll
-            for (int e = 0; e < 2; ++e) Mma<M16>::run(oacc[e][f * (NI / 2) + c + i], fa, ph[e][F - 1 ? f : 0][0], ph[e][F - 1 ? f : 0][1]);
+            for (int e = 0; e < NB; ++e) Mma<M16>::run(oacc[e][f * (NI / 2) + c + i], fa, ph[e][F - 1 ? f : 0][0], ph[e][F - 1 ? f : 0][1]);
           }
         }
       } else {
@@ -406,7 +425,7 @@ __device__ __forceinline__ void diff_tokens(const JoinArgs& a, unsigned x, bool 
           uint32_t x4[4];
           ldsm4_trans(vf + Gm::at(vrow, 2 * i + vhalf), x4);
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
+          for (int e = 0; e < NB; ++e) {
             Mma<M16>::run(oacc[e][f * (NI / 2) + i], x4, ph[e][0][0], ph[e][0][1]);
             if (REST) Mma<M16>::run(oacc[e][f * (NI / 2) + i], x4, pl[e][0], pl[e][1]);
           }
@@ -422,18 +441,18 @@ __device__ __forceinline__ void diff_tokens(const JoinArgs& a, unsigned x, bool 
   __syncthreads();
   float* const s_o = reinterpret_cast<float*>(smem_raw + ((128u - (smem_addr(smem_raw) & 127u)) & 127u));   // [NW][2][R][W]
 #pragma unroll
-  for (int e = 0; e < 2; ++e)
+  for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
     for (int hh = 0; hh < 2; ++hh) {
-      const int r = 2 * t4 + hh;
+      const int r = (2 * t4 + hh) % R, e = PACK ? t4 >> 1 : nb;
 #pragma unroll
       for (int f = 0; f < F; ++f) {
-        float l = rl[e][f][hh];
+        float l = rl[nb][f][hh];
         l += __shfl_xor_sync(FULL, l, 4);
         l += __shfl_xor_sync(FULL, l, 8);
         l += __shfl_xor_sync(FULL, l, 16);
         if (g8 == 0) {
-          s_m[warp][e][r][f] = rm[e][f][hh];
+          s_m[warp][e][r][f] = rm[nb][f][hh];
           s_l[warp][e][r][f] = l;
         }
       }
@@ -441,8 +460,8 @@ __device__ __forceinline__ void diff_tokens(const JoinArgs& a, unsigned x, bool 
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
         const int d = 16 * i + (E4M3 ? 2 * g8 : g8);
-        po[d] = oacc[e][i][hh];
-        po[d + (E4M3 ? 1 : 8)] = oacc[e][i][2 + hh];
+        po[d] = oacc[nb][i][hh];
+        po[d + (E4M3 ? 1 : 8)] = oacc[nb][i][2 + hh];
       }
     }
   __syncthreads();
@@ -477,43 +496,46 @@ __device__ __forceinline__ void diff_tokens(const JoinArgs& a, unsigned x, bool 
   done();
 }
 
-template <typename T, bool E4M3, int D>
-__global__ void __launch_bounds__(NT, DiffGeom<E4M3, D>::CTAS) diff_tokens_kernel(const __grid_constant__ JoinArgs a) {
-  diff_tokens<T, E4M3, D>(a, blockIdx.x, blockIdx.x == 0);
+template <typename T, bool E4M3, int D, bool PACK>
+__global__ void __launch_bounds__(DiffGeom<E4M3, D>::THREADS, DiffGeom<E4M3, D>::CTAS) diff_tokens_kernel(const __grid_constant__ JoinArgs a) {
+  diff_tokens<T, E4M3, D, PACK>(a, blockIdx.x, blockIdx.x == 0);
 }
 // Both passes, `first` CTAs of the one over the prefixes.
-template <typename T, bool E4M3, int D>
-__global__ void __launch_bounds__(NT, DiffGeom<E4M3, D>::CTAS) diff_both_kernel(const __grid_constant__ Passes p, unsigned first) {
-  const bool own = blockIdx.x >= first;
-  diff_tokens<T, E4M3, D>(p.p[own], own ? blockIdx.x - first : blockIdx.x, false);
+template <typename T, bool E4M3, int D, bool PACK>
+__global__ void __launch_bounds__(DiffGeom<E4M3, D>::THREADS, DiffGeom<E4M3, D>::CTAS) diff_both_kernel(const __grid_constant__ Passes p, unsigned first) {
+  if (blockIdx.x < first) diff_tokens<T, E4M3, D, false>(p.p[0], blockIdx.x, false);
+  else diff_tokens<T, E4M3, D, PACK>(p.p[1], blockIdx.x - first, false);
 }
 
-template <typename T, bool E4M3, int D>
+template <typename T, bool E4M3, int D, bool PACK>
 cudaError_t inst(const JoinArgs* p, const JoinArgs& a, bool behind) {
   constexpr int smem = DiffGeom<E4M3, D>::SMEM;
-  const void* const kern = p ? (const void*)diff_both_kernel<T, E4M3, D> : (const void*)diff_tokens_kernel<T, E4M3, D>;
+  const void* const kern = p ? (const void*)diff_both_kernel<T, E4M3, D, PACK> : (const void*)diff_tokens_kernel<T, E4M3, D, PACK>;
   static std::atomic<unsigned long long> raised[2] = {{0}, {0}};
   const cudaError_t e = raise_smem(kern, smem, raised[p != nullptr]);
   if (e != cudaSuccess) return e;
-  if (!p) return launch_pass(diff_tokens_kernel<T, E4M3, D>, (unsigned)tokens_grid(a), NT, smem, a.stream, behind, a);
+  if (!p) return launch_pass(diff_tokens_kernel<T, E4M3, D, PACK>, (unsigned)tokens_grid(a), DiffGeom<E4M3, D>::THREADS, smem, a.stream, behind, a);
   const unsigned first = (unsigned)tokens_grid(*p);
-  return launch_pass(diff_both_kernel<T, E4M3, D>, first + (unsigned)tokens_grid(a), NT, smem, a.stream, false, Passes{{*p, a}}, first);
+  return launch_pass(diff_both_kernel<T, E4M3, D, PACK>, first + (unsigned)tokens_grid(a), DiffGeom<E4M3, D>::THREADS, smem, a.stream, false, Passes{{*p, a}}, first);
+}
+template <typename T, bool E4M3, int D>
+cudaError_t rows(const JoinArgs* p, const JoinArgs& a, bool behind) {
+  return a.rows == 4 ? inst<T, E4M3, D, true>(p, a, behind) : inst<T, E4M3, D, false>(p, a, behind);
 }
 template <typename T>
 cudaError_t type(const JoinArgs* p, const JoinArgs& a, bool behind) {
-  if (a.D == 128) return a.e4m3 ? inst<T, true, 128>(p, a, behind) : inst<T, false, 128>(p, a, behind);
-  return a.e4m3 ? inst<T, true, 64>(p, a, behind) : inst<T, false, 64>(p, a, behind);
+  if (a.D == 128) return a.e4m3 ? rows<T, true, 128>(p, a, behind) : rows<T, false, 128>(p, a, behind);
+  return a.e4m3 ? rows<T, true, 64>(p, a, behind) : rows<T, false, 64>(p, a, behind);
 }
 
 }  // namespace
 
 void plan_diff_tokens(JoinArgs& a, int span, int more_blocks) {
-  const int ctas = a.D == 128 && !a.e4m3 ? DiffGeom<false, 128>::CTAS : DiffGeom<true, 128>::CTAS;
-  a.rows = 8;
+  a.rows = a.phase != 1 && (long long)a.max_q * a.G <= 4 ? 4 : 8;   // a group has more rows than its sequences
   a.tokens = 0;
-  a.tiles = (int)(((long long)a.max_q * a.G + 7) / 8);
+  a.tiles = (int)(((long long)a.max_q * a.G + a.rows - 1) / a.rows);
   const int blks = (span + PG_BLK - 1) / PG_BLK + more_blocks;
-  plan_splits(a, (long long)a.B * (a.Hkv / 2) * a.tiles, (long long)ctas * a.num_sms, blks, blks + 32);
+  plan_splits(a, (long long)a.B * (a.Hkv / 2) * a.tiles, 2ll * a.num_sms, blks, blks + 32);
 }
 
 cudaError_t launch_diff_tokens(const JoinArgs* prefixes, const JoinArgs& a, bool behind) {

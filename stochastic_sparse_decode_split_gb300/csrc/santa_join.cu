@@ -47,7 +47,7 @@ template <int D, bool DIFF, int R>
 __device__ __forceinline__ Place locate(const JoinArgs& a, int vb, const Seq& s, int i, int x, int g0, int lane) {
   Place l;
   if (!a.chunk) {
-    const int shift = a.rows == 8 ? 3 : 4, pr = i * a.G + g0 + lane % R, tile = pr >> shift;
+    const int shift = a.rows == 16 ? 4 : a.rows == 8 ? 3 : 2, pr = i * a.G + g0 + lane % R, tile = pr >> shift;
     const unsigned i0 = (unsigned)(tile << shift) / (unsigned)a.G, i1 = (unsigned)((tile << shift) + a.rows - 1) / (unsigned)a.G;
     const int blk = tile_keys(a, s, (int)i0, min((int)i1, s.n - 1), PG_BLK).blk;
     l.count = max(1, (int)((unsigned)(blk + a.split_blk - 1) / (unsigned)a.split_blk));
@@ -57,7 +57,7 @@ __device__ __forceinline__ Place locate(const JoinArgs& a, int vb, const Seq& s,
   }
   const unsigned per = CHUNK_ROWS / (unsigned)a.G, tile = (unsigned)i / (unsigned)a.tokens, in = i - tile * a.tokens, sub = DIFF ? 0 : in / per;
   const int part = a.heads == x_items(a) ? 0 : lane >> 4;   // columns of the second value head
-  l.at = ((unsigned)vb * a.tiles + tile) * a.heads + (a.heads == x_items(a) ? x : 2 * x + part);
+  l.at = ((unsigned)s.q0 + tile * a.tokens) * a.heads + (a.heads == x_items(a) ? x : 2 * x + part);
   l.count = (int)(sub * CHUNK_ROWS + (in - sub * per) * a.G) + g0;
   return l;
 }

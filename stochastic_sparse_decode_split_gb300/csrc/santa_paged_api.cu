@@ -208,13 +208,16 @@ int prefix_ctas(const santa::JoinArgs& p, const santa::JoinArgs& own) {
   const double blocks = tiles * p.heads * p.max_prefix / santa::BKEYS * (p.B > 1 ? 0.6 : 1.0);
   const bool one = !p.diff && p.max_q <= p.tokens / 2;
   const double first = blocks * (p.e4m3 ? 2.6 : 1.9) * (p.D == 64 ? 0.7 : 1.0) * (one ? 0.5 : 1.0);
-  const int per_sm = p.diff && !p.e4m3 && p.D == 128 ? 1 : 2;
+  constexpr int per_sm = 2;   // CTAs of the other pass
   const double ctas = (double)own.B * own.tiles * own.heads * own.splits, row = p.e4m3 ? p.D + 4.0 : 2.0 * p.D;
   const double each = 4 + 0.5 * own.max_own / own.splits * 2 * row * (p.diff ? 2 : 1) * per_sm / 45e3;
+  const int items = (int)std::min<int64_t>((int64_t)p.tiles * p.heads, p.num_sms);
   int best = p.splits;
   double least = 1e30;
   for (int sixteenths = 16; sixteenths >= 10; --sixteenths) {
-    const int x = std::min(p.splits, p.num_sms * sixteenths / 16), rest = p.num_sms - x;
+    int x = std::min(p.splits, p.num_sms * sixteenths / 16);
+    if (p.B == 1 && items < x) x = std::min(p.splits, (x + items - 1) / items * items);   // as many for each item
+    const int rest = p.num_sms - x;
     const double t1 = 15 + first / x, t2 = rest ? each * std::max(1.0, ctas / (rest * per_sm)) : 1e9;
     const double all = each * std::max(1.0, ctas / (p.num_sms * per_sm));
     const double t = t2 <= t1 ? t1 : t1 + std::max(each, all * (rest ? 1 - t1 / t2 : 1));
@@ -245,7 +248,7 @@ void lay_out(santa::JoinArgs& a, unsigned char* ws, size_t& at) {
     a.part_ml = reinterpret_cast<float*>(take(rows * 2 * sizeof(float)));
     a.row_o = reinterpret_cast<float*>(take(all * wide * sizeof(float)));
     a.row_ml = reinterpret_cast<float*>(take(all * 2 * (wide / cols) * sizeof(float)));
-    a.notes = reinterpret_cast<santa::PieceNote*>(take((size_t)a.B * a.tiles * a.heads * sizeof(santa::PieceNote)));
+    a.notes = reinterpret_cast<santa::PieceNote*>(take((size_t)a.total_q * a.heads * sizeof(santa::PieceNote)));
   } else {
     const size_t rows = (size_t)a.B * a.tiles * a.heads * a.splits * a.rows * (a.diff ? 2 : 1);
     a.part_o = reinterpret_cast<float*>(take(rows * wide * sizeof(float)));

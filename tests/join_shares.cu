@@ -55,7 +55,7 @@ int main() {
         total += w, items += w > 0, most = std::max(most, w);
       }
       const long long T = total * a.heads;
-      const int P = (int)std::min<long long>(places, T);
+      const int P = share_ctas(a, T, (int)std::min<long long>(places, T), items * a.heads, most);
       std::map<std::tuple<int, int, int>, std::vector<Part>> got;
       std::map<std::tuple<int, int, int>, std::vector<PieceNote>> notes;
       int outside = 0;
