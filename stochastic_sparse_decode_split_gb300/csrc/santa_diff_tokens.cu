@@ -8,7 +8,7 @@
 // block is 16 keys of four heads; a tile is eight query rows of each map, or,
 // where a sequence has no more than four of them (PACK), four of each, which
 // then share the eight columns of a product: half the exponentials and products
-// with V.  LATER
+// with V.
 // The
 // sums of the two maps stay apart (their difference is taken where all pieces
 // of a row are known, in santa_join.cu).  Over an e4m3 cache the two value

@@ -118,12 +118,13 @@ __device__ __forceinline__ int last_at_most(const int64_t* v, int n, long long t
 // WARPS warps of a CTA share the pieces of a set, or (WARPS = 1) each of its
 // four warps has sets of its own.  A CTA has `sets` sets of a token, whose
 // look-ups are made once for them: one round for the sequence (32 offsets at a
-// time), one for its lengths, one for the notes, one for U pieces of RS rows.
+// time), one for its lengths, one for the notes, then U pieces of the set's rows at
+// a time.
 template <int WARPS> constexpr int join_threads() { return WARPS == 1 ? 128 : WARPS * 32; }
 
-template <typename T, int D, bool DIFF, int WARPS, int RS>
-__global__ void __launch_bounds__(join_threads<WARPS>(), WARPS == 16 ? 1 : WARPS == 1 && DIFF ? 6 : 4) join_kernel(const __grid_constant__ Passes ps, int sets, int ctas) {
-  constexpr int W = DIFF ? 2 * D : D, E = W / 32, ROWS = DIFF ? 2 : RS, U = WARPS == 1 && DIFF ? 1 : ROWS == 1 ? 4 : 2;
+template <typename T, int D, bool DIFF, int WARPS, int RS, int U>
+__global__ void __launch_bounds__(join_threads<WARPS>(), WARPS == 16 ? 1 : WARPS == 1 && DIFF ? 6 : WARPS == 4 && U == 4 ? 3 : 4) join_kernel(const __grid_constant__ Passes ps, int sets, int ctas) {
+  constexpr int W = DIFF ? 2 * D : D, E = W / 32, ROWS = DIFF ? 2 : RS;
   static_assert(!DIFF || RS == 1, "a pair at a time");
   const JoinArgs &p = ps.p[0], &a = ps.p[1];
   __shared__ float s_o[WARPS][ROWS][W], s_ml[WARPS][ROWS][32][2];
@@ -329,21 +330,25 @@ __global__ void __launch_bounds__(join_threads<WARPS>(), WARPS == 16 ? 1 : WARPS
 }
 
 // How many warps share a set of rows, and how many sets a CTA has.
-template <typename T, int D, bool DIFF, int WARPS, int RS>
+template <typename T, int D, bool DIFF, int WARPS, int RS, int U>
 cudaError_t sized(const JoinArgs& p, const JoinArgs& a) {
   const int all = x_items(a) * ((a.G + RS - 1) / RS), least = WARPS == 1 ? 4 : 1;
   const long long want = std::max<long long>(1, a.total_q * all / least / (12ll * a.num_sms));   // CTAs for about two rounds
   const int ctas = (int)((all + least - 1) / least / std::min<long long>(want, (all + least - 1) / least));
   const int sets = ((all + ctas - 1) / ctas + least - 1) / least * least, n = (all + sets - 1) / sets;
-  return launch_pass(join_kernel<T, D, DIFF, WARPS, RS>, (unsigned)(a.total_q * n), join_threads<WARPS>(), 0, a.stream, true, Passes{{p, a}}, sets, n);
+  return launch_pass(join_kernel<T, D, DIFF, WARPS, RS, U>, (unsigned)(a.total_q * n), join_threads<WARPS>(), 0, a.stream, true, Passes{{p, a}}, sets, n);
 }
 template <typename T, int D, bool DIFF>
 cudaError_t rows(const JoinArgs& p, const JoinArgs& a) {
   const int sources = (p.n_groups ? p.sources : 0) + a.sources;
   const long long n = a.total_q * (DIFF ? a.H / 2 : a.H);
   constexpr int RS = DIFF ? 1 : 4;
-  if (sources > 16 && n <= 2ll * a.num_sms) return sized<T, D, DIFF, 16, 1>(p, a);
-  return sources > 4 ? sized<T, D, DIFF, 4, RS>(p, a) : sized<T, D, DIFF, 1, RS>(p, a);
+  if (sources > 16 && n <= 2ll * a.num_sms) return sized<T, D, DIFF, 16, 1, DIFF ? 2 : 4>(p, a);
+  if (sources <= 4) return sized<T, D, DIFF, 1, RS, DIFF ? 1 : 2>(p, a);
+  // few rows: what a warp has to read in one round rather than two, with more registers (sixteen tokens behind
+  // 8192 keys 21.5 -> 20.8 us; 64 behind 32768 the other way round, 87.7 -> 92.0; differential, 16 rows 8.3 -> 8.1,
+  // 512 44.9 -> 47.9)
+  return n <= (DIFF ? 2ll : 12ll) * a.num_sms ? sized<T, D, DIFF, 4, RS, 4>(p, a) : sized<T, D, DIFF, 4, RS, 2>(p, a);
 }
 template <typename T>
 cudaError_t shape(const JoinArgs& p, const JoinArgs& a) {

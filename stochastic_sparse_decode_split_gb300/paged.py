@@ -285,6 +285,7 @@ class PagedStep:
         self._kv_shape = torch.Size((self.total_q, cache.n_kv_heads, cache.head_dim))
         self._lse_shape, self._weight_shape = self._shape[:2], self._shape[2:]
         self._diff_shape = torch.Size((self.total_q, n_q_heads // 2, 2 * cache.head_dim))
+        self._pairs, self._norm_shape = self._diff_shape[1:2], self._diff_shape[2:]
         self._kept = (cache.K, cache.V, cache.k_scale, cache.v_scale)
         self._pool = tuple(ctypes.c_void_p(None if t is None else t.data_ptr()) for t in self._kept)
         self._ws = (ctypes.c_void_p(self.workspace.data_ptr()), ctypes.c_size_t(n))
@@ -320,14 +321,14 @@ class PagedStep:
     def _heads(self, x, shape, name):
         """Token rows of heads: any row stride, each row dense.  Returns the stride in elements."""
         row, head, one = x.stride() if x.dim() == 3 else (0, 0, 0)
-        if x.dtype is not self.dtype or x.shape != shape or x.device != self.device:
+        if x.dtype is not self.dtype or x.shape != shape or x.get_device() != self._index:   # -1: not on a GPU
             raise ValueError(f"{name} must be {self.dtype} {list(shape)} on the cache's device")
         if one != 1 or (head != shape[2] and shape[1] > 1):
             raise ValueError(f"the rows of {name} must be dense")
         return row if shape[0] > 1 else shape[1] * shape[2]
 
     def _dense(self, x, shape, dtype, name):
-        if x.dtype is not dtype or x.shape != shape or x.device != self.device or not x.is_contiguous():
+        if x.dtype is not dtype or x.shape != shape or x.get_device() != self._index or not x.is_contiguous():
             raise ValueError(f"{name} must be contiguous {dtype} {list(shape)} on the cache's device")
         return x.data_ptr()
 
@@ -437,15 +438,16 @@ class PagedStep:
         if not self.diff:
             raise ValueError("make the step with diff=True")
         q_ptr = self._dense(q, self._shape, self.dtype, "q")
-        pairs = self._diff_shape[1]
         stride = 0
-        if weights.dim() == 2 and weights.shape[0] == self.total_q and self.total_q > 1:
-            stride = weights.stride(0)
-        elif weights.dim() != 1 and not (weights.dim() == 2 and weights.shape[0] == self.total_q):
-            raise ValueError("weights must be [n_q_heads / 2] or [total_q, n_q_heads / 2]")
-        if weights.dtype is not torch.float32 or weights.device != self.device or weights.shape[-1] != pairs or (
-                pairs > 1 and weights.stride(-1) != 1) or (stride and stride < pairs):
-            raise ValueError("weights must be float32 [.., n_q_heads / 2] with dense rows on the cache's device")
+        if weights.shape != self._pairs or not weights.is_contiguous():   # not the same for all tokens
+            pairs = self._pairs[0]
+            if weights.shape != self._diff_shape[:2] or (pairs > 1 and weights.stride(1) != 1):
+                raise ValueError("weights must be [n_q_heads / 2] or [total_q, n_q_heads / 2] with dense rows")
+            stride = weights.stride(0) if self.total_q > 1 else 0
+            if 0 < stride < pairs:
+                raise ValueError("the rows of weights overlap")
+        if weights.dtype is not torch.float32 or weights.get_device() != self._index:
+            raise ValueError("weights must be float32 on the cache's device")
         if out is not None:
             out_ptr = self._dense(out, self._diff_shape, self.dtype, "out")
         else:
@@ -457,7 +459,7 @@ class PagedStep:
         elif return_lse:
             lse = self._own("lse", raw, self._lse_shape, torch.float32, stream)
             lse_ptr = lse.data_ptr()
-        norm_ptr = 0 if norm is None else self._dense(norm, self._diff_shape[2:], self.dtype, "norm")
+        norm_ptr = 0 if norm is None else self._dense(norm, self._norm_shape, self.dtype, "norm")
         d = _DIFF.pack(weights.data_ptr(), stride, norm_ptr, eps, gain)
         self._check(self._diff_fn(self._ref, self._prefix_ref, d, q_ptr, *self._pool, out_ptr, lse_ptr, *self._ws, raw),
                     "santa_diff_attention")
