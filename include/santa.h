@@ -281,8 +281,8 @@ santa_status_t santa_get_error(void* workspace, santa_stream_t stream, int32_t* 
  *                                written there, rows read from it come back zero, and the
  *                                attention rows that are computed with it come out zero
  *   SANTA_CACHE_DEVERR_POSITION  a position past the rotation table: the token is skipped
- *   SANTA_DEVERR_TIMEOUT         a bounded wait inside santa_paged_attention ran out: out is not to be used
- * The three calls share one workspace, cleared once by santa_workspace_init. */
+ *   SANTA_DEVERR_TIMEOUT         a bounded wait inside an attention kernel ran out: out is not to be used
+ * The calls of a batch share one workspace, cleared once by santa_workspace_init. */
 typedef struct {
   int32_t batch;              /* 1 .. 65535 */
   int32_t n_q_heads;          /* n_q_heads % n_kv_heads == 0, group <= SANTA_MAX_GROUP */

@@ -37,13 +37,13 @@
 // complete therefore says that the O of the same tile is too, which is when
 // the softmax may rescale it.
 //
-// Measured: 2048 tokens at 32768 keys, 32 and 8 heads of 128, bf16: 763 to 788
-// us, 1.35 to 1.39 PFLOP/s (0.70 to 0.72 of a library product's rate; the clock
-// falls from 1.86 to 1.74 GHz as the tensor cores fill, 700 us before); six chunks of up to 700
-// tokens over e4m3 in a window of 4096: 200 us.  There a block takes 4900
-// cycles: softmax 3100, issue of the products 1300, hand-overs 500 one after
-// another for a tile, the other tile in between; K left in e4m3, for products
-// of that kind with q as a sum of two or three such values, took as long.
+// Measured: 2048 tokens at 32768 keys, 32 and 8 heads of 128, bf16: 745 to 774
+// us, 1.37 to 1.43 PFLOP/s (0.72 to 0.75 of a library product's rate; the clock
+// falls from 1.86 to 1.74 GHz as the tensor cores fill); six chunks of up to 700
+// tokens over e4m3 in a window of 4096: 185 us, where for a tile softmax, issue
+// of the products and hand-overs follow one another, the other tile in between
+// (K left in e4m3, for products of that kind with q as a sum of two or three
+// such values, took as long).
 #pragma once
 
 #include <algorithm>

@@ -8,11 +8,16 @@
 // block is 16 keys of four heads; a tile is eight query rows of each map, or,
 // where a sequence has no more than four of them (PACK), four of each, which
 // then share the eight columns of a product: half the exponentials and products
-// with V.
-// The
-// sums of the two maps stay apart (their difference is taken where all pieces
-// of a row are known, in santa_join.cu).  Over an e4m3 cache the two value
-// heads' scales differ, so each map has a maximum and probabilities for each.
+// with V.  The sums of the two maps stay apart (their difference is taken where
+// all pieces of a row are known, in santa_join.cu).  Over an e4m3 cache the two
+// value heads' scales differ, so each map has a maximum and probabilities for
+// each.
+//
+// Measured: 16 sequences of 1024 to 32768 keys, 28 and 4 heads of 128, fp16: 102
+// us, 5.5 TB/s (0.82 of a copy's rate; CTAs' starts and ends, the join 8 us);
+// two of 131072 over e4m3, 32 and 8 heads: 107 us, 4.9 TB/s (142 with each map
+// in columns of its own: bound by its instructions); one token over 1000 keys
+// 8.3 us, two launches and their chains of look-ups.
 #include <type_traits>
 
 #include "santa_join.cuh"
