@@ -211,7 +211,8 @@ __device__ __forceinline__ void take_share(const A& a, Share& sh, long long* s_s
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   constexpr int NWP = NT / 32;
   const long long n = (long long)a.B * a.tiles;
-  const int mine = item_weight(a, tid, blockIdx.x == 0);
+  const Item item = item_at(a, tid, blockIdx.x == 0);
+  const int mine = item.w;
   int incl = scan_add(mine, lane), items = __popc(__ballot_sync(FULL, mine > 0)), most = (int)__reduce_max_sync(FULL, (unsigned)mine);
   long long sum = __shfl_sync(FULL, incl, 31);
   for (long long i = tid + NT; i < n + lane; i += NT) {   // whole warps
@@ -220,7 +221,10 @@ __device__ __forceinline__ void take_share(const A& a, Share& sh, long long* s_s
     items += __popc(__ballot_sync(FULL, w > 0));
     most = max(most, (int)__reduce_max_sync(FULL, (unsigned)w));
   }
-  if (tid == 0) sh.b = a.B;
+  if (tid == 0) {
+    sh.b = a.B;
+    sh.known = 0;
+  }
   if (lane == 0) {
     s_sum[warp] = sum;
     s_items[warp] = items;
@@ -251,13 +255,13 @@ __device__ __forceinline__ void take_share(const A& a, Share& sh, long long* s_s
     sh.split = item_split(a, T, P, all * heads, most);
   }
   if (n <= NT) {
-    share_place(a, sh, lo, tid, before + incl - mine, mine);
+    share_place(a, sh, lo, before + incl - mine, item);
     return;
   }
   long long base = 0;   // weight of the items before i0
   for (long long i0 = 0; i0 < n && base * heads <= lo; i0 += NT) {
-    const int w = item_weight(a, i0 + tid, false);
-    incl = scan_add(w, lane);
+    const Item x = item_at(a, i0 + tid, false);
+    incl = scan_add(x.w, lane);
     __syncthreads();
     if (lane == 31) s_sum[warp] = incl;
     __syncthreads();
@@ -267,7 +271,7 @@ __device__ __forceinline__ void take_share(const A& a, Share& sh, long long* s_s
       if (k < warp) before += s_sum[k];
       base += s_sum[k];
     }
-    share_place(a, sh, lo, i0 + tid, before + incl - w, w);
+    share_place(a, sh, lo, before + incl - x.w, x);
   }
 }
 
@@ -316,15 +320,17 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
   if (tid == 0) {
     s_dead = 0;
     for (int i = 0; i < 4; ++i) s_bad[i] = s_odd[i] = 0;
-    for (int i = 0; i < N_BAR; ++i) {
-      const int count = i == Q_READY || i == PIECE_SEEN ? 8
-                        : i == K_READY || i == K_READY + 1 ? 4
-                        : i == V_READY || i == V_READY + 1 ? (E4M3 ? 4 : 2)
-                        : i == P_FULL || i == P_FULL + 1 || i == O_FREE || i == O_FREE + 1 || i == ML_FULL || i == Q_SEEN ? 4 : 1;
-      mbar_init(bar(i), (unsigned)count);
-    }
-    mbar_fence_init();
     if (!JOIN) a.share[blockIdx.x].count = 0;
+  }
+  static_assert(N_BAR <= 64, "a lane of warps 10 and 11 each");
+  if (tid >= 320 && tid < 320 + N_BAR) {   // warps that have nothing else to do yet
+    const int i = tid - 320;
+    const int count = i == Q_READY || i == PIECE_SEEN ? 8
+                      : i == K_READY || i == K_READY + 1 ? 4
+                      : i == V_READY || i == V_READY + 1 ? (E4M3 ? 4 : 2)
+                      : i == P_FULL || i == P_FULL + 1 || i == O_FREE || i == O_FREE + 1 || i == ML_FULL || i == Q_SEEN ? 4 : 1;
+    mbar_init(bar(i), (unsigned)count);
+    mbar_fence_init();
   }
   if (warp == 8) tm_alloc(smem_addr(&s_tm), 512);
   if (tid == 288) {

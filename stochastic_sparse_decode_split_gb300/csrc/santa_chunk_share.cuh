@@ -22,6 +22,9 @@ struct Share {
   int P, split;
   int b, kvh, tile;   // the item that holds block lo
   long long pos;      // its first block
+  int known, i0, i1;  // whether its sequence, tokens and keys are here, too
+  Seq s;
+  TileKeys tk;
 };
 SANTA_HD long long share_begin(long long T, int c, int P) {
   if (T < (1ll << 24)) return (unsigned)T * (unsigned)c / (unsigned)P;   // c < 256
@@ -47,7 +50,14 @@ struct Walk {
     kvh = sh.kvh;
     tile = sh.tile;
     pos = sh.pos;
-    if (b < a.B) load(a);
+    if (sh.known) {   // looked up once for all roles
+      s = sh.s;
+      i0 = sh.i0;
+      i1 = sh.i1;
+      tk = sh.tk;
+    } else if (b < a.B) {
+      load(a);
+    }
   }
   template <typename A>
   SANTA_HD void load(const A& a) {   // a sequence and its tile
@@ -99,16 +109,32 @@ struct Walk {
   }
 };
 
-// Blocks of item i = (sequence, tile), 0 where the tile has no token.
+// Item i = (sequence, tile): its blocks w, at least one, 0 where the tile has no token.
+struct Item {
+  int w, b, tile, i0, i1;
+  Seq s;
+  TileKeys tk;
+};
+template <typename A>
+SANTA_HD Item item_at(const A& a, long long i, bool flag) {
+  Item x;
+  x.w = 0;
+  if (i >= (long long)a.B * a.tiles) return x;
+  x.b = i < (1ll << 31) ? (int)((unsigned)i / (unsigned)a.tiles) : (int)(i / a.tiles);   // 32-bit division takes a fifth of the time
+  x.tile = (int)(i - (long long)x.b * a.tiles);
+  x.s = paged_seq(a, x.b, flag && x.tile == 0);
+  if (x.tile * a.tokens >= x.s.n) return x;
+  tile_tokens(a, x.s.n, x.tile, x.i0, x.i1);
+  x.tk = tile_keys(a, x.s, x.i0, x.i1, BKEYS);
+  x.w = max(x.tk.blk, 1);
+  return x;
+}
 template <typename A>
 SANTA_HD int item_weight(const A& a, long long i, bool flag) {
-  if (i >= (long long)a.B * a.tiles) return 0;
-  const int b = (int)(i / a.tiles), tile = (int)(i - (long long)b * a.tiles);
-  const Seq s = paged_seq(a, b, flag && tile == 0);
-  if (tile * a.tokens >= s.n) return 0;
-  int i0, i1;
-  tile_tokens(a, s.n, tile, i0, i1);
-  return max(tile_keys(a, s, i0, i1, BKEYS).blk, 1);
+  return item_at(a, i, flag).w;
+}
+SANTA_HD long long quotient(long long n, int d) {   // of numbers that are small as a rule
+  return n < (1ll << 31) ? (long long)((unsigned)n / (unsigned)d) : n / d;
 }
 
 // Whether items are shared between CTAs, from their number, the blocks of the
@@ -118,8 +144,8 @@ SANTA_HD int item_weight(const A& a, long long i, bool flag) {
 // differs between CTAs (their shares do, by one block): an item that one CTA
 // leaves to be shared and the next one does not take up would be lost.
 SANTA_HD bool share_split(long long T, int P, long long items, int most) {
-  const long long each = items <= P ? 1 : (items + P - 1) / P;
-  return most > CHUNK_LEAST && each * most > T / P + CHUNK_SHARE;
+  const long long each = items <= P ? 1 : quotient(items + P - 1, P);
+  return most > CHUNK_LEAST && each * most > quotient(T, P) + CHUNK_SHARE;
 }
 // Of P CTAs those that take part.
 SANTA_HD int share_ctas(const PagedArgs&, long long, int P, long long, int) { return P; }
@@ -134,6 +160,20 @@ SANTA_HD void share_place(const A& a, Share& sh, long long lo, long long i, long
   sh.tile = (int)(i - (long long)sh.b * a.tiles);
   sh.kvh = (int)(lo - pos) / w;
   sh.pos = pos + (long long)sh.kvh * w;
+}
+template <typename A>
+SANTA_HD void share_place(const A& a, Share& sh, long long lo, long long first, const Item& x) {
+  const long long pos = first * item_heads(a);
+  if (x.w == 0 || lo < pos || lo >= pos + (long long)x.w * item_heads(a)) return;
+  sh.b = x.b;
+  sh.tile = x.tile;
+  sh.kvh = (int)(lo - pos) / x.w;
+  sh.pos = pos + (long long)sh.kvh * x.w;
+  sh.s = x.s;
+  sh.i0 = x.i0;
+  sh.i1 = x.i1;
+  sh.tk = x.tk;
+  sh.known = 1;
 }
 // What CTA `cta`, which has the last piece of a shared item, leaves for the merge.
 SANTA_HD ChunkShare share_note(const Share& sh, const Piece& p, int cta) {

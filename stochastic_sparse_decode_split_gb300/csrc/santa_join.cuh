@@ -122,15 +122,15 @@ SANTA_HD int x_items(const JoinArgs& a) { return a.diff ? a.Hkv / 2 : a.Hkv; }  
 // The sums of a pass are joined in any case, so that sharing an item costs little.
 constexpr int JOIN_SHARE = 2;
 SANTA_HD bool item_split(const JoinArgs&, long long T, int P, long long items, int most) {
-  const long long each = items <= P ? 1 : (items + P - 1) / P;
-  return most > 1 && each * most > T / P + JOIN_SHARE;
+  const long long each = items <= P ? 1 : quotient(items + P - 1, P);
+  return most > 1 && each * most > quotient(T, P) + JOIN_SHARE;
 }
 // Items that are all as long (one group's) are divided into the same number of
 // pieces each, so that no CTA has the end of one and the start of another: the
 // second piece costs 8 us.  32 differential tokens behind 16384 keys, 8 items:
 // 43.8 us with 96 CTAs, 49.0 with 95.
 SANTA_HD int share_ctas(const JoinArgs&, long long T, int P, long long items, int most) {
-  return items <= P && items * most == T ? (int)(P / items * items) : P;
+  return items <= P && items * most == T ? P / (int)items * (int)items : P;
 }
 // A group's prefix is looked up in the table's row of its first sequence.
 SANTA_HD const int32_t* page_row(const JoinArgs& a, int b) {
