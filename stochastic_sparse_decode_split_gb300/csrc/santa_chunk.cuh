@@ -281,8 +281,8 @@ __device__ __forceinline__ void take_share(const A& a, Share& sh, long long* s_s
 // DIFF (with JoinArgs): differential heads.  The two tiles are the same 128
 // rows of the first and of the second query heads; each has K blocks of its own
 // (stage t of K is tile t's), and both use the same columns of V: those of both
-// value heads where they are 128 together, else an item has those of one.  Over
-// an e4m3 cache, whose two value heads differ in their scales, it always has.
+// value heads of 64, or, over an e4m3 cache, where their scales differ, those of
+// one (heads of 128 over 16 bits: santa_diff_wide.cu).
 template <typename T, bool E4M3, int D, typename A, bool DIFF>
 __global__ void __launch_bounds__(ChunkGeom<E4M3, D, diff_columns<E4M3, D, DIFF>(), DIFF>::THREADS, 1)
 paged_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,

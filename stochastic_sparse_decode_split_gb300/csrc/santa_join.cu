@@ -56,7 +56,7 @@ __device__ __forceinline__ Place locate(const JoinArgs& a, int vb, const Seq& s,
     return l;
   }
   const unsigned per = CHUNK_ROWS / (unsigned)a.G, tile = (unsigned)i / (unsigned)a.tokens, in = i - tile * a.tokens, sub = DIFF ? 0 : in / per;
-  const int part = a.heads == x_items(a) ? 0 : lane >> 4;   // columns of the second value head
+  const int part = a.heads == x_items(a) || a.wide ? 0 : lane >> 4;   // columns of the second value head
   l.at = ((unsigned)s.q0 + tile * a.tokens) * a.heads + (a.heads == x_items(a) ? x : 2 * x + part);
   l.count = (int)(sub * CHUNK_ROWS + (in - sub * per) * a.G) + g0;
   return l;
@@ -86,7 +86,7 @@ __device__ __forceinline__ Sums sums(const JoinArgs& a, const Place& l, const Pi
     f.step = a.rows * (DIFF ? 2 : 1);
     f.map = a.rows;
   } else {
-    const bool whole = n.count == 0, halves = DIFF && a.heads != x_items(a);
+    const bool whole = n.count == 0, halves = DIFF && a.heads != x_items(a) && !a.wide;
     const int dv = halves ? D : W;
     f.o = whole ? a.row_o + column : a.part_o + (halves && column >= D ? column - D : column);
     f.ml = whole ? a.row_ml + (halves && column >= D ? 2 : 0) : a.part_ml;
@@ -97,7 +97,7 @@ __device__ __forceinline__ Sums sums(const JoinArgs& a, const Place& l, const Pi
     f.next = 0u - (unsigned)(n.slot * a.rows);
     f.step = 2 * a.rows;
     f.rise = whole && DIFF ? 2 : 1;
-    f.map = whole ? 1 : CHUNK_ROWS;
+    f.map = whole ? 1 : a.wide ? 0 : CHUNK_ROWS;   // wide: each map has pieces of its own
   }
   if (!there) f.count = 0;
   return f;
@@ -123,7 +123,7 @@ __device__ __forceinline__ int last_at_most(const int64_t* v, int n, long long t
 template <int WARPS> constexpr int join_threads() { return WARPS == 1 ? 128 : WARPS * 32; }
 
 template <typename T, int D, bool DIFF, int WARPS, int RS, int U>
-__global__ void __launch_bounds__(join_threads<WARPS>(), WARPS == 16 ? 1 : WARPS == 1 && DIFF ? 6 : WARPS == 4 && U == 4 ? 3 : 4) join_kernel(const __grid_constant__ Passes ps, int sets, int ctas) {
+__global__ void __launch_bounds__(join_threads<WARPS>(), WARPS == 16 ? 1 : WARPS == 1 && DIFF ? (D == 128 ? 5 : 6) : WARPS == 4 && U == 4 ? 3 : 4) join_kernel(const __grid_constant__ Passes ps, int sets, int ctas) {
   constexpr int W = DIFF ? 2 * D : D, E = W / 32, ROWS = DIFF ? 2 : RS;
   static_assert(!DIFF || RS == 1, "a pair at a time");
   const JoinArgs &p = ps.p[0], &a = ps.p[1];
@@ -160,10 +160,17 @@ __global__ void __launch_bounds__(join_threads<WARPS>(), WARPS == 16 ? 1 : WARPS
     if (prefix) pre = locate<D, DIFF, RS>(p, g, sp, ip, x, g0, lane);
   };
   // the notes of the next set are on their way while this one's sums are read
-  PieceNote own_note = {}, pre_note = {};
-  auto notes = [&] {
-    if (a.chunk && s.ok) own_note = a.notes[own.at];
-    if (p.chunk && prefix) pre_note = p.notes[pre.at];
+  constexpr int NE = DIFF && D == 128 ? 2 : 1;
+  PieceNote own_note[NE] = {}, pre_note[NE] = {};
+  auto notes = [&] {   // wide: one for each map
+    if (a.chunk && s.ok) {
+      own_note[0] = a.notes[own.at];
+      if (NE == 2 && a.wide) own_note[NE - 1] = a.notes[own.at + 1];
+    }
+    if (p.chunk && prefix) {
+      pre_note[0] = p.notes[pre.at];
+      if (NE == 2 && p.wide) pre_note[NE - 1] = p.notes[pre.at + 1];
+    }
   };
   if (first < set_end) look(first);
   wait_for_predecessor();
@@ -172,7 +179,15 @@ __global__ void __launch_bounds__(join_threads<WARPS>(), WARPS == 16 ? 1 : WARPS
   for (int set = first; set < set_end; set += WARPS == 1 ? 4 : 1) {   // `own`, `pre` and the notes are this set's
     const int x = (int)((unsigned)set / (unsigned)per_x), g0 = (set - x * per_x) * RS, rows = DIFF ? 2 : min(RS, a.G - g0), unit0 = x * a.G + g0;
     const unsigned row_at = t * (unsigned)a.H + (DIFF ? 2 * unit0 : unit0);
-    const Sums f0 = sums<D, DIFF>(p, pre, pre_note, column, row_at, prefix), f1 = sums<D, DIFF>(a, own, own_note, column, row_at, s.ok);
+    Sums f0[NE], f1[NE];
+    f0[0] = sums<D, DIFF>(p, pre, pre_note[0], column, row_at, prefix);
+    f1[0] = sums<D, DIFF>(a, own, own_note[0], column, row_at, s.ok);
+    if constexpr (NE == 2) {
+      f0[1] = f0[0];
+      f1[1] = f1[0];
+      if (p.wide) f0[1] = sums<D, DIFF>(p, pre, pre_note[1], column, row_at, prefix);
+      if (a.wide) f1[1] = sums<D, DIFF>(a, own, own_note[1], column, row_at, s.ok);
+    }
     const int next = set + (WARPS == 1 ? 4 : 1);
     float m[ROWS], l[ROWS], o[ROWS][E];
     unsigned at0[ROWS], at1[ROWS];
@@ -185,16 +200,17 @@ __global__ void __launch_bounds__(join_threads<WARPS>(), WARPS == 16 ? 1 : WARPS
 #pragma unroll
       for (int c = 0; c < E; ++c) o[r][c] = 0.f;
       if (DIFF) {
-        at0[r] = f0.at + r * f0.map;
-        at1[r] = f1.at + r * f1.map;
-        n0[r] = f0.count;
-        n1[r] = f1.count;
+        const int e = NE == 2 ? r : 0;
+        at0[r] = f0[e].at + r * f0[e].map;
+        at1[r] = f1[e].at + r * f1[e].map;
+        n0[r] = f0[e].count;
+        n1[r] = f1[e].count;
       } else {
         const int from = p.chunk ? lane : r, from1 = a.chunk ? lane : r;   // few rows: the lane that looked for it
-        at0[r] = __shfl_sync(FULL, f0.at, from) + r * f0.rise;
-        at1[r] = __shfl_sync(FULL, f1.at, from1) + r * f1.rise;
-        n0[r] = __shfl_sync(FULL, f0.count, from);
-        n1[r] = __shfl_sync(FULL, f1.count, from1);
+        at0[r] = __shfl_sync(FULL, f0[0].at, from) + r * f0[0].rise;
+        at1[r] = __shfl_sync(FULL, f1[0].at, from1) + r * f1[0].rise;
+        n0[r] = __shfl_sync(FULL, f0[0].count, from);
+        n1[r] = __shfl_sync(FULL, f1[0].count, from1);
         if (r >= rows) n0[r] = n1[r] = 0;
       }
       most = max(most, n0[r] + n1[r]);
@@ -219,9 +235,10 @@ __global__ void __launch_bounds__(join_threads<WARPS>(), WARPS == 16 ? 1 : WARPS
           if (k >= n0[r] + n1[r]) continue;
           const bool in0 = k < n0[r];
           const int kk = in0 ? k : k - n0[r];
-          const unsigned at = (in0 ? at0[r] : at1[r]) + (kk == 0 ? 0u : (in0 ? f0.next : f1.next) + (unsigned)kk * (in0 ? f0.step : f1.step));
-          ml[u][r] = *reinterpret_cast<const float2*>((in0 ? f0.ml : f1.ml) + (size_t)at * (in0 ? f0.ml_step : f1.ml_step));
-          const float* const src = (in0 ? f0.o : f1.o) + (size_t)at * (in0 ? f0.width : f1.width);
+          const Sums &x0 = f0[NE == 2 ? r : 0], &x1 = f1[NE == 2 ? r : 0];
+          const unsigned at = (in0 ? at0[r] : at1[r]) + (kk == 0 ? 0u : (in0 ? x0.next : x1.next) + (unsigned)kk * (in0 ? x0.step : x1.step));
+          ml[u][r] = *reinterpret_cast<const float2*>((in0 ? x0.ml : x1.ml) + (size_t)at * (in0 ? x0.ml_step : x1.ml_step));
+          const float* const src = (in0 ? x0.o : x1.o) + (size_t)at * (in0 ? x0.width : x1.width);
           if constexpr (E == 2) *reinterpret_cast<float2*>(y[u][r]) = *reinterpret_cast<const float2*>(src);
 #pragma unroll
           for (int c = 0; c + 3 < E; c += 4) *reinterpret_cast<float4*>(&y[u][r][c]) = *reinterpret_cast<const float4*>(src + c);

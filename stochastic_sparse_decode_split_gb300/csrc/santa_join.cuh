@@ -38,7 +38,7 @@ struct JoinArgs : PagedArgs {
   PieceNote* notes;                // chunks: [total_q, heads], at an item's first token
   int sources;                     // pieces of a row, about
   // differential heads: the weights of the second maps, the norm behind them
-  int diff;
+  int diff, wide;                  // wide: an item is a map, over the columns of both value heads
   const float* lambda;
   long long lambda_stride;         // from token to token (0: the same for all)
   const void* norm;                // [2 D] or null
@@ -169,6 +169,7 @@ cudaError_t launch_join_chunk(const JoinArgs& a, bool behind);
 void plan_diff_tokens(JoinArgs& a, int span, int more_blocks);
 cudaError_t launch_diff_tokens(const JoinArgs* prefixes, const JoinArgs& a, bool behind);
 cudaError_t launch_diff_chunk(const JoinArgs& a, bool behind);
+cudaError_t launch_diff_wide(const JoinArgs& a, bool behind);
 cudaError_t launch_join(const JoinArgs& prefixes, const JoinArgs& own);
 
 }  // namespace santa

@@ -181,8 +181,9 @@ void plan_pass(santa::JoinArgs& a, int64_t span, bool inside) {
   }
   a.heads = santa::x_items(a);
   if (a.chunk) {
-    if (a.diff && (a.e4m3 || a.D == 128)) a.heads *= 2;   // an item for each value head
-    a.rows = 2 * santa::CHUNK_ROWS;
+    a.wide = a.diff && !a.e4m3 && a.D == 128;
+    if (a.diff && (a.e4m3 || a.D == 128)) a.heads *= 2;   // an item for each value head, or (wide) for each map
+    a.rows = (a.wide ? 1 : 2) * santa::CHUNK_ROWS;
     a.tiles = (a.max_q + a.tokens - 1) / a.tokens;
     const int64_t items = (int64_t)a.B * a.heads * a.tiles, blocks = (span + santa::BKEYS - 1) / santa::BKEYS + inside;
     a.splits = (int)std::min<int64_t>(a.num_sms, items * blocks);
@@ -196,32 +197,34 @@ void plan_pass(santa::JoinArgs& a, int64_t span, bool inside) {
 // few rows: that one, which HBM bounds, then runs on the other SMs from the
 // start on, under the start, the products and the stores of the first.  The
 // division is the best of a few by an estimate of both: a block of 256 rows and
-// 128 keys is 1.9 us of an SM (e4m3 2.6; heads of 64 0.7 of that, one tile of
-// rows half), and 15 us are start and end; the other pass's CTAs take 4 us and
-// their keys (half of what may be) at 45 GB/s per SM; what it has not done when
-// the first is over it does on all SMs.  Several prefixes count as 0.6 of their
-// bound each, and the first pass keeps at least 10 sixteenths.  Measured, 64 sequences of 100 to 2000
-// keys behind 32768, 32 and 8 heads of 128: 118 us on all SMs one after the
-// other, 99 with 120, 91 with 90, 92 with 76, 100 with 60.
+// 128 keys is 1.9 us of an SM (e4m3 3.4; 128 rows of a wide differential map 1.2;
+// heads of 64 0.7 of that, one tile of rows half), and 15 us are start and end;
+// the other pass's CTAs take 4 us and their keys (half of what may be) at 45 GB/s
+// per SM; what it has not done when the first is over it does on all SMs.
+// Several prefixes count as 0.6 of their bound each, and the first pass keeps at
+// least 9 sixteenths.  Measured, 64 sequences of 100 to 2000 keys behind 32768, 32
+// and 8 heads of 128: 118 us on all SMs one after the other, 99 with 120, 91
+// with 90, 92 with 76, 100 with 60; 16 behind 8192, 28 and 4 heads: 27.5 on all,
+// 20.9 with 104, 19.6 with 88, 20.4 with 64.
 int prefix_ctas(const santa::JoinArgs& p, const santa::JoinArgs& own) {
   const double tiles = std::min((double)p.B * p.tiles, (double)p.total_q / p.tokens + 0.5 * p.B);
   const double blocks = tiles * p.heads * p.max_prefix / santa::BKEYS * (p.B > 1 ? 0.6 : 1.0);
   const bool one = !p.diff && p.max_q <= p.tokens / 2;
-  const double first = blocks * (p.e4m3 ? 2.6 : 1.9) * (p.D == 64 ? 0.7 : 1.0) * (one ? 0.5 : 1.0);
+  const double first = blocks * (p.e4m3 ? 3.4 : p.wide ? 1.2 : 1.9) * (p.D == 64 ? 0.7 : 1.0) * (one ? 0.5 : 1.0);
   constexpr int per_sm = 2;   // CTAs of the other pass
   const double ctas = (double)own.B * own.tiles * own.heads * own.splits, row = p.e4m3 ? p.D + 4.0 : 2.0 * p.D;
   const double each = 4 + 0.5 * own.max_own / own.splits * 2 * row * (p.diff ? 2 : 1) * per_sm / 45e3;
   const int items = (int)std::min<int64_t>((int64_t)p.tiles * p.heads, p.num_sms);
   int best = p.splits;
   double least = 1e30;
-  for (int sixteenths = 16; sixteenths >= 10; --sixteenths) {
+  for (int sixteenths = 9; sixteenths <= 16; ++sixteenths) {   // more only where it gives more
     int x = std::min(p.splits, p.num_sms * sixteenths / 16);
     if (p.B == 1 && items < x) x = std::min(p.splits, (x + items - 1) / items * items);   // as many for each item
     const int rest = p.num_sms - x;
     const double t1 = 15 + first / x, t2 = rest ? each * std::max(1.0, ctas / (rest * per_sm)) : 1e9;
     const double all = each * std::max(1.0, ctas / (p.num_sms * per_sm));
-    const double t = t2 <= t1 ? t1 : t1 + std::max(each, all * (rest ? 1 - t1 / t2 : 1));
-    if (t < least) {
+    const double t = t2 <= t1 ? t1 : std::min(t2, t1 + std::max(each, all * (rest ? 1 - t1 / t2 : 1)));
+    if (t < 0.97 * least) {
       least = t;
       best = x;
     }
@@ -243,7 +246,7 @@ void lay_out(santa::JoinArgs& a, unsigned char* ws, size_t& at) {
     return p;
   };
   if (a.chunk) {
-    const size_t rows = (size_t)a.splits * 2 * a.rows, cols = wide * santa::x_items(a) / a.heads;
+    const size_t rows = (size_t)a.splits * 2 * a.rows, cols = a.wide ? wide : wide * santa::x_items(a) / a.heads;
     a.part_o = reinterpret_cast<float*>(take(rows * cols * sizeof(float)));
     a.part_ml = reinterpret_cast<float*>(take(rows * 2 * sizeof(float)));
     a.row_o = reinterpret_cast<float*>(take(all * wide * sizeof(float)));
@@ -330,7 +333,8 @@ santa_status_t join(const santa_paged_t* p, const santa_prefix_t* x, const santa
   const bool both = x && !l.prefix.chunk && !l.own.chunk;   // in one launch
   auto launch = [&](const santa::JoinArgs& a, bool behind) {
     const santa::JoinArgs* const first = both ? &l.prefix : nullptr;
-    if (a.diff) return a.chunk ? santa::launch_diff_chunk(a, behind) : santa::launch_diff_tokens(first, a, behind);
+    if (a.diff && a.chunk) return a.wide ? santa::launch_diff_wide(a, behind) : santa::launch_diff_chunk(a, behind);
+    if (a.diff) return santa::launch_diff_tokens(first, a, behind);
     return a.chunk ? santa::launch_join_chunk(a, behind) : santa::launch_join_tokens(first, a, behind);
   };
   cudaError_t e = x && !both ? launch(l.prefix, false) : cudaSuccess;
