@@ -34,7 +34,7 @@ struct JoinArgs : PagedArgs {
   const int32_t* prefix_lens;
   int max_prefix, max_own;
   float* row_o;                    // chunks: sums of items that one CTA has whole, [total_q, H, width]
-  float* row_ml;                   // [total_q, H, 2 or (differential, halves) 2 x 2]
+  float* row_ml;                   // [total_q, H, 2]; 2 x 2, one for each value head, in a differential e4m3 pass of chunks
   PieceNote* notes;                // chunks: [total_q, heads], at an item's first token
   int sources;                     // pieces of a row, about
   // differential heads: the weights of the second maps, the norm behind them
