@@ -56,7 +56,7 @@ __device__ __forceinline__ Place locate(const JoinArgs& a, int vb, const Seq& s,
     return l;
   }
   const unsigned per = CHUNK_ROWS / (unsigned)a.G, tile = (unsigned)i / (unsigned)a.tokens, in = i - tile * a.tokens, sub = DIFF ? 0 : in / per;
-  const int part = a.heads == x_items(a) || a.wide ? 0 : lane >> 4;   // columns of the second value head
+  const int part = a.heads == x_items(a) || a.one_map ? 0 : lane >> 4;   // columns of the second value head
   l.at = ((unsigned)s.q0 + tile * a.tokens) * a.heads + (a.heads == x_items(a) ? x : 2 * x + part);
   l.count = (int)(sub * CHUNK_ROWS + (in - sub * per) * a.G) + g0;
   return l;
@@ -86,7 +86,7 @@ __device__ __forceinline__ Sums sums(const JoinArgs& a, const Place& l, const Pi
     f.step = a.rows * (DIFF ? 2 : 1);
     f.map = a.rows;
   } else {
-    const bool whole = n.count == 0, halves = DIFF && a.heads != x_items(a) && !a.wide;
+    const bool whole = n.count == 0, halves = DIFF && a.heads != x_items(a) && !a.one_map;
     const int dv = halves ? D : W;
     f.o = whole ? a.row_o + column : a.part_o + (halves && column >= D ? column - D : column);
     f.ml = whole ? a.row_ml + (halves && column >= D ? 2 : 0) : a.part_ml;
@@ -97,7 +97,7 @@ __device__ __forceinline__ Sums sums(const JoinArgs& a, const Place& l, const Pi
     f.next = 0u - (unsigned)(n.slot * a.rows);
     f.step = 2 * a.rows;
     f.rise = whole && DIFF ? 2 : 1;
-    f.map = whole ? 1 : a.wide ? 0 : CHUNK_ROWS;   // wide: each map has pieces of its own
+    f.map = whole ? 1 : a.one_map ? 0 : CHUNK_ROWS;   // one_map: each map has pieces of its own
   }
   if (!there) f.count = 0;
   return f;
@@ -162,14 +162,14 @@ __global__ void __launch_bounds__(join_threads<WARPS>(), WARPS == 16 ? 1 : WARPS
   // the notes of the next set are on their way while this one's sums are read
   constexpr int NE = DIFF && D == 128 ? 2 : 1;
   PieceNote own_note[NE] = {}, pre_note[NE] = {};
-  auto notes = [&] {   // wide: one for each map
+  auto notes = [&] {   // one_map: one for each map
     if (a.chunk && s.ok) {
       own_note[0] = a.notes[own.at];
-      if (NE == 2 && a.wide) own_note[NE - 1] = a.notes[own.at + 1];
+      if (NE == 2 && a.one_map) own_note[NE - 1] = a.notes[own.at + 1];
     }
     if (p.chunk && prefix) {
       pre_note[0] = p.notes[pre.at];
-      if (NE == 2 && p.wide) pre_note[NE - 1] = p.notes[pre.at + 1];
+      if (NE == 2 && p.one_map) pre_note[NE - 1] = p.notes[pre.at + 1];
     }
   };
   if (first < set_end) look(first);
@@ -185,8 +185,8 @@ __global__ void __launch_bounds__(join_threads<WARPS>(), WARPS == 16 ? 1 : WARPS
     if constexpr (NE == 2) {
       f0[1] = f0[0];
       f1[1] = f1[0];
-      if (p.wide) f0[1] = sums<D, DIFF>(p, pre, pre_note[1], column, row_at, prefix);
-      if (a.wide) f1[1] = sums<D, DIFF>(a, own, own_note[1], column, row_at, s.ok);
+      if (p.one_map) f0[1] = sums<D, DIFF>(p, pre, pre_note[1], column, row_at, prefix);
+      if (a.one_map) f1[1] = sums<D, DIFF>(a, own, own_note[1], column, row_at, s.ok);
     }
     const int next = set + (WARPS == 1 ? 4 : 1);
     float m[ROWS], l[ROWS], o[ROWS][E];

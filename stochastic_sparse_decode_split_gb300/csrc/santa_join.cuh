@@ -38,7 +38,7 @@ struct JoinArgs : PagedArgs {
   PieceNote* notes;                // chunks: [total_q, heads], at an item's first token
   int sources;                     // pieces of a row, about
   // differential heads: the weights of the second maps, the norm behind them
-  int diff, wide;                  // wide: an item is a map, over the columns of both value heads
+  int diff, one_map;               // one_map: an item is a map, over the columns of both value heads (santa_diff_wide.cu)
   const float* lambda;
   long long lambda_stride;         // from token to token (0: the same for all)
   const void* norm;                // [2 D] or null

@@ -130,28 +130,35 @@ Plan plan(santa::PagedArgs& a) {
 }
 
 // Differential heads: the kernel for few rows takes eight rows of both maps at a
-// time, and has the calls whose tiles meet at most 9216 blocks of 16 keys.
-// Measured, few rows against chunks, 32 and 8 heads of 128: at 4096 blocks (one
-// sequence of 2048 keys, 16 tokens) 20.6 against 26.7 us, of 8192 keys and 4
-// tokens 22.6 against 26.9; at 8192 blocks (8192 keys, 8 tokens) 28.8 against
-// 28.8, e4m3 28.8 against 32.9; at 16384 (16 tokens) 51.3 against 34.8, e4m3 43.1
-// against 37.0; 16 and 2 heads of 64, 16384 blocks (32768 keys, 8 tokens) 26.7
-// against 24.7, e4m3 34.9 against 29.9.
-bool few_diff(const santa::PagedArgs& a, int64_t span, int64_t blocks) {
-  const int64_t rows = (int64_t)a.max_q * a.G;
-  return rows <= 8 || (rows + 7) / 8 <= blocks * 16 / span / ((int64_t)a.B * (a.Hkv / 2));
-}
-// The borders of a pass over prefixes, whose chunks run beside the other pass.
-// Measured, few rows against chunks, one group, 1 to 300 keys of their own: 28
-// and 4 heads of 128 over 16 bits, 8192 blocks (8 sequences, 8192 keys) 22.3
-// against 22.2 us, 14336 (16 sequences) 25.1 against 24.4, 28672 (32) 35.2
-// against 30.5; 32 and 8 heads, e4m3, 16384 (16, 8192 keys) 31.5 against 33.0, 32768
-// 55.7 against 34.5.  Differential, 32 and 8 heads, 4096 blocks 26.5 against 29.9
-// and 25.6 against 26.2, 8192 33.0 against 27.5; e4m3 28.2 against 34.5, 35.6
-// against 33.7.
+// time.  It has the calls of at most two such tiles per sequence (its cache is
+// then read at most twice, mostly from the L2), and those whose tiles meet at most
+// 9216 blocks of 16 keys.  Measured, few rows against chunks, 32 and 8 heads of
+// 128: two tiles (4 tokens) at 8192 keys 19.8 against 25.0 us, e4m3 22.1 against
+// 28.2, at 32768 keys 38.7 against 48.1, e4m3 42.9 against 63.2; 4096 blocks (2048
+// keys, 16 tokens) 18.1 against 24.5, e4m3 20.3 against 25.0; 8192 (8192 keys, 8
+// tokens) 25.0 against 25.6, e4m3 27.8 against 28.6; 16384 (16 tokens) 38.4
+// against 31.2, e4m3 41.9 against 33.7; 16 and 2 heads of 64, 16384 blocks (32768
+// keys, 8 tokens) 23.7 against 21.4.
+//
+// A pass over prefixes, whose chunks run beside the other pass, has borders of
+// its own.  Measured, few rows against chunks, one group, 1 to 300 keys of their
+// own: 28 and 4 heads of 128 over 16 bits, 8192 blocks (8 sequences, 8192 keys)
+// 22.3 against 22.2 us, 14336 (16 sequences) 25.1 against 24.4, 28672 (32) 35.2
+// against 30.5; 32 and 8 heads, e4m3, 16384 (16, 8192 keys) 31.5 against 33.0,
+// 32768 55.7 against 34.5.  Differential, 32 and 8 heads of 128, 16 bits, 1024
+// blocks (4 sequences, 2048 keys) 17.0 against 17.6, 2048 (4 and 4096) 19.7 against
+// 18.9, (8 and 2048) 20.3 against 17.9, 4096 (8 and 4096) 23.7 against 19.3; e4m3,
+// 4096 (16 and 2048) 27.0 against 28.1, 8192 (16 and 4096) 33.7 against 32.4, two
+// tiles (4 and 32768) 45.5 against 63.1; 16 and 2 heads of 64, 4096 (16 and 4096)
+// 18.3 against 18.8, 8192 (16 and 8192) 21.3 against 19.9, two tiles (2 and 32768)
+// 17.2 against 19.4.
 int64_t border(const santa::JoinArgs& a) {
-  if (a.phase == 1) return a.diff ? 5120 : a.e4m3 ? 20480 : 12288;
+  if (a.phase == 1) return !a.diff ? (a.e4m3 ? 20480 : 12288) : a.e4m3 || a.D == 64 ? 5120 : 1920;
   return a.diff ? 9216 : 3 * 8192;
+}
+bool few_diff(const santa::JoinArgs& a, int64_t span) {
+  const int64_t rows = (int64_t)a.max_q * a.G, any = a.phase == 1 && !a.e4m3 && a.D == 128 ? 8 : 16;
+  return rows <= any || (rows + 7) / 8 <= border(a) * 16 / span / ((int64_t)a.B * (a.Hkv / 2));
 }
 
 // ---- attention in passes: a shared prefix, differential heads
@@ -171,7 +178,7 @@ santa_status_t check_join(const santa_paged_t* p, const santa_prefix_t* x, bool 
 // A pass's kernel and the sizes of its sums; `span` keys, that may begin inside a block.
 void plan_pass(santa::JoinArgs& a, int64_t span, bool inside) {
   if (a.diff) {
-    a.chunk = !few_diff(a, span, border(a));
+    a.chunk = !few_diff(a, span);
     if (a.chunk) a.tokens = santa::CHUNK_ROWS / a.G;
     else santa::plan_diff_tokens(a, (int)span, inside);
   } else {
@@ -181,9 +188,9 @@ void plan_pass(santa::JoinArgs& a, int64_t span, bool inside) {
   }
   a.heads = santa::x_items(a);
   if (a.chunk) {
-    a.wide = a.diff && !a.e4m3 && a.D == 128;
-    if (a.diff && (a.e4m3 || a.D == 128)) a.heads *= 2;   // an item for each value head, or (wide) for each map
-    a.rows = (a.wide ? 1 : 2) * santa::CHUNK_ROWS;
+    a.one_map = a.diff && !a.e4m3 && a.D == 128;
+    if (a.diff && (a.e4m3 || a.D == 128)) a.heads *= 2;   // an item for each value head, or (one_map) for each map
+    a.rows = (a.one_map ? 1 : 2) * santa::CHUNK_ROWS;
     a.tiles = (a.max_q + a.tokens - 1) / a.tokens;
     const int64_t items = (int64_t)a.B * a.heads * a.tiles, blocks = (span + santa::BKEYS - 1) / santa::BKEYS + inside;
     a.splits = (int)std::min<int64_t>(a.num_sms, items * blocks);
@@ -197,7 +204,7 @@ void plan_pass(santa::JoinArgs& a, int64_t span, bool inside) {
 // few rows: that one, which HBM bounds, then runs on the other SMs from the
 // start on, under the start, the products and the stores of the first.  The
 // division is the best of a few by an estimate of both: a block of 256 rows and
-// 128 keys is 1.9 us of an SM (e4m3 3.4; 128 rows of a wide differential map 1.2;
+// 128 keys is 1.9 us of an SM (e4m3 3.4; 128 rows of a differential map with both value heads 1.2;
 // heads of 64 0.7 of that, one tile of rows half), and 15 us are start and end;
 // the other pass's CTAs take 4 us and their keys (half of what may be) at 45 GB/s
 // per SM; what it has not done when the first is over it does on all SMs.
@@ -210,7 +217,7 @@ int prefix_ctas(const santa::JoinArgs& p, const santa::JoinArgs& own) {
   const double tiles = std::min((double)p.B * p.tiles, (double)p.total_q / p.tokens + 0.5 * p.B);
   const double blocks = tiles * p.heads * p.max_prefix / santa::BKEYS * (p.B > 1 ? 0.6 : 1.0);
   const bool one = !p.diff && p.max_q <= p.tokens / 2;
-  const double first = blocks * (p.e4m3 ? 3.4 : p.wide ? 1.2 : 1.9) * (p.D == 64 ? 0.7 : 1.0) * (one ? 0.5 : 1.0);
+  const double first = blocks * (p.e4m3 ? 3.4 : p.one_map ? 1.2 : 1.9) * (p.D == 64 ? 0.7 : 1.0) * (one ? 0.5 : 1.0);
   constexpr int per_sm = 2;   // CTAs of the other pass
   const double ctas = (double)own.B * own.tiles * own.heads * own.splits, row = p.e4m3 ? p.D + 4.0 : 2.0 * p.D;
   const double each = 4 + 0.5 * own.max_own / own.splits * 2 * row * (p.diff ? 2 : 1) * per_sm / 45e3;
@@ -246,7 +253,7 @@ void lay_out(santa::JoinArgs& a, unsigned char* ws, size_t& at) {
     return p;
   };
   if (a.chunk) {
-    const size_t rows = (size_t)a.splits * 2 * a.rows, cols = a.wide ? wide : wide * santa::x_items(a) / a.heads;
+    const size_t rows = (size_t)a.splits * 2 * a.rows, cols = a.one_map ? wide : wide * santa::x_items(a) / a.heads;
     a.part_o = reinterpret_cast<float*>(take(rows * cols * sizeof(float)));
     a.part_ml = reinterpret_cast<float*>(take(rows * 2 * sizeof(float)));
     a.row_o = reinterpret_cast<float*>(take(all * wide * sizeof(float)));
@@ -333,7 +340,7 @@ santa_status_t join(const santa_paged_t* p, const santa_prefix_t* x, const santa
   const bool both = x && !l.prefix.chunk && !l.own.chunk;   // in one launch
   auto launch = [&](const santa::JoinArgs& a, bool behind) {
     const santa::JoinArgs* const first = both ? &l.prefix : nullptr;
-    if (a.diff && a.chunk) return a.wide ? santa::launch_diff_wide(a, behind) : santa::launch_diff_chunk(a, behind);
+    if (a.diff && a.chunk) return a.one_map ? santa::launch_diff_wide(a, behind) : santa::launch_diff_chunk(a, behind);
     if (a.diff) return santa::launch_diff_tokens(first, a, behind);
     return a.chunk ? santa::launch_join_chunk(a, behind) : santa::launch_join_tokens(first, a, behind);
   };

@@ -206,3 +206,76 @@ def test_output_over_the_queries_and_other_streams():
         graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(captured, want) and step.error() == 0
+
+
+def ramped(batch, every, factors):
+    """The batch with the keys of every `every` positions of a sequence times the next of `factors` (powers of two)."""
+    for b in range(batch.B):
+        for i in range(batch.kv[b]):
+            page, at, f = int(batch.table[b, i // batch.page]), i % batch.page, factors[i // every % len(factors)]
+            if batch.e4m3:
+                batch.ks[page, :, at] *= f
+            else:
+                batch.K[page, at] *= f
+    return batch
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("kv,n", [([1400, 130], [1, 2]), ([1400, 700], [140, 300])])
+@pytest.mark.parametrize("factors", [(0.25, 1, 2, 4, 8, 16), (16, 8, 1, 0.25), (0.5, 16, 0.25, 32, 1, 8)])
+def test_maxima_that_grow_and_fall_along_the_keys(factors, kv, n, D, e4m3):
+    """What a block's maximum is above the one before, a group's above the other's: nothing, a little, more than 2^8."""
+    run(ramped(Batch(kv, n, 8, 2, D, BF16, e4m3, 32, seed=D), 97, factors), norm=False)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n", [1, 150])
+def test_a_bad_page_zeroes_the_rows_that_are_computed_with_it(n, D, e4m3):
+    batch = Batch([700, 600], [n, n], 8, 2, D, FP16, e4m3, 32, seed=5)
+    step, w, _ = run(batch, norm=False)
+    want, want_lse = (x.clone() for x in step.attend_diff(batch.q, w, return_lse=True))
+    batch.table[0, 1] = -1
+    out, lse = step.attend_diff(batch.q, w, return_lse=True)
+    assert step.error() == santa.CACHE_DEVERR_PAGE
+    assert bool((out[:n] == 0).all()) and bool((lse[:n] == float("-inf")).all())
+    assert torch.equal(out[n:], want[n:]) and torch.equal(lse[n:], want_lse[n:])
+
+
+@pytest.mark.parametrize("n", [[1, 0, 2], [150, 0, 90]])
+def test_padding_is_left_as_it_was(n):
+    batch = Batch([200, 300, 150], n, 8, 2, 128, BF16, False, 16, seed=4, pad=9)
+    w, _ = learned(batch, per_token=True)
+    step = batch.step(diff=True)
+    out = torch.full((batch.total_q, 4, 256), 7.0, dtype=BF16, device="cuda")
+    lse = torch.full((batch.total_q, 8), 7.0, device="cuda")
+    step.attend_diff(batch.q, w, out=out, lse=lse)
+    assert step.error() == 0
+    check_diff(batch, out, lse, w)
+    assert bool((out[batch.tokens:] == 7).all()) and bool((lse[batch.tokens:] == 7).all())
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_captured_over_a_prefix_and_replayed_with_other_lengths(D):
+    """One graph for every length within the bounds; the same bits from one replay to the next."""
+    batch = Shared([4000], [0, 40], [1 + 9 * i % 90 for i in range(40)], [1] * 40, 16, 4, D, BF16, False, 32, seed=7, whole=True, pairs=True)
+    w, _ = learned(batch)
+    step = batch.shared_step(diff=True, max_own=100)
+    step.attend_diff(batch.q, w)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out, lse = step.attend_diff(batch.q, w, return_lse=True)
+    longest = batch.kv
+    for prefix in (4000, 3001, 128, 1, 0, 2500):
+        batch.prefix[0] = prefix
+        batch.kv = [min(k, prefix + 1 + 7 * b % 90) for b, k in enumerate(longest)]
+        batch.prefix_t.fill_(prefix)
+        batch.kv_t.copy_(torch.tensor(batch.kv, dtype=torch.int32))
+        graph.replay()
+        assert step.error() == 0
+        check_diff(batch, out, lse, w)
+        first, first_lse = out.clone(), lse.clone()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(first, out) and torch.equal(first_lse, lse)

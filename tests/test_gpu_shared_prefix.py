@@ -196,3 +196,18 @@ def test_the_prefix_of_a_group_is_read_through_its_first_sequence_after_an_appen
         assert float((out.float() - want.float()).abs().max()) <= 4 * 2.0 ** -8 * float(cache.V.float().abs().max())
         assert float((lse - want_lse).abs().max()) <= 1e-4
     assert shared.error() == 0 and alone.error() == 0
+
+
+@pytest.mark.parametrize("own", [[5, 60, 1], [300, 400, 260]])
+def test_output_over_the_queries_and_another_stream(own):
+    batch = Shared([4000], [0, 3], own, [min(k, 250) if own[0] > 5 else 1 for k in own], 8, 2, 128, BF16, False, 16, seed=2)
+    step = batch.shared_step()
+    want = step.attend(batch.q).clone()
+    q = batch.q.clone()
+    got = step.attend(q, out=q)
+    assert torch.equal(got, want) and got.data_ptr() == q.data_ptr()
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    other = step.attend(batch.q, stream=stream)
+    stream.synchronize()
+    assert torch.equal(other, want) and step.error() == 0
