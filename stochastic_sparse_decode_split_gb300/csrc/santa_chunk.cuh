@@ -40,7 +40,7 @@
 // Measured: 2048 tokens at 32768 keys, 32 and 8 heads of 128, bf16: 745 to 774
 // us, 1.37 to 1.43 PFLOP/s (0.72 to 0.75 of a library product's rate; the clock
 // falls from 1.86 to 1.74 GHz as the tensor cores fill); six chunks of up to 700
-// tokens over e4m3 in a window of 4096: 185 us, where for a tile softmax, issue
+// tokens over e4m3 in a window of 4096: 181 us, where for a tile softmax, issue
 // of the products and hand-overs follow one another, the other tile in between
 // (K left in e4m3, for products of that kind with q as a sum of two or three
 // such values, took as long).
@@ -298,6 +298,13 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
   // of 4096 202.7 -> 187.2.  All 128 at once where a CTA has many blocks of a
   // 16-bit cache: 2048 tokens at 32768 keys 779 against 796 us.
   constexpr bool SHORT = E4M3 || JOIN;
+  // Over e4m3 a block of K is loaded and widened before the V of the block before
+  // it, whose place is free only behind the product of the V two earlier, when
+  // that K's scores are due half a block later: 96 tokens behind three prefixes of
+  // up to 20001 keys 123.7 -> 109.4 us, six chunks in a window of 4096 184.9 ->
+  // 180.5.  Not over 16 bits, where K needs no widening (757 against 764 us, 2048 tokens
+  // at 32768 keys), nor where tiles have K of their own, whose places are freed later.
+  constexpr bool AHEAD = E4M3 && !DIFF;
   using Gm = ChunkGeom<E4M3, D, DV, DIFF>;
   using M16 = typename std::conditional<E4M3, fp16_t, T>::type;
   constexpr float BIAS = fp16_bias<M16>(CHUNK_BIAS);
@@ -472,7 +479,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         auto row_of = [&](int pid, int j) {   // first row of a lane's box
           return (pid << a.page_shift) + (((p.blk0 + j) * BKEYS + lane * rows) & ((1 << a.page_shift) - 1));
         };
-        int pid = page_of(0), pid1 = page_of(1);
+        int pid = page_of(0), pid1 = page_of(1), pid2 = AHEAD ? page_of(2) : INT32_MIN;
         for (int j = 0; j < p.nblk; ++j, ++n) {
           const int st = n & 1;
           const bool ok = pid != INT32_MIN && (unsigned)pid < (unsigned)a.n_pages;
@@ -483,23 +490,29 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
           const unsigned boxes_ok = (unsigned)__popc(__ballot_sync(FULL, ok)) * (unsigned)rows;
           const int row = ok ? row_of(pid, j) : 0;
           const uint32_t vd = base + Gm::OFF_V + st * Gm::VTILE;
+          auto load_k = [&](int page, int i, unsigned at) {   // block i of the piece, block `at` of all
+            const bool there = page != INT32_MIN && (unsigned)page < (unsigned)a.n_pages;
+            const unsigned bytes = (unsigned)__popc(__ballot_sync(FULL, there)) * (unsigned)(rows * ROWB);
+            const int first = there ? row_of(page, i) : 0;
 #pragma unroll
-          for (int t = 0; t < (DIFF ? 2 : 1); ++t) {
-            const int ks = DIFF ? t : st;
-            if (n > (DIFF ? 0 : 1)) wait_phase(bar(K_EMPTY + ks), ((DIFF ? n : n >> 1) - 1) & 1, a.err, dead);
-            const uint32_t kd = base + Gm::OFF_K + ks * Gm::TILE;
-            if (lane == 0) mbar_expect_tx(bar(K_FULL + ks), boxes_ok * ROWB);
-            __syncwarp();
-            if (ok) {
-              if (E4M3) {
-                tma_load(kd + Gm::TILE / 2 + lane * rows * D, &tmK, 0, k_head + t, row, bar(K_FULL + ks));
-              } else {
+            for (int t = 0; t < (DIFF ? 2 : 1); ++t) {
+              const int ks = DIFF ? t : (int)(at & 1);
+              if (at > (DIFF ? 0 : 1)) wait_phase(bar(K_EMPTY + ks), ((DIFF ? at : at >> 1) - 1) & 1, a.err, dead);
+              const uint32_t kd = base + Gm::OFF_K + ks * Gm::TILE;
+              if (lane == 0) mbar_expect_tx(bar(K_FULL + ks), bytes);
+              __syncwarp();
+              if (there) {
+                if (E4M3) {
+                  tma_load(kd + Gm::TILE / 2 + lane * rows * D, &tmK, 0, k_head + t, first, bar(K_FULL + ks));
+                } else {
 #pragma unroll
-                for (int h = 0; h < D / 64; ++h)
-                  tma_load(kd + h * Gm::HALF + lane * rows * 128, &tmK, 64 * h, k_head + t, row, bar(K_FULL + ks));
+                  for (int h = 0; h < D / 64; ++h)
+                    tma_load(kd + h * Gm::HALF + lane * rows * 128, &tmK, 64 * h, k_head + t, first, bar(K_FULL + ks));
+                }
               }
             }
-          }
+          };
+          if (j == 0 || !AHEAD) load_k(pid, j, n);
           if (j == 0) {
             // Q, once the previous piece's products are over; the last
             // token's box may reach past q, where it reads zeros
@@ -517,6 +530,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
             }
             __syncwarp();
           }
+          if (AHEAD && j + 1 < p.nblk) load_k(pid1, j + 1, n + 1);
           // No piece's sums are complete (its V is not there) before every softmax
           // warp has seen that the previous one's were: see PIECE_SEEN below.
           if (j == 0 && np > 0) wait_phase(bar(PIECE_SEEN), (np - 1) & 1, a.err, dead);
@@ -533,7 +547,8 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
             }
           }
           pid = pid1;   // looked up two blocks ahead
-          pid1 = page_of(j + 2);
+          pid1 = AHEAD ? pid2 : page_of(j + 2);
+          if (AHEAD) pid2 = page_of(j + 3);
         }
         ++np;
       }
@@ -594,19 +609,21 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         const int pair = p.kvh / PARTS, k_head = DIFF ? 2 * pair : p.kvh, v_head = DIFF ? 2 * pair + (PARTS == 2 ? p.kvh % 2 : 0) : p.kvh;
         constexpr int STEPS = DIFF ? 3 : 2;           // the blocks of K, then V's
         for (int i = 0; i < STEPS * p.nblk; ++i) {
-          const int which = i % STEPS;
-          const bool is_v = which == STEPS - 1;
-          const int st = n & 1, key0 = (p.blk0 + i / STEPS) * BKEYS, live = min(BKEYS, p.s.kv - key0);
+          // in the order in which they are loaded
+          const bool is_v = AHEAD ? (i > 0 && i % 2 == 0) || i + 1 == STEPS * p.nblk : i % STEPS == STEPS - 1;
+          const int which = AHEAD ? is_v : i % STEPS, j = AHEAD ? (is_v ? i - 1 : i + 1) / 2 : i / STEPS;
+          const unsigned at = n + j;
+          const int st = at & 1, key0 = (p.blk0 + j) * BKEYS, live = min(BKEYS, p.s.kv - key0);
           if (which == 0) {   // this thread's key's scales, on their way while the codes arrive
             const int key = key0 + ct;
             float ksc = 0.f, ksc1 = 0.f, vsc = 1.f;
             if (ct < live) {
               const int pid = table[key >> a.page_shift];
               if ((unsigned)pid < (unsigned)a.n_pages) {
-                auto at = [&](int head) { return ((((long long)pid * a.Hkv) + head) << a.page_shift) + (key & ((1 << a.page_shift) - 1)); };
-                ksc = __ldg(a.ks + at(k_head));
-                if (DIFF) ksc1 = __ldg(a.ks + at(k_head + 1));
-                vsc = __ldg(a.vs + at(v_head));
+                auto scale_at = [&](int head) { return ((((long long)pid * a.Hkv) + head) << a.page_shift) + (key & ((1 << a.page_shift) - 1)); };
+                ksc = __ldg(a.ks + scale_at(k_head));
+                if (DIFF) ksc1 = __ldg(a.ks + scale_at(k_head + 1));
+                vsc = __ldg(a.vs + scale_at(v_head));
               }
             }
             if (odd_scale(vsc)) {   // the values are NaN, the softmax is not: given back at the end
@@ -617,7 +634,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
             float lv, rv;
             asm("lg2.approx.f32 %0, %1;" : "=f"(lv) : "f"(vsc));
             asm("rcp.approx.f32 %0, %1;" : "=f"(rv) : "f"(vsc));
-            const uint32_t sc = base + Gm::OFF_SC + (n & 3) * Gm::SC_STAGE + ct * 4;
+            const uint32_t sc = base + Gm::OFF_SC + (at & 3) * Gm::SC_STAGE + ct * 4;
             asm volatile("st.shared.f32 [%0], %1;" ::"r"(sc), "f"(ksc) : "memory");
             asm volatile("st.shared.f32 [%0], %1;" ::"r"(sc + BKEYS * 4), "f"(lv) : "memory");
             asm volatile("st.shared.f32 [%0], %1;" ::"r"(sc + 2 * BKEYS * 4), "f"(rv) : "memory");
@@ -625,7 +642,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
           }
           const int stage = DIFF && !is_v ? which : st;
           const uint32_t dst = base + (is_v ? Gm::OFF_V : Gm::OFF_K) + stage * Gm::TILE, src = dst + Gm::TILE / 2;   // DV == D
-          wait_phase(bar((is_v ? V_FULL : K_FULL) + stage), (DIFF && !is_v ? n : n >> 1) & 1, a.err, dead);
+          wait_phase(bar((is_v ? V_FULL : K_FULL) + stage), (DIFF && !is_v ? at : at >> 1) & 1, a.err, dead);
           const int c = ct % CPR, r0 = ct / CPR;      // this thread's chunk of rows r0, r0 + 128 / CPR, ...
           // chunks 2c and 2c + 1 of a row's 16-bit elements; rows of a thread are 0 modulo 8 apart
           const uint32_t row = dst + (uint32_t)((c >> 2) * Gm::HALF + r0 * 128);
@@ -666,9 +683,9 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(bar((is_v ? V_READY : K_READY) + stage));
-          n += is_v;
         }
         ++np;
+        n += p.nblk;
       }
     }
   } else {

@@ -204,20 +204,22 @@ void plan_pass(santa::JoinArgs& a, int64_t span, bool inside) {
 // few rows: that one, which HBM bounds, then runs on the other SMs from the
 // start on, under the start, the products and the stores of the first.  The
 // division is the best of a few by an estimate of both: a block of 256 rows and
-// 128 keys is 1.9 us of an SM (e4m3 3.4; 128 rows of a differential map with both value heads 1.2;
-// heads of 64 0.7 of that, one tile of rows half), and 15 us are start and end;
-// the other pass's CTAs take 4 us and their keys (half of what may be) at 45 GB/s
-// per SM; what it has not done when the first is over it does on all SMs.
-// Several prefixes count as 0.6 of their bound each, and the first pass keeps at
-// least 9 sixteenths.  Measured, 64 sequences of 100 to 2000 keys behind 32768, 32
-// and 8 heads of 128: 118 us on all SMs one after the other, 99 with 120, 91
-// with 90, 92 with 76, 100 with 60; 16 behind 8192, 28 and 4 heads: 27.5 on all,
-// 20.9 with 104, 19.6 with 88, 20.4 with 64.
+// 128 keys is 1.9 us of an SM (e4m3 3.4, differential 2.5; 128 rows of a
+// differential map with both value heads 1.2; heads of 64 0.7 of that, one tile of
+// rows half, e4m3 three quarters), and 15 us are start and end; the other pass's
+// CTAs take 4 us and their keys (half of what may be) at 45 GB/s per SM; what it
+// has not done when the first is over it does on all SMs.  Several prefixes count
+// as 0.75 of their bound each, and the first pass keeps at least 9 sixteenths.
+// Measured, 64 sequences of 100 to 2000 keys behind 32768, 32 and 8 heads of 128:
+// 118 us on all SMs one after the other, 99 with 120, 91 with 90, 92 with 76, 100
+// with 60; e4m3 108 on all, 98 with 112, 86 with 96, 92 with 80; 16 behind 8192, 28
+// and 4 heads: 27.5 on all, 20.9 with 104, 19.6 with 88, 20.4 with 64; differential,
+// 32 behind 16384, e4m3: 64 on all, 52 with 112 or 104, 57 with 88.
 int prefix_ctas(const santa::JoinArgs& p, const santa::JoinArgs& own) {
   const double tiles = std::min((double)p.B * p.tiles, (double)p.total_q / p.tokens + 0.5 * p.B);
-  const double blocks = tiles * p.heads * p.max_prefix / santa::BKEYS * (p.B > 1 ? 0.6 : 1.0);
+  const double blocks = tiles * p.heads * p.max_prefix / santa::BKEYS * (p.B > 1 ? 0.75 : 1.0);
   const bool one = !p.diff && p.max_q <= p.tokens / 2;
-  const double first = blocks * (p.e4m3 ? 3.4 : p.one_map ? 1.2 : 1.9) * (p.D == 64 ? 0.7 : 1.0) * (one ? 0.5 : 1.0);
+  const double first = blocks * (p.e4m3 ? (p.diff ? 2.5 : 3.4) : p.one_map ? 1.2 : 1.9) * (p.D == 64 ? 0.7 : 1.0) * (!one ? 1.0 : p.e4m3 ? 0.75 : 0.5);
   constexpr int per_sm = 2;   // CTAs of the other pass
   const double ctas = (double)own.B * own.tiles * own.heads * own.splits, row = p.e4m3 ? p.D + 4.0 : 2.0 * p.D;
   const double each = 4 + 0.5 * own.max_own / own.splits * 2 * row * (p.diff ? 2 : 1) * per_sm / 45e3;
