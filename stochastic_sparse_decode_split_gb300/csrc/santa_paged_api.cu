@@ -144,16 +144,16 @@ Plan plan(santa::PagedArgs& a) {
 // its own.  Measured, few rows against chunks, one group, 1 to 300 keys of their
 // own: 28 and 4 heads of 128 over 16 bits, 8192 blocks (8 sequences, 8192 keys)
 // 22.3 against 22.2 us, 14336 (16 sequences) 25.1 against 24.4, 28672 (32) 35.2
-// against 30.5; 32 and 8 heads, e4m3, 16384 (16, 8192 keys) 31.5 against 33.0,
-// 32768 55.7 against 34.5.  Differential, 32 and 8 heads of 128, 16 bits, 1024
-// blocks (4 sequences, 2048 keys) 17.0 against 17.6, 2048 (4 and 4096) 19.7 against
-// 18.9, (8 and 2048) 20.3 against 17.9, 4096 (8 and 4096) 23.7 against 19.3; e4m3,
-// 4096 (16 and 2048) 27.0 against 28.1, 8192 (16 and 4096) 33.7 against 32.4, two
-// tiles (4 and 32768) 45.5 against 63.1; 16 and 2 heads of 64, 4096 (16 and 4096)
-// 18.3 against 18.8, 8192 (16 and 8192) 21.3 against 19.9, two tiles (2 and 32768)
-// 17.2 against 19.4.
+// against 30.5; 32 and 8 heads, e4m3, 8192 (16, 4096 keys) 22.7 against 22.2,
+// 16384 (16, 8192 keys) 31.2 against 26.1.  Differential, 32 and 8 heads of 128,
+// 16 bits, 1024 blocks (4 sequences, 2048 keys) 17.0 against 17.6, 2048 (4 and
+// 4096) 19.7 against 18.9, (8 and 2048) 20.3 against 17.9, 4096 (8 and 4096) 23.7
+// against 19.3; e4m3, 4096 (16 and 2048) 26.9 against 28.3, 8192 (16 and 4096) 33.7
+// against 32.6, two tiles (4 and 32768) 45.6 against 63.2; 16 and 2 heads of 64,
+// 4096 (16 and 4096) 18.3 against 18.8, 8192 (16 and 8192) 21.3 against 19.9, two
+// tiles (2 and 32768) 17.2 against 19.4.
 int64_t border(const santa::JoinArgs& a) {
-  if (a.phase == 1) return !a.diff ? (a.e4m3 ? 20480 : 12288) : a.e4m3 || a.D == 64 ? 5120 : 1920;
+  if (a.phase == 1) return !a.diff ? 12288 : a.e4m3 || a.D == 64 ? 5120 : 1920;
   return a.diff ? 9216 : 3 * 8192;
 }
 bool few_diff(const santa::JoinArgs& a, int64_t span) {
