@@ -220,7 +220,7 @@ class PagedStep:
     by the GPU when a call runs).  Attention then reads a group's prefix once, through its first sequence's row of the
     table; the new tokens stand behind it, and there is no window.  ``max_prefix`` bounds the prefixes, ``max_own`` the
     keys that a sequence has behind its own, ``max_group`` the sequences of a group: the closer, the better the work is
-    divided.  ``diff``: the step's heads are differential (``attend_diff``, whose workspace it then holds)."""
+    divided.  ``append``, ``read`` and ``sample`` look every key up in its own sequence's row.  ``diff``: the step's heads are differential (``attend_diff``, whose workspace it then holds)."""
 
     def __init__(self, cache: PagedCache, page_table, kv_lens=None, *, n_q_heads: int, dtype=None,
                  nk: Optional[int] = None, max_q: int = 1, total_q: Optional[int] = None, q_offsets=None,
