@@ -31,7 +31,7 @@ constexpr int W_BYTES = W_V + 3 * W_TILE, W_SMEM = W_BYTES + 1024;
 constexpr int W_THREADS = 384;
 
 enum { WQ_FULL, WK_FULL, WK_EMPTY = WK_FULL + 2, WV_FULL = WK_EMPTY + 2, WV_READY = WV_FULL + 3, WV_EMPTY = WV_READY + 3,
-       WS_FULL = WV_EMPTY + 3, WP_FULL = WS_FULL + 2, WM_READY = WP_FULL + 2, WO_STEP = WM_READY + 2, WO_DONE, WO_FREE, WPIECE_SEEN, W_BARS };
+       WS_FULL = WV_EMPTY + 3, WP_FULL = WS_FULL + 2, WM_READY = WP_FULL + 2, WO_STEP = WM_READY + 2, WO_DONE = WO_STEP + 2, WO_FREE, WPIECE_SEEN, W_BARS };
 
 // Stage and use of half h of V.
 struct VStage {
@@ -157,7 +157,7 @@ diff_wide_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
 #pragma unroll
             for (int i = 0; i < BKEYS / 16; ++i) mma_ts(tmO + 128, tmS + 128 * t + 8 * i, b1.at(i * 2048), shape_o, k > 0 || i != 0);
             mma_commit(bar(WV_EMPTY + v1.st));
-            mma_commit(bar(WO_STEP));
+            mma_commit(bar(WO_STEP + t));
             if (more) product_s(group);
             if (k + 1 == nblk) mma_commit(bar(WO_DONE));
           }
@@ -304,7 +304,7 @@ diff_wide_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     const int t = warp >> 2, row = tid & 127;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t mS = tmS + 128 * t + lanes, mO = tmO + lanes;
-    unsigned np = 0, jobs = 0, others = 0, n = 0;      // pieces, this group's and the other's jobs, blocks
+    unsigned np = 0, jobs = 0, others = 0;             // pieces, this group's and the other's jobs
     Piece& pc = s_piece[warp];
     if (lane == 0) s_walk[warp].start(a, sh);
     for (;;) {
@@ -367,10 +367,10 @@ diff_wide_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
           const float old = *(volatile float*)&s_m[row];
           mn = fmaxf(old, top);
           if (__any_sync(FULL, mn > old + RESCALE)) {
-            // the product of block j - 1; the next one waits for this group's P, the one before is over (S of this
-            // block was issued behind it), and is waited for as well lest its phase be taken for the next
-            if (j > 1) wait_phase(bar(WO_STEP), (n + j - 2) & 1, a.err, dead);
-            wait_phase(bar(WO_STEP), (n + j - 1) & 1, a.err, dead);
+            // The product of block j - 1, on the barrier of the other group's products, where no other phase can be
+            // taken for it: the one before, of block j - 3, is over (the other group's scores of block j - 1, whose
+            // maximum is here, were issued behind it), and the next, of block j + 1, waits for this group's P.
+            wait_phase(bar(WO_STEP + 1 - t), seen & 1, a.err, dead);
             tm_fence_after();
             const float f = fast_exp2(old - (mn > -INFINITY ? mn : 0.f));
 #pragma unroll 1
@@ -506,7 +506,6 @@ diff_wide_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       }
       if (nblk > 0) ++np;
       others += (unsigned)(t == 0 ? nblk >> 1 : (nblk + 1) >> 1);
-      n += nblk;
     }
     tm_fence_before();
   }

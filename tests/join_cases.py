@@ -1,0 +1,34 @@
+"""Calls of joined attention that are meant for one kernel: (what ``route`` takes, the kernels that it is to go to, the
+fewest blocks of 128 keys per piece of a chunk pass, on the whole).  The GPU tests run them, a host test checks the way
+that they take."""
+
+# differential chunks and prefix passes of many blocks per CTA
+LONG_PIECES = [
+    (dict(kv=[4000], n=[1200], H=8, Hkv=2, D=128, page=32, diff=True), ["own:{wide}"], 8),
+    (dict(kv=[2500, 3000, 700], n=[900, 1000, 700], H=14, Hkv=2, D=128, page=64, diff=True), ["own:{wide}"], 8),
+    (dict(kv=[30 + 3 * i for i in range(40)], n=[1] * 40, H=16, Hkv=4, D=128, page=128, diff=True, prefix=[40000], first=[0, 40]),
+     ["prefix:{wide}", "own:tokens"], 8),
+    (dict(kv=[3000], n=[1000], H=16, Hkv=4, D=64, page=16, diff=True), ["own:chunk"], 4),
+]
+
+
+def kernels(case, e4m3):
+    """The names, with {wide} the kernel for heads of 128 over 16 bits."""
+    return [x.format(wide="chunk" if e4m3 else "wide") for x in case[1]]
+
+
+def blocks_per_cta(case, e4m3, ctas=152):
+    """Blocks of a chunk pass (the first of the call) over its CTAs."""
+    c = case[0]
+    G, parts = c["H"] // c["Hkv"], 1
+    per = 128 // G * (1 if c["diff"] else 2)
+    items = c["Hkv"] // 2 if c["diff"] else c["Hkv"]
+    if c["diff"] and (e4m3 or c["D"] == 128):
+        parts = 2
+    if "prefix" in c:
+        total = sum(-(-p // 128) * -(-sum(c["n"][a:b]) // per) for p, a, b in zip(c["prefix"], c["first"], c["first"][1:]))
+    else:
+        total = 0
+        for kv, n in zip(c["kv"], c["n"]):
+            total += sum(-(-(kv - n + min(n, i + per)) // 128) for i in range(0, n, per))
+    return total * items * parts / ctas
