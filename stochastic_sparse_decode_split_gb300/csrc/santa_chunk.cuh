@@ -22,7 +22,8 @@
 //                   into the L2 beside it cost more than it gave (with
 //                   pages of 16, 1500 tokens of heads of 64 267 -> 214 us
 //                   without; of 64, 2048 tokens at 32768 keys 780 -> 761)
-//   warps 10, 11    16-bit caches: V rows past the last key become zeros, and
+//   warps 10, 11    16-bit caches: V rows past the last key (and, behind a prefix,
+//                   before the pass's first) become zeros, and
 //                   in blocks that not every row sees NaN and infinities, whose
 //                   product with a masked probability would not be zero, are
 //                   taken out and given back at the end to the rows that see them
@@ -472,9 +473,12 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         // heads: of K (differential: of tile 0; tile 1 has the next one), the first of V
         const int pair = p.kvh / PARTS, k_head = DIFF ? 2 * pair : p.kvh, v_head = DIFF ? 2 * pair + (PARTS == 2 ? p.kvh % 2 : 0) : p.kvh;
         const int32_t* const table = page_row(a, p.b);
-        auto page_of = [&](int j) {   // lane l: page of box l of block j (INT32_MIN: no key there)
+        // lane l: page of box l of block j (INT32_MIN: no key of this pass there; the row of a sequence behind a
+        // prefix need not name the pages that lie wholly inside it, some of which its first block may cover)
+        auto page_of = [&](int j) {
           const int key = (p.blk0 + j) * BKEYS + lane * rows;
-          return j < p.nblk && lane < boxes && key < p.s.kv ? max(table[key >> a.page_shift], -1) : INT32_MIN;
+          const bool there = key < p.s.kv && (!JOIN || key > p.s.from - rows);
+          return j < p.nblk && lane < boxes && there ? max(table[key >> a.page_shift], -1) : INT32_MIN;
         };
         auto row_of = [&](int pid, int j) {   // first row of a lane's box
           return (pid << a.page_shift) + (((p.blk0 + j) * BKEYS + lane * rows) & ((1 << a.page_shift) - 1));
@@ -564,7 +568,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       if (*dead)
         for (int i = 0; i < 1000; ++i) __nanosleep(1000);
     } else if (!E4M3 && warp < 12) {
-      // ------------------------------------- V: rows past the end, odd values
+      // -------------------- V: rows past the end or another pass's, odd values
       unsigned np = 0, n = 0;
       while (walk.next(a, sh, p)) {
         if (p.nblk == 0) continue;
@@ -572,14 +576,14 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         visible_keys(a, p.s, p.s.kv - p.s.n + p.i0, lo0, hi0);
         visible_keys(a, p.s, p.s.kv - p.s.n + p.i1, lo1, hi1);
         for (int j = 0; j < p.nblk; ++j, ++n) {
-          const int st = n & 1, key0 = (p.blk0 + j) * BKEYS, live = min(BKEYS, p.s.kv - key0);
+          const int st = n & 1, key0 = (p.blk0 + j) * BKEYS, live = min(BKEYS, p.s.kv - key0), first = JOIN ? p.s.from - key0 : 0;
           wait_phase(bar(V_FULL + st), (n >> 1) & 1, a.err, dead);
           if (key0 < lo1 || key0 + BKEYS > hi0) {
             const uint32_t vd = base + Gm::OFF_V + st * Gm::VTILE;
             bool found = false;
             for (int i = tid - 320; i < Gm::VTILE / 16; i += 64) {
               const int r = (i >> 3) & (TROWS - 1);   // chunk i of the tile lies in row r of its half
-              if (r >= live) {
+              if (r >= live || r < first) {
                 sts128(vd + i * 16, make_uint4(0u, 0u, 0u, 0u));
               } else {
                 uint4 v = lds128(vd + i * 16);
@@ -613,11 +617,11 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
           const bool is_v = AHEAD ? (i > 0 && i % 2 == 0) || i + 1 == STEPS * p.nblk : i % STEPS == STEPS - 1;
           const int which = AHEAD ? is_v : i % STEPS, j = AHEAD ? (is_v ? i - 1 : i + 1) / 2 : i / STEPS;
           const unsigned at = n + j;
-          const int st = at & 1, key0 = (p.blk0 + j) * BKEYS, live = min(BKEYS, p.s.kv - key0);
+          const int st = at & 1, key0 = (p.blk0 + j) * BKEYS, live = min(BKEYS, p.s.kv - key0), first = JOIN ? p.s.from - key0 : 0;
           if (which == 0) {   // this thread's key's scales, on their way while the codes arrive
             const int key = key0 + ct;
             float ksc = 0.f, ksc1 = 0.f, vsc = 1.f;
-            if (ct < live) {
+            if (ct < live && ct >= first) {
               const int pid = table[key >> a.page_shift];
               if ((unsigned)pid < (unsigned)a.n_pages) {
                 auto scale_at = [&](int head) { return ((((long long)pid * a.Hkv) + head) << a.page_shift) + (key & ((1 << a.page_shift) - 1)); };
@@ -657,10 +661,10 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
             for (int q = 0; q < 4; ++q) w[q] = lds128(src + (ct + 128 * (q0 + q)) * 16);
             if (PASS == 4) group_sync(1, 128);
             else __syncwarp();
-            if (live < BKEYS) {   // past the last key: whatever was there before
+            if (live < BKEYS || first > 0) {   // no key of this pass: whatever was there before
 #pragma unroll
               for (int q = 0; q < 4; ++q)
-                if (r0 + (q0 + q) * (128 / CPR) >= live) w[q] = make_uint4(0u, 0u, 0u, 0u);
+                if (r0 + (q0 + q) * (128 / CPR) >= live || r0 + (q0 + q) * (128 / CPR) < first) w[q] = make_uint4(0u, 0u, 0u, 0u);
             }
             uint32_t nan = 0;     // bit 7 of a byte: some code there is a NaN
 #pragma unroll
@@ -1084,7 +1088,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
             for (int key0 = blk0 * BKEYS; key0 < end; key0 += 32) {
               const int block = key0 & -BKEYS, key = key0 + lane;
               if (!E4M3 && block >= clean_lo && block + BKEYS <= clean_hi) continue;
-              const int pid = key < end ? table[key >> a.page_shift] : -1;
+              const int pid = key < end && (!JOIN || key >= pc.s.from) ? table[key >> a.page_shift] : -1;
               const int in_page = key & ((1 << a.page_shift) - 1);
               long long at_v = 0;
               uint32_t found = 0;   // e4m3: the odd columns; else whether there are any

@@ -186,9 +186,9 @@ diff_wide_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         if (p.nblk == 0) continue;
         const int pair = p.kvh >> 1, map = p.kvh & 1;
         const int32_t* const table = page_row(a, p.b);
-        auto page_of = [&](int j) {   // lane l: page of box l of block j (INT32_MIN: no key there)
+        auto page_of = [&](int j) {   // lane l: page of box l of block j (INT32_MIN: no key of this pass there)
           const int key = (p.blk0 + j) * BKEYS + lane * rows;
-          return j < p.nblk && lane < boxes && key < p.s.kv ? max(table[key >> a.page_shift], -1) : INT32_MIN;
+          return j < p.nblk && lane < boxes && key < p.s.kv && key > p.s.from - rows ? max(table[key >> a.page_shift], -1) : INT32_MIN;
         };
         int pid = page_of(0), pid1 = page_of(1);
         for (int j = 0; j < p.nblk; ++j, ++n) {
@@ -258,7 +258,7 @@ diff_wide_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       if (*dead)
         for (int i = 0; i < 1000; ++i) __nanosleep(1000);
     } else {
-      // ------------------------------------- V: rows past the end, odd values
+      // -------------------- V: rows past the end or another pass's, odd values
       unsigned np = 0, n = 0;
       while (walk.next(a, sh, p)) {
         if (p.nblk == 0) continue;
@@ -266,7 +266,7 @@ diff_wide_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         visible_keys(a, p.s, p.s.kv - p.s.n + p.i0, lo0, hi0);
         visible_keys(a, p.s, p.s.kv - p.s.n + p.i1, lo1, hi1);
         for (int j = 0; j < p.nblk; ++j, ++n) {
-          const int key0 = (p.blk0 + j) * BKEYS, live = min(BKEYS, p.s.kv - key0);
+          const int key0 = (p.blk0 + j) * BKEYS, live = min(BKEYS, p.s.kv - key0), first = p.s.from - key0;
           const bool partial = key0 < lo1 || key0 + BKEYS > hi0;
 #pragma unroll 1
           for (int f = 0; f < 2; ++f) {
@@ -277,7 +277,7 @@ diff_wide_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
               bool found = false;
               for (int i = tid - 320; i < W_TILE / 16; i += 64) {
                 const int r = (i >> 3) & (TROWS - 1);   // chunk i of the tile lies in row r of its half
-                if (r >= live) {
+                if (r >= live || r < first) {
                   sts128(vd + i * 16, make_uint4(0u, 0u, 0u, 0u));
                 } else {
                   uint4 y = lds128(vd + i * 16);
@@ -481,7 +481,7 @@ diff_wide_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         for (int key0 = blk0 * BKEYS; key0 < end; key0 += 32) {
           const int block = key0 & -BKEYS, key = key0 + lane;
           if (block >= clean_lo && block + BKEYS <= clean_hi) continue;
-          const int pid = key < end ? table[key >> a.page_shift] : -1;
+          const int pid = key < end && key >= pc.s.from ? table[key >> a.page_shift] : -1;
           long long at_v = 0;
           bool found = false;
           if ((unsigned)pid < (unsigned)a.n_pages) {

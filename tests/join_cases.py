@@ -1,6 +1,6 @@
-"""Calls of joined attention that are meant for one kernel: (what ``route`` takes, the kernels that it is to go to, the
-fewest blocks of 128 keys per piece of a chunk pass, on the whole).  The GPU tests run them, a host test checks the way
-that they take."""
+"""Calls of joined attention that are meant for one kernel: (what ``route`` takes, the kernels that it is to go to[, the
+fewest blocks of 128 keys that a CTA has on the whole]).  The GPU tests run them, a host test checks the way that they
+take."""
 
 # differential chunks and prefix passes of many blocks per CTA
 LONG_PIECES = [
@@ -11,6 +11,25 @@ LONG_PIECES = [
     (dict(kv=[3000], n=[1000], H=16, Hkv=4, D=64, page=16, diff=True), ["own:chunk"], 4),
 ]
 
+# chunks behind prefixes, whose first block of 128 keys begins before pages that lie wholly inside the prefix
+OWN_CHUNKS = [
+    (dict(kv=[400, 310, 333], n=[300, 310, 200], H=32, Hkv=8, D=128, page=16, prefix=[192], first=[0, 3]), ["prefix:chunk", "own:chunk"]),
+    (dict(kv=[500, 420, 600, 380], n=[400, 300, 450, 200], H=16, Hkv=8, D=64, page=32, prefix=[250, 1000], first=[0, 2, 4]),
+     ["prefix:chunk", "own:chunk"]),
+    (dict(kv=[700, 450, 651], n=[500, 450, 300], H=28, Hkv=4, D=128, page=64, prefix=[1000], first=[0, 3]), ["prefix:chunk", "own:chunk"]),
+    (dict(kv=[390, 2, 300, 640], n=[380, 1, 290, 333], H=32, Hkv=16, D=64, page=16, prefix=[0, 127], first=[0, 1, 4]),
+     ["prefix:chunk", "own:chunk"]),
+    (dict(kv=[400, 310, 333], n=[300, 310, 200], H=8, Hkv=2, D=128, page=16, prefix=[1216], first=[0, 3], diff=True),
+     ["prefix:{wide}", "own:{wide}"]),
+    (dict(kv=[500, 420, 600, 380], n=[400, 300, 450, 200], H=8, Hkv=4, D=64, page=32, prefix=[250, 1000], first=[0, 2, 4], diff=True),
+     ["prefix:chunk", "own:chunk"]),
+    (dict(kv=[700, 450, 651], n=[500, 450, 300], H=14, Hkv=2, D=128, page=64, prefix=[1000], first=[0, 3], diff=True),
+     ["prefix:{wide}", "own:{wide}"]),
+    (dict(kv=[400, 310, 333], n=[300, 310, 200], H=32, Hkv=8, D=128, page=16, prefix=[20], first=[0, 3]), ["prefix:tokens", "own:chunk"]),
+    (dict(kv=[400, 310, 333], n=[300, 310, 200], H=8, Hkv=2, D=128, page=16, prefix=[20], first=[0, 3], diff=True),
+     ["prefix:tokens", "own:{wide}"]),
+]
+
 
 def kernels(case, e4m3):
     """The names, with {wide} the kernel for heads of 128 over 16 bits."""
@@ -18,12 +37,11 @@ def kernels(case, e4m3):
 
 
 def blocks_per_cta(case, e4m3, ctas=152):
-    """Blocks of a chunk pass (the first of the call) over its CTAs."""
+    """Blocks of a differential call's chunk pass (its first) over its CTAs."""
     c = case[0]
     G, parts = c["H"] // c["Hkv"], 1
-    per = 128 // G * (1 if c["diff"] else 2)
-    items = c["Hkv"] // 2 if c["diff"] else c["Hkv"]
-    if c["diff"] and (e4m3 or c["D"] == 128):
+    per, items = 128 // G, c["Hkv"] // 2
+    if e4m3 or c["D"] == 128:
         parts = 2
     if "prefix" in c:
         total = sum(-(-p // 128) * -(-sum(c["n"][a:b]) // per) for p, a, b in zip(c["prefix"], c["first"], c["first"][1:]))

@@ -18,6 +18,10 @@ def test_calls_of_long_pieces():
     check(join_cases.LONG_PIECES)
 
 
+def test_calls_of_chunks_behind_prefixes():
+    check(join_cases.OWN_CHUNKS)
+
+
 @pytest.mark.parametrize("n,kernel", [(16, "tokens"), (1200, "chunk")])
 def test_the_plain_attention_has_its_own(n, kernel):
     assert route([4000], [n], 8, 2, 128) == [kernel]
