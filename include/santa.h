@@ -371,7 +371,8 @@ santa_status_t santa_paged_attention(const santa_paged_t* p, const void* q, cons
  *
  * SANTA_CACHE_DEVERR_PREFIX: a group with bad offsets, more new tokens than
  * max_group * max_q, or prefix_lens[g] outside [0, max_prefix]; a sequence in no
- * group, whose new tokens begin inside the prefix (not causal: of fewer keys), or
+ * group, whose tokens are not among its group's (q_offsets that decrease further
+ * on), whose new tokens begin inside the prefix (not causal: of fewer keys), or
  * with more than max_own keys behind it.  The attention rows of the sequences
  * that it concerns come out zero. */
 typedef struct {

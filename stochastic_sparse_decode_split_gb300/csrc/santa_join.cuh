@@ -81,6 +81,8 @@ SANTA_HD int group_of(const JoinArgs& a, int b) {
 }
 
 // In phase 2 a sequence is refused whose group is, that no group holds, whose
+// tokens are not among the group's (whose range two offsets give, those between
+// them may be anything; the join finds a token's sums by its place there), whose
 // new tokens begin inside the prefix, or with more keys of its own than stated.
 SANTA_HD Seq paged_seq(const JoinArgs& a, int b, bool flag) {
   bool fine = true;
@@ -97,6 +99,7 @@ SANTA_HD Seq paged_seq(const JoinArgs& a, int b, bool flag) {
     if (a.phase == 2) {
       const Group g = group_at(a, group_of(a, b));
       fine = g.ok && g.first <= b && b < g.last;
+      if (s.ok) fine = fine && s.q0 >= g.q0 && s.q0 + s.n <= g.q0 + g.n;
       if (s.ok) fine = fine && g.prefix <= (a.causal ? max(s.kv - s.n, 0) : s.kv) && s.kv - g.prefix <= a.max_own;
       s.from = fine ? g.prefix : 0;
       if (!fine) s.kv = 0;
