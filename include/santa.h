@@ -369,7 +369,8 @@ santa_status_t santa_paged_attention(const santa_paged_t* p, const void* q, cons
  * anywhere in a page, whose further keys each sequence then has in a page of
  * its own table row.  A prefix of 0 shares nothing.
  *
- * SANTA_CACHE_DEVERR_PREFIX: a group with bad offsets, more new tokens than
+ * SANTA_CACHE_DEVERR_PREFIX: a group with bad offsets (or, where they decrease,
+ * one that has a sequence in common with another), more new tokens than
  * max_group * max_q, or prefix_lens[g] outside [0, max_prefix]; a sequence in no
  * group, whose tokens are not among its group's (q_offsets that decrease further
  * on), whose new tokens begin inside the prefix (not causal: of fewer keys), or

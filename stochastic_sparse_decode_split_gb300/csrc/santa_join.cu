@@ -115,6 +115,21 @@ __device__ __forceinline__ int last_at_most(const int64_t* v, int n, long long t
   }
 }
 
+// Whether another group holds a sequence of group g as well, which offsets that
+// decrease somewhere can bring about: both then have left sums, and notes, at the
+// same rows.  The same in every lane.
+__device__ __forceinline__ bool overlapped(const JoinArgs& a, int g, int lane) {
+  if (a.n_groups == 1) return false;
+  const int first = a.group_offsets[g], last = a.group_offsets[g + 1];
+  bool hit = false;
+#pragma unroll 4
+  for (int k = lane; k < a.n_groups; k += 32) {
+    const int lo = a.group_offsets[k], hi = a.group_offsets[k + 1];
+    hit |= k != g && lo < hi && lo < last && hi > first;
+  }
+  return __any_sync(FULL, hit);
+}
+
 // WARPS warps of a CTA share the pieces of a set, or (WARPS = 1) each of its
 // four warps has sets of its own.  A CTA has `sets` sets of a token, whose
 // look-ups are made once for them: one round for the sequence (32 offsets at a
@@ -141,7 +156,7 @@ __global__ void __launch_bounds__(join_threads<WARPS>(), WARPS == 16 ? 1 : WARPS
     b = (int)(t / (unsigned)a.max_q);
     if (b >= a.B) return wait_for_predecessor();
   }
-  const Seq s = paged_seq(a, b, false);
+  Seq s = paged_seq(a, b, false);
   const int i = (int)(t - s.q0);
   if (i >= s.n) return wait_for_predecessor();
   Seq sp = {};
@@ -149,6 +164,7 @@ __global__ void __launch_bounds__(join_threads<WARPS>(), WARPS == 16 ? 1 : WARPS
   if (p.n_groups) {
     g = group_of(a, b);
     sp = paged_seq(p, g, false);
+    if (overlapped(p, g, lane)) s.ok = false;
   }
   const bool prefix = s.ok && sp.kv > 0;
   const int ip = prefix ? (int)(t - sp.q0) : 0;

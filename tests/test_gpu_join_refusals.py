@@ -49,3 +49,22 @@ def test_tokens_that_are_not_among_their_groups(n, prefix, e4m3, diff):
     assert gone(out[95 * k:96 * k], lse[95 * k:96 * k])
     torch.testing.assert_close(out[:k].float(), want[:k].float(), rtol=2.0 ** -6, atol=2.0 ** -6)
     torch.testing.assert_close(lse[:k], want_lse[:k], rtol=2.0 ** -16, atol=2.0 ** -10)
+
+
+@pytest.mark.parametrize("diff", [False, True])
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("n,prefix", SHAPES)
+def test_groups_that_overlap(n, prefix, e4m3, diff):
+    """Offsets that decrease: two groups have the third sequence, and neither's rows are to be had; the last is apart."""
+    k, P = n[0], prefix[0]
+    batch = Shared([P] * 4, [0, 2, 2, 4, 6], [k + 5 + 3 * b for b in range(6)], [k] * 6, 16, 4, 128, BF16, e4m3, 16, seed=k,
+                   pairs=diff, whole=True)
+    step = batch.shared_step(diff=diff, max_group=3)
+    want, want_lse = attend(step, batch, diff)
+    assert step.error() == 0
+    batch.first_t.copy_(torch.tensor([0, 3, 2, 4, 6], dtype=torch.int32))
+    out, lse = attend(step, batch, diff)
+    assert step.error() == santa.CACHE_DEVERR_PREFIX
+    assert gone(out[:4 * k], lse[:4 * k])
+    torch.testing.assert_close(out[4 * k:].float(), want[4 * k:].float(), rtol=2.0 ** -6, atol=2.0 ** -6)
+    torch.testing.assert_close(lse[4 * k:], want_lse[4 * k:], rtol=2.0 ** -16, atol=2.0 ** -10)
