@@ -133,7 +133,7 @@ SANTA_HD bool item_split(const JoinArgs&, long long T, int P, long long items, i
 // second piece costs 8 us.  32 differential tokens behind 16384 keys, 8 items:
 // 43.8 us with 96 CTAs, 49.0 with 95.
 SANTA_HD int share_ctas(const JoinArgs&, long long T, int P, long long items, int most) {
-  return items <= P && items * most == T ? P / (int)items * (int)items : P;
+  return items > 0 && items <= P && items * most == T ? P / (int)items * (int)items : P;   // 0: every group is refused or empty
 }
 // A group's prefix is looked up in the table's row of its first sequence.
 SANTA_HD const int32_t* page_row(const JoinArgs& a, int b) {
