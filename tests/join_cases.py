@@ -30,6 +30,29 @@ OWN_CHUNKS = [
      ["prefix:tokens", "own:{wide}"]),
 ]
 
+# every form of the chunk kernels, for what goes beyond lengths: odd values, bad pages, padding, replays
+FORMS = [
+    OWN_CHUNKS[1], OWN_CHUNKS[2], OWN_CHUNKS[5], OWN_CHUNKS[6],
+    (dict(kv=[2000, 1500], n=[700, 400], H=8, Hkv=2, D=128, page=32, diff=True), ["own:{wide}"]),
+    (dict(kv=[2000, 1500], n=[700, 400], H=8, Hkv=2, D=64, page=16, diff=True), ["own:chunk"]),
+]
+
+# differential chunks in a window, unmasked, and with rows that see nothing
+WINDOWS = [(dict(kv=[2500, 900], n=[700, 300], H=8, Hkv=2, D=D, page=page, diff=True, window=w), ["own:{wide}" if D == 128 else "own:chunk"])
+           for D, page in ((128, 32), (64, 16)) for w in (1, 16, 100, 128, 1000)]
+UNMASKED = [
+    (dict(kv=[1500, 5, 700], n=[448, 300, 200], H=16, Hkv=4, D=128, page=64, diff=True, causal=False), ["own:{wide}"]),
+    (dict(kv=[1500, 5, 700], n=[448, 300, 200], H=16, Hkv=4, D=64, page=16, diff=True, causal=False), ["own:chunk"]),
+    (dict(kv=[300, 5, 420], n=[448, 600, 200], H=16, Hkv=8, D=128, page=16, prefix=[250], first=[0, 3], causal=False), ["prefix:chunk", "own:chunk"]),
+    (dict(kv=[300, 5, 420], n=[448, 600, 200], H=16, Hkv=4, D=64, page=32, prefix=[250], first=[0, 3], causal=False, diff=True),
+     ["prefix:chunk", "own:chunk"]),
+    (dict(kv=[300, 5, 420], n=[448, 600, 200], H=16, Hkv=4, D=128, page=16, prefix=[1400], first=[0, 3], causal=False, diff=True),
+     ["prefix:{wide}", "own:{wide}"]),
+]
+NOTHING_SEEN = [
+    (dict(kv=[0, 40, 698, 600], n=[700, 700, 700, 1], H=8, Hkv=2, D=D, page=page, diff=True), ["own:{wide}" if D == 128 else "own:chunk"])
+    for D, page in ((128, 32), (64, 16))]
+
 
 def kernels(case, e4m3):
     """The names, with {wide} the kernel for heads of 128 over 16 bits."""

@@ -22,6 +22,10 @@ def test_calls_of_chunks_behind_prefixes():
     check(join_cases.OWN_CHUNKS)
 
 
+def test_calls_of_every_form_of_the_chunk_kernels():
+    check(join_cases.FORMS + join_cases.WINDOWS + join_cases.UNMASKED + join_cases.NOTHING_SEEN)
+
+
 @pytest.mark.parametrize("n,kernel", [(16, "tokens"), (1200, "chunk")])
 def test_the_plain_attention_has_its_own(n, kernel):
     assert route([4000], [n], 8, 2, 128) == [kernel]
