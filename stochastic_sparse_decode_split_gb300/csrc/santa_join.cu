@@ -117,9 +117,9 @@ __device__ __forceinline__ int last_at_most(const int64_t* v, int n, long long t
 
 // Whether another group holds a sequence of group g as well, which offsets that
 // decrease somewhere can bring about: both then have left sums, and notes, at the
-// same rows.  The same in every lane.
-__device__ __forceinline__ bool overlapped(const JoinArgs& a, int g, int lane) {
-  if (a.n_groups == 1) return false;
+// same rows.  The same in every lane.  A call, which one group does without: inlined
+// it costs the join's loops registers.
+__device__ __noinline__ bool overlapped(const JoinArgs& a, int g, int lane) {
   const int first = a.group_offsets[g], last = a.group_offsets[g + 1];
   bool hit = false;
 #pragma unroll 4
@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(join_threads<WARPS>(), WARPS == 16 ? 1 : WARPS
   if (p.n_groups) {
     g = group_of(a, b);
     sp = paged_seq(p, g, false);
-    if (overlapped(p, g, lane)) s.ok = false;
+    if (p.n_groups > 1 && overlapped(p, g, lane)) s.ok = false;
   }
   const bool prefix = s.ok && sp.kv > 0;
   const int ip = prefix ? (int)(t - sp.q0) : 0;
