@@ -99,8 +99,7 @@ SANTA_HD Seq paged_seq(const JoinArgs& a, int b, bool flag) {
     if (a.phase == 2) {
       const Group g = group_at(a, group_of(a, b));
       fine = g.ok && g.first <= b && b < g.last;
-      if (s.ok) fine = fine && s.q0 >= g.q0 && s.q0 + s.n <= g.q0 + g.n;
-      if (s.ok) fine = fine && g.prefix <= (a.causal ? max(s.kv - s.n, 0) : s.kv) && s.kv - g.prefix <= a.max_own;
+      if (s.ok) fine = fine && s.n <= g.n && (unsigned)((int)s.q0 - (int)g.q0) <= (unsigned)(g.n - s.n) && g.prefix <= (a.causal ? max(s.kv - s.n, 0) : s.kv) && s.kv - g.prefix <= a.max_own;
       s.from = fine ? g.prefix : 0;
       if (!fine) s.kv = 0;
       s.ok = s.ok && fine;
