@@ -390,8 +390,9 @@ typedef struct {
 size_t santa_shared_workspace_size(const santa_paged_t* p, const santa_prefix_t* x);
 
 /* santa_paged_attention for a batch whose sequences share prefixes: the same
- * result, with a group's prefix read once.  No window (SANTA_ERR_UNSUPPORTED):
- * what a group sees of its prefix would differ from token to token. */
+ * result, with a group's prefix read once, and the same roundings: probabilities
+ * enter the second product in 16 bits.  No window (SANTA_ERR_UNSUPPORTED): what a
+ * group sees of its prefix would differ from token to token. */
 santa_status_t santa_shared_attention(const santa_paged_t* p, const santa_prefix_t* x, const void* q, const void* K, const void* V,
                                       const float* k_scale, const float* v_scale, void* out, float* lse, void* workspace,
                                       size_t ws_bytes, santa_stream_t stream);
@@ -417,7 +418,12 @@ size_t santa_diff_workspace_size(const santa_paged_t* p, const santa_prefix_t* x
  *   out  [total_q, n_q_heads / 2, 2 * head_dim] in dtype; may be q itself
  *   lse  optional float32 [total_q, n_q_heads], as santa_paged_attention's
  * Layouts, masks, empty rows (zeros), and x (or NULL) as above; n_kv_heads is
- * even.  The difference and the norm are taken of float32 sums. */
+ * even.  The difference and the norm are taken of float32 sums; of both maps the
+ * probabilities enter the product with the values as santa_paged_attention's do,
+ * in 16 bits, and where the maps are much alike the difference is smaller than
+ * they are and that rounding a larger share of it (chunks over a bf16 cache:
+ * 0.0025 of the result, of which its own rounding is 0.0017; calls of few rows
+ * over 16 bits keep the rounding's rest in a second product). */
 santa_status_t santa_diff_attention(const santa_paged_t* p, const santa_prefix_t* x, const santa_diff_t* d, const void* q,
                                     const void* K, const void* V, const float* k_scale, const float* v_scale, void* out, float* lse,
                                     void* workspace, size_t ws_bytes, santa_stream_t stream);

@@ -206,10 +206,13 @@ void plan_pass(santa::JoinArgs& a, int64_t span, bool inside) {
 // division is the best of a few by an estimate of both: a block of 256 rows and
 // 128 keys is 1.9 us of an SM (e4m3 3.4, differential 2.5; 128 rows of a
 // differential map with both value heads 1.2; heads of 64 0.7 of that, one tile of
-// rows half, e4m3 three quarters), and 15 us are start and end; the other pass's
+// rows half, e4m3 three quarters; from prefixes of 65536 and 131072 keys heads of
+// 64 come to 0.77 over 16 bits and of differential e4m3 blocks, to 0.98 of 256
+// e4m3 rows), and 15 us are start and end; the other pass's
 // CTAs take 4 us and their keys (half of what may be) at 45 GB/s per SM; what it
 // has not done when the first is over it does on all SMs.  Several prefixes count
-// as 0.75 of their bound each, and the first pass keeps at least 9 sixteenths.
+// as 0.75 of their bound each (between half of it and all: of their lengths the
+// host knows the bound alone), and the first pass keeps at least 9 sixteenths.
 // Measured, 64 sequences of 100 to 2000 keys behind 32768, 32 and 8 heads of 128:
 // 118 us on all SMs one after the other, 99 with 120, 91 with 90, 92 with 76, 100
 // with 60; e4m3 108 on all, 98 with 112, 86 with 96, 92 with 80; 16 behind 8192, 28

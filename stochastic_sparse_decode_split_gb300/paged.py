@@ -153,7 +153,8 @@ def rope_table(positions: int, rotated: int, base: float = 10000.0, *, linear: f
 
 def diff_weights(q1, k1, q2, k2, init: float) -> torch.Tensor:
     """The weights of differential heads from their learned vectors, float32: exp(q1 . k1) - exp(q2 . k2) + init over the
-    last dimension, [H / 2, d] to the [H / 2] that ``PagedStep.attend_diff`` takes."""
+    last dimension, [H / 2, d] to the [H / 2] that ``PagedStep.attend_diff`` takes.  (One weight for all heads, from
+    vectors [d], becomes that by ``.expand(H // 2).contiguous()``, once per layer.)"""
     q1, k1, q2, k2 = (x.float() for x in (q1, k1, q2, k2))
     return (q1 * k1).sum(-1).exp() - (q2 * k2).sum(-1).exp() + init
 
@@ -220,7 +221,8 @@ class PagedStep:
     by the GPU when a call runs).  Attention then reads a group's prefix once, through its first sequence's row of the
     table; the new tokens stand behind it, and there is no window.  ``max_prefix`` bounds the prefixes, ``max_own`` the
     keys that a sequence has behind its own, ``max_group`` the sequences of a group: the closer, the better the work is
-    divided.  ``append``, ``read`` and ``sample`` look every key up in its own sequence's row.  ``diff``: the step's heads are differential (``attend_diff``, whose workspace it then holds)."""
+    divided.  ``append``, ``read`` and ``sample`` look every key up in its own sequence's row.  ``diff``: the
+    step's heads are differential (``attend_diff``, whose workspace it then holds)."""
 
     def __init__(self, cache: PagedCache, page_table, kv_lens=None, *, n_q_heads: int, dtype=None,
                  nk: Optional[int] = None, max_q: int = 1, total_q: Optional[int] = None, q_offsets=None,
